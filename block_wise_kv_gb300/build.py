@@ -20,7 +20,8 @@ LIBDIR = os.path.join(HERE, "_lib")
 OBJDIR = os.path.join(LIBDIR, "obj")
 LIBPATH = os.path.join(LIBDIR, "libdllm.so")
 
-SOURCES = ["dllm_api.cu", "qkv_gemm.cu", "qkv_wide.cu", "attn_rows.cu", "attn_stream.cu", "misc.cu", "noalloc.cu", "lm_head.cu", "ffn.cu"]
+SOURCES = ["dllm_api.cu", "qkv_gemm.cu", "qkv_wide.cu", "attn_rows.cu", "attn_stream.cu", "misc.cu", "noalloc.cu",
+           "lm_head.cu", "ffn.cu", "batch_plan.cu", "kv8_write.cu", "kv8_attn.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-I", INCLUDE, "-I",
          CSRC]

@@ -6,6 +6,7 @@
 
 #include "dllm.h"
 #include "kernels.cuh"
+#include "kv8.cuh"
 
 using namespace dllm;
 
@@ -506,6 +507,173 @@ dllm_status dllm_block_ffn(const dllm_layer_desc* desc, const dllm_batch* batch,
   w.down_scale = w_down_scale;
   DLLM_CUDA_TRY(launch_ffn(a, w, ws, device_sms(), static_cast<cudaStream_t>(stream)));
   return DLLM_OK;
+}
+
+namespace {
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+dllm_status check_kv8(const dllm_kv8_cache* c, const dllm_layer_desc* d) {
+  if (c == nullptr || c->num_pages < 1 || c->n_kv_heads < 1) return DLLM_ERR_INVALID_ARGUMENT;
+  if (d->n_heads % c->n_kv_heads != 0) return DLLM_ERR_INVALID_ARGUMENT;
+  if (static_cast<int64_t>(c->num_pages) * c->n_kv_heads * kPage > kMaxRows) return DLLM_ERR_UNSUPPORTED;
+  if (!aligned(c->k_pool, 16) || !aligned(c->v_pool, 16) || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
+    return DLLM_ERR_INVALID_ARGUMENT;
+  return DLLM_OK;
+}
+
+Kv8Pools kv8_pools(const dllm_kv8_cache* c) {
+  Kv8Pools p;
+  p.k = static_cast<uint8_t*>(c->k_pool);
+  p.v = static_cast<uint8_t*>(c->v_pool);
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  p.n_kv_heads = c->n_kv_heads;
+  return p;
+}
+
+BatchArgs kv8_batch(const dllm_batch* b, int32_t num_pages) {
+  dllm_cache pages = {};
+  pages.num_pages = num_pages;
+  return batch_args(b, &pages);
+}
+
+bool rows_ok(const void* p, int64_t row, int64_t head) {
+  return aligned(p, 16) && row >= 0 && head >= 0 && row % 8 == 0 && head % 8 == 0;
+}
+}  // namespace
+
+dllm_status dllm_batch_plan(const dllm_batch* batch, const int32_t* pages_held, int32_t* pages_held_out,
+                            int32_t* block_table, int32_t* cu_block, int32_t* cu_seq, const dllm_page_ring* ring,
+                            int32_t* row_slot, int32_t* row_seq, int32_t* row_pos, void* stream) {
+  if (batch == nullptr || ring == nullptr || batch->batch < 0) return DLLM_ERR_INVALID_ARGUMENT;
+  if (batch->batch > 65535) return DLLM_ERR_UNSUPPORTED;
+  if (!aligned(cu_block, 4) || !aligned(cu_seq, 4) || !aligned(ring->pages, 4) || !aligned(ring->state, 4) ||
+      !aligned(ring->state_out, 4) || ring->num_pages < 1)
+    return DLLM_ERR_INVALID_ARGUMENT;
+  if (ring->num_pages > kMaxRows / kPage) return DLLM_ERR_UNSUPPORTED;  // slots are int32
+  if (overlap(ring->state, 8, ring->state_out, 8)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (batch->error_flag != nullptr && !aligned(batch->error_flag, 4)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (batch->total_block_rows < 0 || batch->total_seq_rows < 0) return DLLM_ERR_INVALID_ARGUMENT;
+  for (const int32_t* p : {row_slot, row_seq, row_pos})
+    if (p != nullptr && !aligned(p, 16)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (batch->batch > 0) {
+    if (!aligned(batch->seq_len, 4) || !aligned(batch->block_start, 4) || !aligned(batch->block_len, 4) ||
+        !aligned(pages_held, 4) || !aligned(pages_held_out, 4) || !aligned(block_table, 4))
+      return DLLM_ERR_INVALID_ARGUMENT;
+    const size_t n = static_cast<size_t>(batch->batch) * 4;
+    if (overlap(pages_held, n, pages_held_out, n)) return DLLM_ERR_INVALID_ARGUMENT;
+    if (batch->max_pages_per_seq < 1 || batch->max_seq_len < 1) return DLLM_ERR_INVALID_ARGUMENT;
+    if (static_cast<int64_t>(batch->max_pages_per_seq) * kPage < batch->max_seq_len) return DLLM_ERR_INVALID_ARGUMENT;
+    if (batch->max_seq_len > 65535 * kPage) return DLLM_ERR_UNSUPPORTED;
+  }
+  PlanArgs a;
+  a.seq_len = batch->seq_len;
+  a.block_start = batch->block_start;
+  a.block_len = batch->block_len;
+  a.held = pages_held;
+  a.held_out = pages_held_out;
+  a.table = block_table;
+  a.cu_block = cu_block;
+  a.cu_seq = cu_seq;
+  a.ring = ring->pages;
+  a.state = ring->state;
+  a.state_out = ring->state_out;
+  a.row_slot = row_slot;
+  a.row_seq = row_seq;
+  a.row_pos = row_pos;
+  a.err = batch->error_flag;
+  a.batch = batch->batch;
+  a.max_pages = batch->max_pages_per_seq;
+  a.num_pages = ring->num_pages;
+  a.max_seq_len = batch->max_seq_len;
+  a.cap_rows = batch->total_block_rows;
+  a.cap_seq = batch->total_seq_rows;
+  return cuda_status(launch_batch_plan(a, device_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+dllm_status dllm_kv8_write(const dllm_layer_desc* desc, const dllm_batch* batch, const void* k_rows,
+                           int64_t k_row_stride, int64_t k_head_stride, const void* v_rows, int64_t v_row_stride,
+                           int64_t v_head_stride, const dllm_kv8_cache* kv8, void* stream) {
+  DLLM_TRY(check_desc(desc));
+  DLLM_TRY(check_batch(batch));
+  if (batch->batch == 0 || batch->total_block_rows == 0) return DLLM_OK;
+  DLLM_TRY(check_kv8(kv8, desc));
+  if (!rows_ok(k_rows, k_row_stride, k_head_stride) || !rows_ok(v_rows, v_row_stride, v_head_stride))
+    return DLLM_ERR_INVALID_ARGUMENT;
+  Kv8WriteArgs a = {};
+  a.bt = kv8_batch(batch, kv8->num_pages);
+  a.kv = kv8_pools(kv8);
+  a.k_src = k_rows;
+  a.v_src = v_rows;
+  a.k_row = k_row_stride;
+  a.k_head = k_head_stride;
+  a.v_row = v_row_stride;
+  a.v_head = v_head_stride;
+  a.head_dim = desc->head_dim;
+  return cuda_status(launch_kv8_write(a, device_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+dllm_status dllm_kv8_write_pool(const dllm_layer_desc* desc, const dllm_batch* batch, const dllm_cache* cache,
+                                const dllm_kv8_cache* kv8, void* stream) {
+  DLLM_TRY(check_desc(desc));
+  DLLM_TRY(check_batch(batch));
+  if (batch->batch == 0 || batch->total_block_rows == 0) return DLLM_OK;
+  DLLM_TRY(check_cache(cache, desc, false, false));
+  DLLM_TRY(check_kv8(kv8, desc));
+  if (kv8->n_kv_heads != desc->n_heads) return DLLM_ERR_INVALID_ARGUMENT;
+  Kv8WriteArgs a = {};
+  a.bt = kv8_batch(batch, cache->num_pages < kv8->num_pages ? cache->num_pages : kv8->num_pages);
+  a.kv = kv8_pools(kv8);
+  a.k_src = cache->k_pool;
+  a.v_src = cache->v_pool;
+  a.head_dim = desc->head_dim;
+  a.from_pool = true;
+  return cuda_status(launch_kv8_write(a, device_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+dllm_status dllm_kv8_attention_workspace_size(const dllm_layer_desc* desc, const dllm_batch* batch,
+                                              const dllm_kv8_cache* kv8, size_t* bytes) {
+  DLLM_TRY(check_desc(desc));
+  DLLM_TRY(check_batch(batch));
+  DLLM_TRY(check_kv8(kv8, desc));
+  if (bytes == nullptr) return DLLM_ERR_INVALID_ARGUMENT;
+  *bytes = batch->batch > 0 && batch->total_block_rows > 0
+               ? kv8_attention_workspace_bytes(batch->max_block_len, desc->n_heads, kv8->n_kv_heads, desc->head_dim,
+                                               device_sms())
+               : 0;
+  return DLLM_OK;
+}
+
+dllm_status dllm_kv8_attention(const dllm_layer_desc* desc, const dllm_batch* batch, const void* q,
+                               int64_t q_row_stride, const dllm_kv8_cache* kv8, void* o, int32_t o_rows, float* lse,
+                               void* ws, size_t ws_bytes, void* stream) {
+  DLLM_TRY(check_desc(desc));
+  DLLM_TRY(check_batch(batch));
+  if (o_rows != DLLM_ROWS_BLOCK && o_rows != DLLM_ROWS_FULL) return DLLM_ERR_INVALID_ARGUMENT;
+  if (batch->batch == 0 || batch->total_block_rows == 0) return DLLM_OK;
+  size_t need = 0;
+  DLLM_TRY(dllm_kv8_attention_workspace_size(desc, batch, kv8, &need));
+  if (!aligned(q, 16) || q_row_stride % 8 != 0 || q_row_stride < static_cast<int64_t>(desc->n_heads) * desc->head_dim)
+    return DLLM_ERR_INVALID_ARGUMENT;
+  if (!aligned(o, 16) || (lse != nullptr && !aligned(lse, 4))) return DLLM_ERR_INVALID_ARGUMENT;
+  if (ws_bytes < need) return DLLM_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned(ws, 256)) return DLLM_ERR_INVALID_ARGUMENT;
+  Kv8AttnArgs a;
+  a.bt = kv8_batch(batch, kv8->num_pages);
+  a.kv = kv8_pools(kv8);
+  a.q = q;
+  a.q_row = q_row_stride;
+  a.o = o;
+  a.lse = lse;
+  a.full_rows = o_rows == DLLM_ROWS_FULL ? 1 : 0;
+  a.n_heads = desc->n_heads;
+  a.head_dim = desc->head_dim;
+  a.scale_log2 = softmax_scale(desc) * 1.4426950408889634f;
+  a.ws = ws;
+  return cuda_status(launch_kv8_attention(a, device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
 const char* dllm_status_string(dllm_status status) {

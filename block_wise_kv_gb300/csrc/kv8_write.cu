@@ -1,0 +1,244 @@
+// kv8_write.cu — rows of K and V into the 8-bit paged cache.
+//
+// A group is 16 token positions of one head: amax over its new rows gives the
+// scale s = 2^e, the smallest power of two with amax <= 448 s (-60 <= e <= 60),
+// and code = e4m3(x / s).  x / s is exact (a power of two), so the only rounding
+// is the one to e4m3.  Where rows of the group stay, s is at least their present
+// scale and their codes are multiplied by the ratio, again a power of two: exact
+// unless the result is an e4m3 subnormal.  A scale of amax / 448 would fill the
+// last bit of the range, but every growth would round all kept rows again.
+//
+// Bound: HBM, 6 bytes a value (read 2, write 1, for K and for V).  A warp takes
+// one group of K and of V: 16 rows of 256 bytes each, every load in flight before
+// the first is used, 8-byte code stores.  Groups start where a block starts or
+// where a position is a multiple of 16, so a CTA takes a slice of packed rows,
+// finds the groups that begin in it, and deals (group, head) items to its warps.
+#include "attn_common.cuh"
+#include "kv8.cuh"
+
+namespace dllm {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxSlice = 64;  // packed rows a CTA looks at, at most
+constexpr int kCuInSmem = 1024;  // batches up to this many sequences are searched in shared memory
+
+struct Group {
+  int row;      // first new row (packed)
+  int t0, n;    // new rows are slots t0 .. t0 + n of the group
+  int keep_lo;  // rows that stay: slots 0 .. keep_lo, and t0 + n .. keep_hi
+  int keep_hi;
+  int page, quarter;
+};
+
+// The smallest e in [-60, 60] with amax <= 448 * 2^e, for the magnitude bits of a finite bf16.
+__device__ __forceinline__ int scale_exponent(uint32_t amax_bits) {
+  // 448 = 1.75 * 2^8; 1.75 is mantissa 96 of 128
+  const int e = static_cast<int>(amax_bits >> 7) - 127 - ((amax_bits & 127u) <= 96u ? 8 : 7);
+  return min(max(e, -kKv8MaxExp), kKv8MaxExp);
+}
+__device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }
+
+__device__ __forceinline__ float2 bf16x2_f32(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+// Two e4m3 codes to fp32 (exact).
+__device__ __forceinline__ float2 e4m3x2_f32(uint16_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  return __half22float2(*reinterpret_cast<__half2*>(&h));
+}
+// Non-finite values of a bf16 pair to not-a-number (so that they become e4m3's).
+__device__ __forceinline__ uint32_t only_nan(uint32_t u) {
+  if ((u & 0x7f80u) == 0x7f80u) u |= 0x7fu;
+  if ((u & 0x7f800000u) == 0x7f800000u) u |= 0x7f0000u;
+  return u;
+}
+
+// The group of one pool: the lane's pieces x[i] are rows kRows * i + lane / kLanes, 8 columns from 8 * (lane % kLanes).
+template <int D>
+__device__ __forceinline__ void quantise(const uint4 (&x)[D / 16], const Group& g, uint8_t* codes, float* scale,
+                                         int lane, int& err) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIter = 16 / kRows;
+  const int sub = lane / kLanes, col = (lane % kLanes) * 8;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kIter; ++i)
+    m = __vmaxu2(__vmaxu2(m, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu)),
+                 __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+  bool odd = (m & 0xffffu) >= 0x7f80u || (m >> 16) >= 0x7f80u;
+  odd = __any_sync(0xffffffffu, odd);
+  if (odd) {  // a value that is not finite takes no part in the scale
+    err |= kErrRange;
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t a = w[k] & 0x7fff7fffu;
+        if ((a & 0xffffu) >= 0x7f80u) a &= 0xffff0000u;
+        if ((a >> 16) >= 0x7f80u) a &= 0xffffu;
+        m = __vmaxu2(m, a);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const uint32_t amax = max(m & 0xffffu, m >> 16);
+  if (amax > (static_cast<uint32_t>(127 + 8 + kKv8MaxExp) << 7) + 96u) err |= kErrRange;  // beyond 448 * 2^60
+  float s = two_to(scale_exponent(amax));
+  const bool keeps = g.keep_lo > 0 || g.keep_hi > g.t0 + g.n;
+  if (keeps) {
+    const float old = *scale;
+    if (old > s) {
+      s = old;
+    } else if (old < s) {
+      const float ratio = __fdiv_rn(old, s);
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) {
+        const int t = i * kRows + sub;
+        if (t < g.keep_lo || (t >= g.t0 + g.n && t < g.keep_hi)) {
+          uint2* p = reinterpret_cast<uint2*>(codes + t * D + col);
+          const uint2 c = *p;
+          uint32_t out[2];
+          const uint32_t in[2] = {c.x, c.y};
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 lo = e4m3x2_f32(static_cast<uint16_t>(in[k])), hi = e4m3x2_f32(static_cast<uint16_t>(in[k] >> 16));
+            out[k] = static_cast<uint32_t>(cvt_e4m3x2(lo.x * ratio, lo.y * ratio)) |
+                     (static_cast<uint32_t>(cvt_e4m3x2(hi.x * ratio, hi.y * ratio)) << 16);
+          }
+          *p = make_uint2(out[0], out[1]);
+        }
+      }
+    }
+  }
+  const float inv = __frcp_rn(s);  // exact for this library's scales; a present scale of another kind is divided by
+  const bool exact = (__float_as_uint(s) & 0x7fffffu) == 0;
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const int t = i * kRows + sub;
+    if (t < g.t0 || t >= g.t0 + g.n) continue;
+    uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint16_t c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (odd) w[k] = only_nan(w[k]);
+      const float2 f = bf16x2_f32(w[k]);
+      c[k] = exact ? cvt_e4m3x2(f.x * inv, f.y * inv) : cvt_e4m3x2(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
+    }
+    *reinterpret_cast<uint2*>(codes + t * D + col) =
+        make_uint2(c[0] | (static_cast<uint32_t>(c[1]) << 16), c[2] | (static_cast<uint32_t>(c[3]) << 16));
+  }
+  __syncwarp();  // every lane has read the old scale
+  if (lane == 0) *scale = s;
+}
+
+template <int D, bool POOL>
+__global__ void __launch_bounds__(kThreads) kv8_write_kernel(const Kv8WriteArgs a, int slice, int heads_per_cta) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIter = 16 / kRows;
+  __shared__ int cu[kCuInSmem + 1];
+  __shared__ Group groups[kMaxSlice];
+  __shared__ int n_groups;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const BatchArgs& bt = a.bt;
+  const int row0 = blockIdx.x * slice;
+  const bool in_smem = bt.batch <= kCuInSmem;
+  int err = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (t == 0) n_groups = 0;
+  if (in_smem)
+    for (int i = t; i <= bt.batch; i += kThreads) cu[i] = __ldg(bt.cu_block + i);
+  __syncthreads();
+  const int* cub = in_smem ? cu : bt.cu_block;
+  const int total = min(cub[bt.batch], bt.total_block_rows);
+  if (row0 >= total) {
+    if (row0 == 0 && t == 0 && cub[bt.batch] < 0) report_error(bt.err, kErrBadShape);
+    return;
+  }
+  if (t < slice && row0 + t < total) {
+    const int j = row0 + t;
+    int lo = 0, hi = bt.batch;  // the last sequence that starts at or before row j
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cub[mid] <= j)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int b = lo, i = j - cub[b];
+    const int n = __ldg(bt.seq_len + b), s = __ldg(bt.block_start + b), len = __ldg(bt.block_len + b);
+    const int pos = s + i;
+    if (n < 0 || n > bt.max_seq_len || s < 0 || len < 0 || len > n - s || i < 0 || i >= len ||
+        pos / kPage >= bt.max_pages) {
+      err |= kErrBadShape;
+    } else if (i == 0 || pos % kKv8Group == 0) {
+      const int pg = __ldg(bt.block_table + static_cast<size_t>(b) * bt.max_pages + pos / kPage);
+      if (pg < 0 || pg >= bt.num_pages) {
+        err |= kErrBadPage;
+      } else {
+        Group g;
+        const int first = pos / kKv8Group * kKv8Group;
+        g.row = j;
+        g.t0 = pos - first;
+        g.n = min(kKv8Group - g.t0, len - i);
+        g.keep_lo = g.t0;
+        g.keep_hi = min(kKv8Group, n - first);
+        g.page = pg;
+        g.quarter = (first % kPage) / kKv8Group;
+        groups[atomicAdd(&n_groups, 1)] = g;
+      }
+    }
+  }
+  __syncthreads();
+  const int h0 = blockIdx.y * heads_per_cta, nh = min(heads_per_cta, a.kv.n_kv_heads - h0);
+  const int items = n_groups * nh;
+  const int sub = lane / kLanes, col = (lane % kLanes) * 8;
+  for (int it = warp; it < items; it += kWarps) {
+    const Group g = groups[it / nh];
+    const int h = h0 + it % nh;
+    const size_t slot = (static_cast<size_t>(g.page) * a.kv.n_kv_heads + h) * kPage + g.quarter * kKv8Group;
+    uint4 k[kIter], v[kIter];
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int tt = i * kRows + sub;
+      const bool on = tt >= g.t0 && tt < g.t0 + g.n;
+      size_t ko, vo;
+      if (POOL) {
+        ko = vo = (slot + tt) * D + col;
+      } else {
+        const long long j = g.row + tt - g.t0;
+        ko = static_cast<size_t>(j * a.k_row + h * a.k_head + col);
+        vo = static_cast<size_t>(j * a.v_row + h * a.v_head + col);
+      }
+      k[i] = on ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k_src) + ko)) : make_uint4(0, 0, 0, 0);
+      v[i] = on ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v_src) + vo)) : make_uint4(0, 0, 0, 0);
+    }
+    const size_t sc = (static_cast<size_t>(g.page) * a.kv.n_kv_heads + h) * kKv8Groups + g.quarter;
+    quantise<D>(k, g, a.kv.k + slot * D, a.kv.k_scale + sc, lane, err);
+    quantise<D>(v, g, a.kv.v + slot * D, a.kv.v_scale + sc, lane, err);
+  }
+  if (err) report_error(bt.err, err);
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_write(const Kv8WriteArgs& a, int num_sms, cudaStream_t stream) {
+  const int rows = a.bt.total_block_rows, heads = a.kv.n_kv_heads;
+  // Slices of 64 rows and four heads where that fills the GPU twice over (16 items and more for a CTA's eight
+  // warps), else 16 rows and one head: single tokens make every row a group of its own.
+  const long long wide = static_cast<long long>((rows + 63) / 64) * ((heads + 3) / 4);
+  const bool big = wide >= 2 * num_sms;
+  const int slice = big ? 64 : 16, hc = big ? 4 : 1;
+  const dim3 grid((rows + slice - 1) / slice, (heads + hc - 1) / hc);
+  if (a.head_dim == 128)
+    return a.from_pool ? attn::launch_pdl(kv8_write_kernel<128, true>, grid, kThreads, 0, 0, stream, a, slice, hc)
+                       : attn::launch_pdl(kv8_write_kernel<128, false>, grid, kThreads, 0, 0, stream, a, slice, hc);
+  return a.from_pool ? attn::launch_pdl(kv8_write_kernel<64, true>, grid, kThreads, 0, 0, stream, a, slice, hc)
+                     : attn::launch_pdl(kv8_write_kernel<64, false>, grid, kThreads, 0, 0, stream, a, slice, hc);
+}
+
+}  // namespace dllm

@@ -33,6 +33,7 @@ DLLM_DEVERR_TIMEOUT = 1
 DLLM_DEVERR_BAD_PAGE = 2
 DLLM_DEVERR_BAD_SHAPE = 4
 DLLM_DEVERR_RANGE = 8
+DLLM_DEVERR_NO_PAGES = 16
 
 DLLM_OP_CACHE_BUILD = 0
 DLLM_OP_BLOCK_QKV_ROPE_WRITE = 1
@@ -41,13 +42,18 @@ DLLM_OP_STATE_MERGE = 3
 DLLM_OP_STEP_ATTENTION = 4
 DLLM_OP_CACHE_ADVANCE = 5
 
+DLLM_ROWS_BLOCK = 0
+DLLM_ROWS_FULL = 1
+
 PAGE = 64
+KV8_GROUP = 16  # token positions that share a scale of the 8-bit cache
 
 # Every symbol include/dllm.h declares.
 EXPORTS = ("dllm_workspace_size", "dllm_rope_table_build", "dllm_qkv_weight_packed_bytes", "dllm_qkv_weight_pack",
            "dllm_cache_build", "dllm_cache_advance", "dllm_block_qkv_rope_write", "dllm_block_qkv_rope_write_noalloc",
            "dllm_block_attention", "dllm_state_merge", "dllm_step_attention", "dllm_lm_head_workspace_size",
-           "dllm_block_lm_head", "dllm_ffn_workspace_size", "dllm_block_ffn", "dllm_status_string")
+           "dllm_block_lm_head", "dllm_ffn_workspace_size", "dllm_block_ffn", "dllm_batch_plan", "dllm_kv8_write",
+           "dllm_kv8_write_pool", "dllm_kv8_attention_workspace_size", "dllm_kv8_attention", "dllm_status_string")
 
 
 class DllmError(RuntimeError):
@@ -78,6 +84,16 @@ class BatchC(ctypes.Structure):
                 ("error_flag", ctypes.c_void_p)]
 
 
+class Kv8CacheC(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32)]
+
+
+class PageRingC(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("state", ctypes.c_void_p), ("state_out", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -93,7 +109,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                    "(run `python -m block_wise_kv_gb300.build`)")
             lib = ctypes.CDLL(p)
             P = ctypes.POINTER
-            vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+            vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
             sig = {
                 "dllm_workspace_size": [P(LayerDescC), P(BatchC), i32, P(sz)],
                 "dllm_rope_table_build": [P(LayerDescC), i32, vp, vp],
@@ -113,6 +129,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
                 "dllm_block_lm_head": [P(LayerDescC), P(BatchC), i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
                 "dllm_ffn_workspace_size": [P(LayerDescC), P(BatchC), i32, P(sz)],
                 "dllm_block_ffn": [P(LayerDescC), P(BatchC), i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+                "dllm_batch_plan": [P(BatchC), vp, vp, vp, vp, vp, P(PageRingC), vp, vp, vp, vp],
+                "dllm_kv8_write": [P(LayerDescC), P(BatchC), vp, i64, i64, vp, i64, i64, P(Kv8CacheC), vp],
+                "dllm_kv8_write_pool": [P(LayerDescC), P(BatchC), P(CacheC), P(Kv8CacheC), vp],
+                "dllm_kv8_attention_workspace_size": [P(LayerDescC), P(BatchC), P(Kv8CacheC), P(sz)],
+                "dllm_kv8_attention": [P(LayerDescC), P(BatchC), vp, i64, P(Kv8CacheC), vp, i32, vp, vp, sz, vp],
             }
             for name, argt in sig.items():
                 fn = getattr(lib, name)
@@ -262,6 +283,44 @@ def dllm_block_ffn(desc, batch, d_ff, o_full, x_block, w_o, ffn_gain, w_gate_up,
         _nbytes(ws), _stream(stream)))
 
 
+def dllm_batch_plan(batch, pages_held, pages_held_out, block_table, cu_block, cu_seq, ring, row_slot=None,
+                    row_seq=None, row_pos=None, stream=None):
+    _check("dllm_batch_plan", load().dllm_batch_plan(
+        ctypes.byref(batch), _ptr(pages_held), _ptr(pages_held_out), _ptr(block_table), _ptr(cu_block), _ptr(cu_seq),
+        ctypes.byref(ring), _ptr(row_slot), _ptr(row_seq), _ptr(row_pos), _stream(stream)))
+
+
+def dllm_kv8_write(desc, batch, k_rows: torch.Tensor, v_rows: torch.Tensor, kv8, stream=None):
+    """k_rows, v_rows: bf16 [M][n_kv_heads][head_dim], the last dimension
+    contiguous (views of a wider projection output are fine)."""
+    if k_rows.stride(-1) != 1 or v_rows.stride(-1) != 1:
+        raise DllmError("dllm_kv8_write", DLLM_ERR_INVALID_ARGUMENT)
+    _check("dllm_kv8_write", load().dllm_kv8_write(
+        ctypes.byref(desc), ctypes.byref(batch), _ptr(k_rows), k_rows.stride(0), k_rows.stride(1), _ptr(v_rows),
+        v_rows.stride(0), v_rows.stride(1), ctypes.byref(kv8), _stream(stream)))
+
+
+def dllm_kv8_write_pool(desc, batch, cache, kv8, stream=None):
+    _check("dllm_kv8_write_pool", load().dllm_kv8_write_pool(
+        ctypes.byref(desc), ctypes.byref(batch), ctypes.byref(cache), ctypes.byref(kv8), _stream(stream)))
+
+
+def dllm_kv8_attention_workspace_size(desc, batch, kv8) -> int:
+    out = ctypes.c_size_t(0)
+    _check("dllm_kv8_attention_workspace_size", load().dllm_kv8_attention_workspace_size(
+        ctypes.byref(desc), ctypes.byref(batch), ctypes.byref(kv8), ctypes.byref(out)))
+    return int(out.value)
+
+
+def dllm_kv8_attention(desc, batch, q: torch.Tensor, kv8, o, lse, ws, o_rows: int = DLLM_ROWS_BLOCK, stream=None):
+    """q: bf16 [M][n_heads][head_dim], rows contiguous, any row stride."""
+    if q.stride(-1) != 1 or q.stride(1) != q.shape[2]:
+        raise DllmError("dllm_kv8_attention", DLLM_ERR_INVALID_ARGUMENT)
+    _check("dllm_kv8_attention", load().dllm_kv8_attention(
+        ctypes.byref(desc), ctypes.byref(batch), _ptr(q), q.stride(0), ctypes.byref(kv8), _ptr(o), int(o_rows),
+        _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
 # ---------------------------------------------------- memory / structs ----
 def layer_desc(d_model: int, n_heads: int, head_dim: int, rope_theta: float, rms_eps: float = 1e-5,
                softmax_scale: float = 0.0) -> LayerDescC:
@@ -319,6 +378,76 @@ class BlockRange:
         self.c = BatchC(base.batch, base.max_pages, self.total_block_rows, base.total_seq_rows, self.max_block_len,
                         base.max_seq_len, _ptr(bd["block_table"]), _ptr(bd["seq_len"]), _ptr(d["block_start"]),
                         _ptr(d["block_len"]), _ptr(d["cu_block"]), _ptr(bd["cu_seq"]), _ptr(base.error))
+
+
+class BatchView:
+    """A dllm_batch over device tensors that the caller holds (int32, as
+    dllm_batch_plan fills them), with the host bounds that size the launches.
+    The tensors stay alive as long as this object."""
+
+    def __init__(self, block_table, seq_len, block_start, block_len, cu_block, cu_seq, total_block_rows: int,
+                 total_seq_rows: int, max_block_len: int, max_seq_len: int, error=None):
+        self.tensors = (block_table, seq_len, block_start, block_len, cu_block, cu_seq, error)
+        self.error = error
+        for t in self.tensors:
+            if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
+                raise ValueError("batch metadata are contiguous int32 tensors")
+        self.c = BatchC(seq_len.shape[0], block_table.shape[1], total_block_rows, total_seq_rows, max_block_len,
+                        max_seq_len, _ptr(block_table), _ptr(seq_len), _ptr(block_start), _ptr(block_len),
+                        _ptr(cu_block), _ptr(cu_seq), _ptr(error))
+
+    def error_bits(self) -> int:
+        return 0 if self.error is None else int(self.error.item())
+
+
+class PageRing:
+    """A dllm_page_ring over device int32 tensors: pages [P], state [2] (head,
+    count) and state_out [2]."""
+
+    def __init__(self, pages, state, state_out):
+        for t in (pages, state, state_out):
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError("a page ring's tensors are contiguous int32")
+        self.pages, self.state, self.state_out = pages, state, state_out
+        self.c = PageRingC(_ptr(pages), _ptr(state), _ptr(state_out), pages.shape[0])
+
+    @classmethod
+    def full(cls, num_pages: int, device="cuda") -> "PageRing":
+        """Every page free, in order."""
+        return cls(torch.arange(num_pages, dtype=torch.int32, device=device),
+                   torch.tensor([0, num_pages], dtype=torch.int32, device=device),
+                   torch.zeros(2, dtype=torch.int32, device=device))
+
+    def swapped(self) -> "PageRing":
+        """The ring of the next step: this one's state_out is its state."""
+        return PageRing(self.pages, self.state_out, self.state)
+
+
+class Kv8Cache:
+    """The 8-bit paged pools of one layer: codes as torch.float8_e4m3fn (zero)
+    and one scale per 16 positions of a head (one)."""
+
+    def __init__(self, num_pages: int, n_kv_heads: int, head_dim: int, device="cuda", tensors=None):
+        if tensors is None:
+            shape = (num_pages, n_kv_heads, PAGE, head_dim)
+            k, v = (torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2))
+            ks, vs = (torch.ones(num_pages, n_kv_heads, PAGE // KV8_GROUP, device=device) for _ in range(2))
+            tensors = (k, v, ks, vs)
+        self.k, self.v, self.k_scale, self.v_scale = tensors
+        for t, dtype in zip(tensors, (torch.float8_e4m3fn,) * 2 + (torch.float32,) * 2):
+            if t.dtype != dtype or not t.is_contiguous():
+                raise ValueError("the pools are contiguous float8_e4m3fn tensors, the scales contiguous float32")
+        shape = (num_pages, n_kv_heads, PAGE, head_dim)
+        scales = (num_pages, n_kv_heads, PAGE // KV8_GROUP)
+        if any(tuple(t.shape) != s for t, s in zip(tensors, (shape, shape, scales, scales))):
+            raise ValueError(f"pools of shape {shape} and scales of shape {scales} are needed")
+        self.num_pages = num_pages
+        self.c = Kv8CacheC(_ptr(self.k), _ptr(self.v), _ptr(self.k_scale), _ptr(self.v_scale), num_pages, n_kv_heads)
+
+    @classmethod
+    def of(cls, k, v, k_scale, v_scale) -> "Kv8Cache":
+        """Over tensors that the caller holds."""
+        return cls(k.shape[0], k.shape[1], k.shape[3], tensors=(k, v, k_scale, v_scale))
 
 
 class PagedCache:

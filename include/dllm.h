@@ -109,7 +109,9 @@ typedef enum dllm_status {
 #define DLLM_DEVERR_TIMEOUT 1   /* a bounded on-chip wait gave up */
 #define DLLM_DEVERR_BAD_PAGE 2  /* block_table entry outside [0, num_pages) */
 #define DLLM_DEVERR_BAD_SHAPE 4 /* seq_len/block_start/block_len/cu_* contradict the host bounds */
-#define DLLM_DEVERR_RANGE 8     /* a state's O~ / l beyond fp16 range (a value above 65504 in magnitude) */
+#define DLLM_DEVERR_RANGE 8     /* a state's O~ / l beyond fp16 range (a value above 65504 in magnitude); in the
+                                 * 8-bit cache a key or value that is not finite or beyond 448 * 2^60 */
+#define DLLM_DEVERR_NO_PAGES 16 /* dllm_batch_plan: fewer free pages than the batch asks for */
 
 /* Shape of one attention layer. */
 typedef struct dllm_layer_desc {
@@ -376,6 +378,125 @@ dllm_status dllm_block_ffn(const dllm_layer_desc* desc, const dllm_batch* batch,
                            const void* x_block, const void* w_o, const void* ffn_gain, const void* w_gate_up,
                            const float* w_gate_up_scale, const void* w_down, const float* w_down_scale,
                            void* y_block, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit paged cache: the batch planned on the device, rows written into
+ * e4m3 pages, and the attention of the block rows over them.  An addition of
+ * this library (the pages above keep a 16-bit cache); it uses the same pages
+ * of 64 tokens, block table and dllm_batch, with grouped heads.
+ *
+ * Where the calls above ask for block_len >= 1 and seq_len >= 1, these accept
+ * 0 for either (a place of a padded batch that holds no request): such a
+ * sequence has no rows, nothing is read or written for it.
+ * total_block_rows, total_seq_rows, max_block_len and max_seq_len bound the
+ * device arrays; the actual sums and lengths may be smaller from one replay of
+ * a captured call to the next.  Every call waits for the preceding kernel of
+ * its stream before it reads or writes anything. */
+
+/* The 8-bit cache of one layer (device buffers, caller-owned).  The value of a
+ * code is code * scale of its group: 16 consecutive token positions (a quarter
+ * of a page) of one head.  k_pool and v_pool 16-byte aligned, the scales 16. */
+typedef struct dllm_kv8_cache {
+  void* k_pool;       /* e4m3 [num_pages][n_kv_heads][64][head_dim] */
+  void* v_pool;       /* e4m3 [num_pages][n_kv_heads][64][head_dim] */
+  float* k_scale;     /* fp32 [num_pages][n_kv_heads][4]: positive, in [2^-60, 2^60] */
+  float* v_scale;     /* fp32 [num_pages][n_kv_heads][4] */
+  int32_t num_pages;  /* num_pages * n_kv_heads * 64 < 2^31 */
+  int32_t n_kv_heads; /* divides dllm_layer_desc.n_heads: query head h reads key head h / (n_heads / n_kv_heads) */
+} dllm_kv8_cache;
+
+/* A ring of free page ids: `count` ids from pages[head] on, modulo num_pages. */
+typedef struct dllm_page_ring {
+  int32_t* pages;       /* device int32 [num_pages] */
+  const int32_t* state; /* device int32 [2]: head, count before the call */
+  int32_t* state_out;   /* device int32 [2]: head, count after it (not `state`) */
+  int32_t num_pages;    /* slots of the ring; page ids are in [0, num_pages) */
+} dllm_page_ring;
+
+/* The batch from request lengths, on the device, in one launch: pages for what
+ * each sequence has grown, pages given back for what it has shrunk, the prefix
+ * sums, and where each block row lies.  With need_b = ceil(seq_len[b] / 64):
+ *   - need_b > pages_held[b]: block_table[b][pages_held[b] .. need_b) get ids
+ *     from the ring's head on, sequences in order.  A sequence gets its pages
+ *     iff the pages asked for up to and including it were free when the call
+ *     began; otherwise it keeps what it holds, and DLLM_DEVERR_NO_PAGES is set.
+ *   - need_b < pages_held[b]: the ids in block_table[b][need_b .. pages_held[b])
+ *     go to the ring's tail, sequences in order (free for the next call); the
+ *     entries stay as they are.
+ *   - pages_held_out[b] = the pages it holds now; ring->state_out likewise.
+ *   - cu_block, cu_seq: exclusive sums of block_len and seq_len, [batch + 1].
+ *   - row j of the packed block rows, i = j - cu_block[b]: row_seq[j] = b,
+ *     row_pos[j] = p = block_start[b] + i, row_slot[j] =
+ *     block_table[b][p / 64] * 64 + p % 64, or -1 where the sequence holds no
+ *     page for p; all three -1 for cu_block[batch] <= j < total_block_rows.
+ * The call reads only what it does not write, so the same call again gives the
+ * same outputs; the next step passes pages_held_out and state_out as its
+ * pages_held and state.  batch->block_table, cu_block and cu_seq are not read;
+ * they are usually the buffers passed here, for the calls that follow (as the
+ * header's note on overlap asks, not as the kernel directly before
+ * dllm_block_attention, dllm_state_merge or dllm_step_attention).
+ *   A seq_len outside [0, max_seq_len], a pages_held outside [0,
+ *   max_pages_per_seq] (both: the sequence keeps its pages, its lengths count
+ *   as 0) or a block outside its sequence (its rows count as 0) sets
+ *   DLLM_DEVERR_BAD_SHAPE, as do sums beyond total_block_rows or
+ *   total_seq_rows and a ring state outside the ring (taken as empty); an id
+ *   outside the pages sets DLLM_DEVERR_BAD_PAGE and is written as -1.
+ *   row_slot, row_seq, row_pos: device int32 [total_block_rows], 16-byte
+ *   aligned, each nullable.  pages_held_out must not overlap pages_held. */
+dllm_status dllm_batch_plan(const dllm_batch* batch, const int32_t* pages_held, int32_t* pages_held_out,
+                            int32_t* block_table, int32_t* cu_block, int32_t* cu_seq, const dllm_page_ring* ring,
+                            int32_t* row_slot, int32_t* row_seq, int32_t* row_pos, void* stream);
+
+/* Write the current blocks' rows of K and V into the 8-bit cache.  A group (16
+ * positions of a head) that gets rows takes the scale
+ *   s = the smallest power of two, in [2^-60, 2^60], with max |new row| <= 448 s,
+ * or, where it also holds rows that stay (positions below seq_len outside the
+ * block), the larger of that and its present scale; the rows that stay are
+ * then expressed in the new scale (exact but for results below 2^-6 s, which
+ * round).  code = e4m3(x / s), round to nearest even.  A value that is not
+ * finite is stored as the not-a-number code, leaves the scale alone and sets
+ * DLLM_DEVERR_RANGE, as does one beyond 448 * 2^60, which is stored as +-448.
+ * Positions at or beyond seq_len are left as they are.
+ *   k_rows, v_rows: device bf16, row j of the packed block rows (cu_block) and
+ *   head h at j * row_stride + h * head_stride elements, head_dim contiguous;
+ *   16-byte aligned, strides multiples of 8 and not negative.
+ * The pages of the positions written must be distinct among the sequences. */
+dllm_status dllm_kv8_write(const dllm_layer_desc* desc, const dllm_batch* batch, const void* k_rows,
+                           int64_t k_row_stride, int64_t k_head_stride, const void* v_rows, int64_t v_row_stride,
+                           int64_t v_head_stride, const dllm_kv8_cache* kv8, void* stream);
+
+/* dllm_kv8_write from the bf16 pools of `cache` (k_pool and v_pool only; as
+ * dllm_cache_build and dllm_block_qkv_rope_write leave them): the same block
+ * table names the pages of both, and kv8->n_kv_heads == desc->n_heads. */
+dllm_status dllm_kv8_write_pool(const dllm_layer_desc* desc, const dllm_batch* batch, const dllm_cache* cache,
+                                const dllm_kv8_cache* kv8, void* stream);
+
+/* Where dllm_kv8_attention puts row i of sequence b's block. */
+#define DLLM_ROWS_BLOCK 0 /* row cu_block[b] + i: packed like q_block */
+#define DLLM_ROWS_FULL 1  /* row cu_seq[b] + block_start[b] + i: o_full, lse of dllm_block_attention */
+
+/* dllm_block_attention over the 8-bit cache, with grouped heads: for each
+ * block row i of sequence b and query head h, over ALL keys j in [0, N_b),
+ *   O = sum_j softmax_j(scale * q_i . k_j) v_j,  L = log sum_j exp(scale * q_i . k_j)
+ * with k_j, v_j the values the codes stand for.  Single-token decoding is
+ * block_len = 1.  What lies at or behind N_b in a sequence's last page is not
+ * used (it may hold anything).  The split of the keys over the GPU depends on
+ * the batch alone, and partial results are joined in a fixed order: the same
+ * call gives the same bits.
+ *   q: device bf16, row j of the packed block rows at j * q_row_stride
+ *   elements, [n_heads][head_dim] contiguous; 16-byte aligned, the stride a
+ *   multiple of 8 and at least n_heads * head_dim.
+ *   o: device bf16 rows of [n_heads][head_dim], 16-byte aligned; lse: device
+ *   fp32 rows of [n_heads], nullable; both as o_rows (DLLM_ROWS_*) says.  Rows
+ *   of no block are left as they are.
+ *   ws: dllm_kv8_attention_workspace_size bytes, 256-byte aligned; its first
+ *   4 KB (counters) must be zero before the first use, and every call leaves
+ *   them zero.  Calls that may run at the same time need workspaces of their own. */
+dllm_status dllm_kv8_attention_workspace_size(const dllm_layer_desc* desc, const dllm_batch* batch,
+                                              const dllm_kv8_cache* kv8, size_t* bytes);
+dllm_status dllm_kv8_attention(const dllm_layer_desc* desc, const dllm_batch* batch, const void* q,
+                               int64_t q_row_stride, const dllm_kv8_cache* kv8, void* o, int32_t o_rows, float* lse,
+                               void* ws, size_t ws_bytes, void* stream);
 
 /* Static description of a status code (never NULL). */
 const char* dllm_status_string(dllm_status status);
