@@ -1,97 +1,797 @@
-// kv8_attn.cu — attention of the block rows over the e4m3 paged cache (simple form:
-// one warp per block row and query head, a lane per key for the scores, the online
-// softmax over 32 keys at a time).
+// kv8_attn.cu — attention of the block rows over the e4m3 paged cache, on tcgen05.
+//
+// A unit of work is (sequence, key head, up to NQ of the rows that share it): row r
+// is block row r / G under query head h G + r % G, G = query heads to a key head.
+// Keys go in tiles of 128 (two pages), and everything is transposed so that the
+// 128 keys fill the tensor core's M and the few rows are its N:
+//
+//   S^T[key][row] = K8 (Q_hi + Q_lo)^T         e4m3 x e4m3, two products into one accumulator
+//   P^T[key][row] = 2^(x),  x = f_key S - R_row  (f_key = key scale x q scale x softmax scale x log2 e)
+//   O^T[col][row] += V8^T (P_hi + P_mid + P_lo)^T  e4m3 x e5m2
+//
+// The pages are used as they lie: no key or value is ever converted.  What makes that
+// exact enough is the other operand.  A row's q is scaled by a power of two so that
+// the unit's largest is in (224, 448] and split into two e4m3 parts: 4 + 4 bits hold
+// bf16's 8 exactly down to 2^-11 of the largest, and below that to 2^-19 of it.
+// A weight is rounded to fp16 (11 bits) and split into three e5m2 parts, which is
+// exact (3 bits each, rounded to nearest) but for an absolute 2^-17, half of the
+// smallest e5m2 step, where a row's largest is 2^12 or more: a softmax with one large
+// weight and a long flat tail that together weighs as much keeps its tail.  The value scale of a key multiplies
+// its weight before the split; the sum l takes the weight without it.
+//
+// The thread that holds a key's scores has its scales as two scalars; a row's
+// reference R is the same for all 128 threads.  R is set from a unit's first tile (so
+// that the largest weight x value scale is 2^12) and raised only when one passes 2^15:
+// a vote per tile, and otherwise no reduction over keys at all until the unit's end,
+// where the 128 partial sums of each row are added.
+//
+// Roles of a CTA's six warps: 0-3 softmax (TMEM lane = key, then = column of O^T),
+// 4 TMA producer, 5 MMA issuer.  K and V tiles share one ring of 16 KB slots (8 KB for
+// d = 64); the scores are double-buffered in TMEM, so the tensor core runs S of the next
+// tile while the softmax works.  Two CTAs an SM cover each other's serial parts.
+//
+// Split: the tiles of all units form one line, cut into as many equal pieces as CTAs
+// (or fewer, where there are few tiles): a ragged batch or one long sequence loads all
+// SMs alike.  A unit cut by a border is joined from its pieces' (O, R, l) in the
+// workspace by the CTA that finishes last, in the order of the keys.
+#include <algorithm>
+
 #include "attn_common.cuh"
 #include "kv8.cuh"
 
 namespace dllm {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kSoftWarps = 4;
+constexpr int kSoft = kSoftWarps * 32;
+constexpr int kProducerWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 192;
+constexpr int kTile = 128;  // keys per tile: two pages
+constexpr int kCtasPerSm = 2;
+constexpr uint32_t kTmemCols = 256;  // of a CTA: two fit an SM's 512
+constexpr int kScaleSlots = 8;       // tiles whose scales are in shared memory
+constexpr size_t kCounterBytes = 4096;
+constexpr float kTop = 12.f;    // log2 of a row's largest weight x value scale when R is set
+constexpr float kLimit = 15.f;  // and where it is raised
 
-__device__ __forceinline__ float2 e4m3x2_f32(uint16_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-  return __half22float2(*reinterpret_cast<__half2*>(&h));
+template <int D, int NQ>
+struct Cfg {
+  static constexpr int kSlotBytes = kTile * D;
+  static constexpr int kQBytes = NQ * D * 2;           // hi, lo
+  static constexpr bool kWide = NQ == 32;              // the three parts side by side in one 128-byte row
+  static constexpr int kPBytes = kWide ? kTile * 128 : 3 * kTile * 64;
+  static constexpr int kOCols = kWide ? 3 * NQ : NQ;   // TMEM columns of O
+  static constexpr int kBudget = 113 * 1024 - 1024 - 5120;  // two CTAs an SM: alignment slack, static shared memory
+  static constexpr int kSlots0 = (kBudget - kQBytes - kPBytes) / kSlotBytes;
+  static constexpr int kSlots = kSlots0 > 10 ? 10 : kSlots0;
+  static constexpr int kDynSmem = kSlots * kSlotBytes + kQBytes + kPBytes + 1024;
+  static_assert(kSlots >= 4, "a tile's K and V, and the next tile's");
+  static_assert(kSlots / 2 + 2 < kScaleSlots, "scales stay until the softmax has read them");
+  static_assert(2 * NQ + kOCols <= static_cast<int>(kTmemCols), "TMEM columns");
+  static constexpr size_t kPartFloats = static_cast<size_t>(NQ) * D + 2 * NQ;  // O, R, l
+};
+
+// ------------------------------------------------------------ descriptors
+// Tiles of 64- or 128-byte rows with the swizzle of that width: 8-row atoms one after the other.
+template <int ROW>
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr) {
+  static_assert(ROW == 64 || ROW == 128, "swizzled rows");
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(ROW * 8 >> 4) << 32;  // stride byte offset: one 8-row atom
+  d |= static_cast<uint64_t>(1) << 46;             // descriptor version for tcgen05
+  d |= static_cast<uint64_t>(ROW == 128 ? 2 : 4) << 61;
+  return d;
+  // leading byte offset 0: no operand here has a second swizzle row along its contiguous dimension.  (V of d = 64
+  // is taken as M = 128 with the offset 0: lanes 64-127 of O^T repeat lanes 0-63 and are not read.)
+}
+// kind::f8f6f4, fp32 accumulator: A e4m3, B e4m3 or e5m2; either operand K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_f8(int m, int n, bool b_e5m2, bool mn) {
+  return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((mn ? 1u : 0u) << 15) | ((mn ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+// Byte offset of 16-byte chunk c of row r in a tile of swizzled ROW-byte rows.
+template <int ROW>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  return ROW == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// Barrier of the softmax warps that ORs a predicate over their threads.
+__device__ __forceinline__ bool soft_any(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "n"(kSoft)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void soft_sync() { named_barrier(1, kSoft); }
+
+// Reduce 32 values over the warp's lanes: lane i gets the result of v[i] (31 shuffles; v is destroyed).
+template <class Op>
+__device__ __forceinline__ float reduce_transposed(float (&v)[32], int lane, Op op) {
+#pragma unroll
+  for (int w = 16; w > 0; w >>= 1) {
+    const bool up = (lane & w) != 0;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float keep = up ? v[i + w] : v[i], give = up ? v[i] : v[i + w];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, w));
+    }
+  }
+  return v[0];
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const Kv8AttnArgs a) {
-  __shared__ float qs[kWarps][D];
+// ------------------------------------------------------------ work
+struct Seq {
+  int n, s, rows, cub, cus;
+  int npages, tiles, nqt;  // tiles = 0: nothing to do
+  bool bad;
+};
+template <int NQ>
+__device__ __forceinline__ Seq load_seq(const Kv8AttnArgs& a, int b) {
   const BatchArgs& bt = a.bt;
-  const int b = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = a.n_heads / a.kv.n_kv_heads;
+  Seq q;
+  q.n = __ldg(bt.seq_len + b);
+  q.s = __ldg(bt.block_start + b);
+  q.rows = __ldg(bt.block_len + b);
+  q.cub = __ldg(bt.cu_block + b);
+  q.cus = __ldg(bt.cu_seq + b);
+  q.tiles = q.nqt = q.npages = 0;
+  q.bad = false;
+  if (q.rows == 0 || q.n == 0) return q;
+  if (q.n < 0 || q.n > bt.max_seq_len || q.rows < 0 || q.rows > bt.max_block_len || q.s < 0 || q.rows > q.n - q.s ||
+      q.cub < 0 || q.rows > bt.total_block_rows - q.cub || (q.n + kPage - 1) / kPage > bt.max_pages ||
+      (a.full_rows && (q.cus < 0 || q.n > bt.total_seq_rows - q.cus))) {
+    q.bad = true;
+    return q;
+  }
+  q.npages = (q.n + kPage - 1) / kPage;
+  q.tiles = (q.n + kTile - 1) / kTile;
+  q.nqt = (q.rows * (a.n_heads / a.kv.n_kv_heads) + NQ - 1) / NQ;
+  return q;
+}
+template <int NQ>
+__device__ __forceinline__ long long seq_work(const Kv8AttnArgs& a, const Seq& q) {
+  return static_cast<long long>(a.kv.n_kv_heads) * q.nqt * q.tiles;
+}
+
+// A CTA's piece [lo, hi) of the line of tiles, walked unit by unit by every role alike.
+template <int NQ>
+struct Walk {
+  const Kv8AttnArgs& a;
+  long long base, pos, hi;  // where sequence b begins on the line; the next tile; the end
+  int b;
+  Seq q;
+  // the current part of a unit: tiles [t0, t1) of (b, h, qt), which lies at u0 on the line
+  int h, qt, t0, t1;
+  long long u0;
+  __device__ Walk(const Kv8AttnArgs& args, int b0, long long base0, long long lo, long long hi0)
+      : a(args), base(base0), pos(lo), hi(hi0), b(b0) {
+    if (pos < hi) q = load_seq<NQ>(a, b);
+  }
+  __device__ bool next() {
+    if (pos >= hi) return false;
+    long long w = seq_work<NQ>(a, q);
+    while (pos >= base + w) {
+      base += w;
+      q = load_seq<NQ>(a, ++b);
+      w = seq_work<NQ>(a, q);
+    }
+    const int x = static_cast<int>((pos - base) / q.tiles);  // unit of the sequence
+    h = x / q.nqt;
+    qt = x % q.nqt;
+    u0 = base + static_cast<long long>(x) * q.tiles;
+    t0 = static_cast<int>(pos - u0);
+    t1 = static_cast<int>(min(static_cast<long long>(q.tiles), hi - u0));
+    pos = u0 + t1;
+    return true;
+  }
+};
+
+// ------------------------------------------------------------ the kernel
+template <int D, int NQ>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const Kv8AttnArgs a) {
+  using C = Cfg<D, NQ>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* const smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+  const uint32_t ring = smem_u32(smem), p_base = ring + C::kSlots * C::kSlotBytes, q_base = p_base + C::kPBytes;
+  __shared__ uint64_t full_bar[C::kSlots], empty_bar[C::kSlots], s_full[2], s_free[2], p_ready, pv_done, q_ready;
+  __shared__ uint64_t scale_bar[kScaleSlots], drain_bar;
+  __shared__ uint32_t tmem_sh;
+  __shared__ __align__(16) float scales[kScaleSlots][2][8];  // K, V: two pages of four groups
+  __shared__ float ref_sh[NQ], alpha_sh[NQ], red_sh[kSoftWarps][NQ], l_sh[NQ];
+  __shared__ long long row_sh[NQ];  // element offset of a row's output, -1 for none
+  __shared__ float amax_sh[kSoftWarps];
+  __shared__ long long seg_sh[kThreads + 1];
+  __shared__ long long start_base;
+  __shared__ int start_b, last_sh;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
+  const BatchArgs& bt = a.bt;
+  if (tid == 0) {
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], kSoftWarps);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) mbar_init(&scale_bar[i], 1);
+    mbar_init(&drain_bar, 1);
+    mbar_init(&p_ready, kSoft);
+    mbar_init(&pv_done, 1);
+    mbar_init(&q_ready, kSoft);
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == kMmaWarp) tmem_alloc(&tmem_sh, kTmemCols);
   griddep_wait();
   griddep_launch_dependents();
-  const int n = bt.seq_len[b], s = bt.block_start[b], rows = bt.block_len[b], cub = bt.cu_block[b], cus = bt.cu_seq[b];
-  if (rows == 0 || n == 0) return;
-  if (n < 0 || n > bt.max_seq_len || rows < 0 || rows > bt.max_block_len || s < 0 || rows > n - s || cub < 0 ||
-      rows > bt.total_block_rows - cub || (a.full_rows && (cus < 0 || n > bt.total_seq_rows - cus)) ||
-      (n + kPage - 1) / kPage > bt.max_pages) {
-    if (threadIdx.x == 0) report_error(bt.err, kErrBadShape);
-    return;
+
+  // ---- the line of tiles: its length, and where this CTA's piece begins
+  const int per = (bt.batch + kThreads - 1) / kThreads;
+  {
+    long long w = 0;
+    for (int b = tid * per; b < min(bt.batch, (tid + 1) * per); ++b) {
+      const Seq q = load_seq<NQ>(a, b);
+      if (q.bad && blockIdx.x == 0) report_error(bt.err, kErrBadShape);
+      w += seq_work<NQ>(a, q);
+    }
+    seg_sh[tid] = w;
   }
-  constexpr int kE = D / 32;
-  for (int r = warp; r < rows * G; r += kWarps) {
-    const int i = r / G, head = h * G + r % G;
-    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + (cub + i) * a.q_row + head * D;
-    __syncwarp();
-    for (int c = lane; c < D; c += 32) qs[warp][c] = __bfloat162float(q[c]) * a.scale_log2;
-    __syncwarp();
-    float m = attn::neg_inf(), l = 0.f, o[kE];
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  if (warp == 0) {
+    long long v[kThreads / 32], sum = 0;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] = 0.f;
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      const int pg = attn::page_of(bt, b, k0 / kPage);
-      const size_t slot = (static_cast<size_t>(pg) * a.kv.n_kv_heads + h) * kPage + k0 % kPage;
-      const size_t sc = (static_cast<size_t>(pg) * a.kv.n_kv_heads + h) * kKv8Groups + (k0 % kPage + lane) / kKv8Group;
-      const bool on = k0 + lane < n;
-      float x = attn::neg_inf(), vs = 0.f;
-      if (on) {
-        x = 0.f;
-        for (int c = 0; c < D; c += 2) {
-          const float2 kv = e4m3x2_f32(*reinterpret_cast<const uint16_t*>(a.kv.k + (slot + lane) * D + c));
-          x += kv.x * qs[warp][c] + kv.y * qs[warp][c + 1];
+    for (int i = 0; i < kThreads / 32; ++i) {
+      v[i] = sum;
+      sum += seg_sh[lane * (kThreads / 32) + i];
+    }
+    long long incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) seg_sh[lane * (kThreads / 32) + i] = v[i] + incl - sum;
+    if (lane == 31) seg_sh[kThreads] = incl;
+  }
+  __syncthreads();
+  const long long T = seg_sh[kThreads];
+  const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), T));  // pieces: at least a tile each
+  const int cta = blockIdx.x;
+  const long long lo = cta < n_cta ? cta * T / n_cta : 0, hi = cta < n_cta ? (cta + 1) * T / n_cta : 0;
+  if (lo < hi && seg_sh[tid] <= lo && lo < seg_sh[tid + 1]) {
+    long long at = seg_sh[tid];
+    int b = tid * per;
+    for (;; ++b) {
+      const long long w = seq_work<NQ>(a, load_seq<NQ>(a, b));
+      if (lo < at + w) break;
+      at += w;
+    }
+    start_b = b;
+    start_base = at;
+  }
+  __syncthreads();
+  Walk<NQ> walk(a, start_b, start_base, lo, hi);
+  const int G = a.n_heads / a.kv.n_kv_heads;
+
+  if (warp == kProducerWarp) {
+    // ------------------------------------------------------------ TMA producer
+    int slot = 0, phase = 0, issued = 0, nt = 0;
+    bool ok = true;
+    const uint64_t once = l2_evict_first_policy();
+    while (ok && walk.next()) {
+      const bool reread = walk.q.nqt > 1;  // other units read the same keys
+      const int32_t* row = bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages;
+      int ids = 0, first = -64;
+      for (int t = walk.t0; t < walk.t1 && ok; ++t, ++nt) {
+        if (2 * t - first >= 32) {  // the page ids of the next 16 tiles, one a lane
+          first = 2 * t;
+          const int p = first + lane;
+          ids = p < walk.q.npages ? __ldg(row + p) : 0;
+          if (ids < 0 || ids >= bt.num_pages) {
+            report_error(bt.err, kErrBadPage);
+            ids = 0;
+          }
         }
-        x *= a.kv.k_scale[sc];
-        vs = a.kv.v_scale[sc];
-      }
-      float mx = x;
-      for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-      const float mn = fmaxf(m, mx), alpha = attn::fast_exp2(m - mn), p = on ? exp2f(x - mn) : 0.f;
-      m = mn;
-      float ps = p;
-      for (int d = 16; d > 0; d >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, d);
-      l = l * alpha + ps;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) o[e] *= alpha;
-      const int keys = min(32, n - k0);
-      for (int j = 0; j < keys; ++j) {
-        const float w = __shfl_sync(0xffffffffu, p * vs, j);
-#pragma unroll
-        for (int e = 0; e < kE; e += 2) {
-          const float2 v = e4m3x2_f32(*reinterpret_cast<const uint16_t*>(a.kv.v + (slot + j) * D + lane * kE + e));
-          o[e] += w * v.x;
-          o[e + 1] += w * v.y;
+        const int pages = min(2, walk.q.npages - 2 * t);
+        const int id0 = __shfl_sync(0xffffffffu, ids, 2 * t - first), id1 = __shfl_sync(0xffffffffu, ids, 2 * t + 1 - first);
+        const size_t at[2] = {static_cast<size_t>(id0) * a.kv.n_kv_heads + walk.h,
+                              static_cast<size_t>(id1) * a.kv.n_kv_heads + walk.h};
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          if (issued >= C::kSlots) ok = __shfl_sync(0xffffffffu, lane == 0 ? mbar_wait(&empty_bar[slot], phase ^ 1) : true, 0);
+          if (!ok) {
+            if (lane == 0) report_error(bt.err, kErrTimeout);
+            break;
+          }
+          if (lane == 0) {
+            uint64_t* bar = &full_bar[slot];
+            uint8_t* dst = smem + slot * C::kSlotBytes;
+            uint64_t* const sbar = &scale_bar[nt % kScaleSlots];
+            mbar_arrive_expect_tx(bar, pages * (kPage * D));
+            if (kv == 0) mbar_arrive_expect_tx(sbar, pages * 32);
+            for (int p = 0; p < pages; ++p) {
+              const int y = static_cast<int>(at[p] * kPage);
+              if (reread)
+                tma_load_2d(dst + p * kPage * D, kv == 0 ? &tm_k : &tm_v, bar, 0, y);
+              else
+                tma_load_2d_hint(dst + p * kPage * D, kv == 0 ? &tm_k : &tm_v, bar, 0, y, once);
+              if (kv == 0) {
+                bulk_load(&scales[nt % kScaleSlots][0][4 * p], a.kv.k_scale + at[p] * kKv8Groups, 16, sbar);
+                bulk_load(&scales[nt % kScaleSlots][1][4 * p], a.kv.v_scale + at[p] * kKv8Groups, 16, sbar);
+              }
+            }
+          }
+          ++issued;
+          if (++slot == C::kSlots) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
     }
-    const size_t row = a.full_rows ? cus + s + i : cub + i;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + (row * a.n_heads + head) * D;
+    if (lane == 0) {  // every copy has landed and every slot's last release has arrived before the CTA ends
+      const int tiles = (issued + 1) / 2;
+      for (int i = max(0, tiles - kScaleSlots); i < tiles; ++i)
+        if (!mbar_wait(&scale_bar[i % kScaleSlots], (i / kScaleSlots) & 1)) report_error(bt.err, kErrTimeout);
+      for (int i = max(0, issued - C::kSlots); i < issued; ++i)
+        if (!mbar_wait(&full_bar[i % C::kSlots], (i / C::kSlots) & 1)) report_error(bt.err, kErrTimeout);
+      for (int i = max(0, issued - C::kSlots); ok && i < issued; ++i)
+        if (!mbar_wait(&empty_bar[i % C::kSlots], (i / C::kSlots) & 1)) report_error(bt.err, kErrTimeout);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_f8(kTile, NQ, false, false);
+      constexpr uint32_t kIdescO = idesc_f8(kTile, C::kOCols, true, true);
+      const uint32_t tm_o = tmem + 2 * NQ;
+      int nt = 0, unit = 0;
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, int parity) {
+        if (ok && !mbar_wait(bar, parity & 1)) {
+          report_error(bt.err, kErrTimeout);
+          ok = false;
+        }
+        return ok;
+      };
+      bool pending = false, fresh = false;  // a tile whose P V is still to be issued; the first of its unit
+      auto issue_pv = [&](int n) {          // tile number n of this CTA
+        const int i = 2 * n + 1, s = i % C::kSlots;
+        if (!wait(&p_ready, n) || !wait(&full_bar[s], i / C::kSlots)) return;
+        tc_fence_after();
+        const uint32_t v = ring + s * C::kSlotBytes;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) out[lane * kE + e] = __float2bfloat16(o[e] / l);
-    if (a.lse != nullptr && lane == 0) a.lse[row * a.n_heads + head] = (m + log2f(l)) * attn::kLn2;
+        for (int part = 0; part < (C::kWide ? 1 : 3); ++part)
+#pragma unroll
+          for (int k = 0; k < kTile / 32; ++k)
+            umma_e4m3(tm_o, desc_rows<D>(v + k * 32 * D),
+                      C::kWide ? desc_rows<128>(p_base + k * 32 * 128) : desc_rows<64>(p_base + part * kTile * 64 + k * 32 * 64),
+                      kIdescO, !fresh || part > 0 || k > 0);
+        umma_commit(&empty_bar[s]);
+        umma_commit(&pv_done);
+      };
+      while (ok && walk.next()) {
+        if (pending) {
+          issue_pv(nt - 1);
+          pending = false;
+        }
+        wait(&q_ready, unit);
+        for (int t = walk.t0; t < walk.t1 && ok; ++t, ++nt) {
+          const int i = 2 * nt, s = i % C::kSlots, buf = nt & 1;
+          if (!wait(&full_bar[s], i / C::kSlots)) break;
+          if (nt >= 2 && !wait(&s_free[buf], (nt >> 1) - 1)) break;
+          tc_fence_after();
+          const uint32_t k8 = ring + s * C::kSlotBytes;
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k)
+              umma_e4m3(tmem + buf * NQ, desc_rows<D>(k8 + k * 32), desc_rows<D>(q_base + part * NQ * D + k * 32), kIdescS,
+                        part > 0 || k > 0);
+          umma_commit(&empty_bar[s]);
+          umma_commit(&s_full[buf]);
+          if (pending) issue_pv(nt - 1);
+          pending = true;
+          fresh = t == walk.t0;
+        }
+        ++unit;
+      }
+      if (pending && ok) issue_pv(nt - 1);
+      // the softmax warps wait for the last S and P V, the producer for the releases; where a wait gave up, the
+      // products that were issued end before the CTA does
+      if (!ok) {
+        umma_commit(&drain_bar);
+        if (!mbar_wait(&drain_bar, 0)) report_error(bt.err, kErrTimeout);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tm_o = tmem + 2 * NQ + lane_base;
+    int nt = 0;
+    bool dead = false;
+    auto wait = [&](uint64_t* bar, int parity) {  // a thread that gave up waits for nothing more, but meets every barrier
+      if (!dead && !mbar_wait(bar, parity & 1)) {
+        report_error(bt.err, kErrTimeout);
+        dead = true;
+      }
+    };
+    while (walk.next()) {
+      const Seq& q = walk.q;
+      const int r0 = walk.qt * NQ, cols = min(NQ, q.rows * G - r0);  // rows of this unit
+      // ---- q: its largest magnitude, two e4m3 parts
+      float f_q;
+      {
+        constexpr int kPer = kSoft / NQ, kVec = D / 8 / kPer;  // threads and 16-byte pieces a row
+        const int c = tid / kPer, piece = (tid % kPer) * kVec, r = r0 + c;
+        uint4 x[kVec];
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (q.cub + r / G) * a.q_row +
+                                   static_cast<size_t>(walk.h * G + r % G) * D;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          x[i] = c < cols ? __ldg(reinterpret_cast<const uint4*>(src) + piece + i) : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // values that are not finite take no part
+            const uint32_t u = w[k] & 0x7fff7fffu;
+            m = max(m, (u & 0xffffu) < 0x7f80u ? u & 0xffffu : 0u);
+            m = max(m, (u >> 16) < 0x7f80u ? u >> 16 : 0u);
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) amax_sh[warp] = __uint_as_float(m << 16);
+        soft_sync();  // (and the last unit's readers of the arrays below are done)
+        const float amax = fmaxf(fmaxf(amax_sh[0], amax_sh[1]), fmaxf(amax_sh[2], amax_sh[3]));
+        // 2^e with amax 2^-e in (224, 448]; 448 = 1.75 2^8
+        const uint32_t bits = __float_as_uint(amax);
+        int e = static_cast<int>(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
+        e = max(e, -118);
+        const float down = __int_as_float((127 - e) << 23);
+        f_q = a.scale_log2 * __int_as_float((127 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < kVec; i += 1) {
+          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          uint32_t hi2[2], lo2[2];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float v[2] = {__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)};
+            float d2[2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              d2[z] = v[z] * down;
+              if (!(fabsf(v[z]) < INFINITY)) d2[z] = __int_as_float(0x7fffffff);  // not a number in its row alone
+            }
+            const uint16_t hc = cvt_e4m3x2(d2[0], d2[1]);
+            uint32_t h16;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(hc));
+            const float2 hf = __half22float2(*reinterpret_cast<__half2*>(&h16));
+            const uint16_t lc = cvt_e4m3x2(d2[0] - hf.x, d2[1] - hf.y);
+            if (k & 1) {
+              hi2[k >> 1] |= static_cast<uint32_t>(hc) << 16;
+              lo2[k >> 1] |= static_cast<uint32_t>(lc) << 16;
+            } else {
+              hi2[k >> 1] = hc;
+              lo2[k >> 1] = lc;
+            }
+          }
+          const int byte = (piece + i) * 8;  // eight codes of row c
+          const uint32_t at = q_base + swz<D>(c, byte >> 4) + (byte & 8);
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi2[0]), "r"(hi2[1]) : "memory");
+          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + NQ * D), "r"(lo2[0]), "r"(lo2[1]) : "memory");
+        }
+        fence_async_smem();
+        mbar_arrive(&q_ready);
+        if (tid < NQ) {
+          const int rr = r0 + tid, i = rr / G;
+          const long long row = a.full_rows ? static_cast<long long>(q.cus) + q.s + i : q.cub + i;
+          row_sh[tid] = tid < cols ? (row * a.n_heads + walk.h * G + rr % G) : -1;
+          ref_sh[tid] = 0.f;
+        }
+      }
+      float l[NQ];
+#pragma unroll
+      for (int c = 0; c < NQ; ++c) l[c] = 0.f;
+
+      for (int t = walk.t0; t < walk.t1; ++t, ++nt) {
+        const int buf = nt & 1, si = 2 * nt;
+        const bool first = t == walk.t0;
+        const int valid = q.n - t * kTile;  // keys of this tile that there are
+        wait(&scale_bar[nt % kScaleSlots], nt / kScaleSlots);
+        const float sv = tid < valid ? scales[nt % kScaleSlots][1][tid / kKv8Group] : 0.f;
+        const float f = tid < valid ? scales[nt % kScaleSlots][0][tid / kKv8Group] * f_q : 0.f;
+        const float lv = sv > 0.f ? log2f(sv) : attn::neg_inf();
+        wait(&s_full[buf], nt >> 1);
+        tc_fence_after();
+        float x[NQ];
+        auto scores = [&]() {  // x = f S - R
+#pragma unroll
+          for (int c0 = 0; c0 < NQ; c0 += 32) {
+            float s[32];
+            tmem_ld_32x32b_x32(tmem + lane_base + buf * NQ + c0, s);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c0 + c] = fmaf(s[c], f, -ref_sh[c0 + c]);
+          }
+          if (tid >= valid) {
+#pragma unroll
+            for (int c = 0; c < NQ; ++c) x[c] = attn::neg_inf();
+          }
+        };
+        bool raise = first;
+        if (first) soft_sync();  // ref_sh is set
+        scores();
+        if (!first) {
+          float xm = attn::neg_inf();
+#pragma unroll
+          for (int c = 0; c < NQ; ++c) xm = fmaxf(xm, x[c]);
+          raise = soft_any(xm + lv > kLimit);
+        }
+        if (raise) {
+          // the largest weight x value scale of each row in this tile
+#pragma unroll
+          for (int c0 = 0; c0 < NQ; c0 += 32) {
+            float u[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) u[c] = x[c0 + c] + lv;
+            const float m = reduce_transposed(u, lane, [](float p, float r) { return fmaxf(p, r); });
+            red_sh[warp][c0 + lane] = m;
+          }
+          soft_sync();
+          if (tid < NQ) {
+            const float m = fmaxf(fmaxf(red_sh[0][tid], red_sh[1][tid]), fmaxf(red_sh[2][tid], red_sh[3][tid]));
+            float up = 0.f;  // what R grows by
+            if ((first || m > kLimit) && fabsf(m) < INFINITY) up = m - kTop;
+            ref_sh[tid] += up;
+            alpha_sh[tid] = first ? 0.f : exp2f(-up);
+          }
+          if (!first) wait(&pv_done, nt - 1);
+          soft_sync();
+          if (!first) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < NQ; ++c) l[c] *= alpha_sh[c];
+#pragma unroll
+            for (int c0 = 0; c0 < C::kOCols; c0 += 32) {
+              float o[32];
+              tmem_ld_32x32b_x32(tm_o + c0, o);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) o[c] *= alpha_sh[(c0 + c) % NQ];
+              tmem_st_32x32b_x32(tm_o + c0, o);
+            }
+            tmem_st_wait();
+          }
+          scores();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[buf]);  // the scores are in registers
+#pragma unroll
+        for (int c = 0; c < NQ; ++c) {
+          const float p = attn::fast_exp2(x[c]);
+          l[c] += p;
+          x[c] = p * sv;
+        }
+        if (nt > 0) wait(&pv_done, nt - 1);  // P's buffer is free
+        if (valid < kTile) {                  // what lies behind the end must not meet a weight, not even 0
+          const int vi = si + 1;
+          wait(&full_bar[vi % C::kSlots], vi / C::kSlots);
+          if (tid >= valid) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) st_shared_v4(ring + (vi % C::kSlots) * C::kSlotBytes + tid * D + i * 16, 0, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < NQ; c0 += 16) {
+          uint32_t part[3][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[3][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t h = pack_f16x2(x[c0 + 4 * j + 2 * k], x[c0 + 4 * j + 2 * k + 1]);
+              // e5m2 is fp16's upper byte: round to it by adding half of the lower one
+              const uint32_t hi8 = (h + 0x00800080u) & 0xff00ff00u;
+              const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&hi8));
+              const uint32_t rb = *reinterpret_cast<const uint32_t*>(&r);
+              const uint32_t mid8 = (rb + 0x00800080u) & 0xff00ff00u;
+              const __half2 z = __hsub2(r, *reinterpret_cast<const __half2*>(&mid8));
+              w[0][k] = hi8;
+              w[1][k] = mid8;
+              w[2][k] = *reinterpret_cast<const uint32_t*>(&z) + 0x00800080u;
+            }
+#pragma unroll
+            for (int z = 0; z < 3; ++z) part[z][j] = __byte_perm(w[z][0], w[z][1], 0x7531);
+          }
+#pragma unroll
+          for (int z = 0; z < 3; ++z) {
+            const uint32_t at = C::kWide ? p_base + swz<128>(tid, z * 2 + c0 / 16) : p_base + z * kTile * 64 + swz<64>(tid, c0 / 16);
+            st_shared_v4(at, part[z][0], part[z][1], part[z][2], part[z][3]);
+          }
+        }
+        tc_fence_before();
+        fence_async_smem();
+        mbar_arrive(&p_ready);
+      }
+
+      // ---- the end of this part of the unit
+#pragma unroll
+      for (int c0 = 0; c0 < NQ; c0 += 32) {
+        float u[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) u[c] = l[c0 + c];
+        red_sh[warp][c0 + lane] = reduce_transposed(u, lane, [](float p, float r) { return p + r; });
+      }
+      wait(&pv_done, nt - 1);
+      soft_sync();
+      tc_fence_after();
+      if (tid < NQ) l_sh[tid] = (red_sh[0][tid] + red_sh[1][tid]) + (red_sh[2][tid] + red_sh[3][tid]);
+      soft_sync();
+      auto load_o = [&](int c0, float (&o)[32]) {  // columns c0 .. c0 + 32 of O^T, this thread's lane
+        tmem_ld_32x32b_x32(tm_o + c0, o);
+        if (C::kWide) {
+          float o2[32];
+          tmem_ld_32x32b_x32(tm_o + NQ + c0, o2);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] += o2[c];
+          tmem_ld_32x32b_x32(tm_o + 2 * NQ + c0, o2);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) o[c] += o2[c];
+        }
+      };
+      __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o);
+      if (walk.t0 == 0 && walk.t1 == q.tiles) {
+        if (a.lse != nullptr && tid < cols) a.lse[row_sh[tid]] = (ref_sh[tid] + log2f(l_sh[tid])) * attn::kLn2;
+#pragma unroll
+        for (int c0 = 0; c0 < NQ; c0 += 32) {
+          float o[32];
+          load_o(c0, o);
+          if (tid < D) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c0 + c < cols) out[row_sh[c0 + c] * D + tid] = __float2bfloat16(o[c] / l_sh[c0 + c]);
+          }
+        }
+        continue;
+      }
+      // ---- a piece: (O, R, l) to the workspace; the last of the unit's CTAs joins them
+      float* const parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kCounterBytes);
+      const int c_first = static_cast<int>(((walk.u0 + 1) * n_cta - 1) / T);
+      const int c_last = static_cast<int>(((walk.u0 + q.tiles) * n_cta - 1) / T);
+      auto part_of = [&](int c) { return parts + (static_cast<size_t>(c) * 2 + (c == c_first ? 1 : 0)) * C::kPartFloats; };
+      {
+        float* const mine = part_of(cta);
+#pragma unroll
+        for (int c0 = 0; c0 < NQ; c0 += 32) {
+          float o[32];
+          load_o(c0, o);
+          if (tid < D) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c0 + c < cols) __stcg(mine + (c0 + c) * D + tid, o[c]);
+          }
+        }
+        if (tid < cols) {
+          __stcg(mine + NQ * D + tid, ref_sh[tid]);
+          __stcg(mine + NQ * D + NQ + tid, l_sh[tid]);
+        }
+      }
+      __threadfence();
+      soft_sync();
+      if (tid == 0) {
+        int32_t* const counter = static_cast<int32_t*>(a.ws) + c_first;
+        const int before = atomicAdd(counter, 1);
+        last_sh = before == c_last - c_first;
+        if (last_sh) *counter = 0;
+        __threadfence();
+      }
+      soft_sync();
+      if (!last_sh) continue;
+      __threadfence();
+      // per row: the largest R, the sum of l in it, and (in red_sh, per piece) the weight of each piece
+      float top = attn::neg_inf(), total = 0.f;
+      if (tid < cols) {
+        for (int c = c_first; c <= c_last; ++c) {
+          const float r = __ldcg(part_of(c) + NQ * D + tid), lp = __ldcg(part_of(c) + NQ * D + NQ + tid);
+          const float now = fmaxf(top, r);
+          total = total * exp2f(top - now) + lp * exp2f(r - now);
+          top = now;
+        }
+        l_sh[tid] = total;
+        ref_sh[tid] = top;
+        if (a.lse != nullptr) a.lse[row_sh[tid]] = (top + log2f(total)) * attn::kLn2;
+      }
+      soft_sync();
+      for (int c0 = 0; c0 < cols; c0 += 32) {
+        float o[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) o[c] = 0.f;
+        for (int p = c_first; p <= c_last; ++p) {
+          const float* const from = part_of(p);
+          soft_sync();  // alpha_sh of the last piece has been read
+          if (tid < 32 && c0 + tid < cols) alpha_sh[tid] = exp2f(__ldcg(from + NQ * D + c0 + tid) - ref_sh[c0 + tid]);
+          soft_sync();
+          if (tid < D) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c0 + c < cols) o[c] = fmaf(__ldcg(from + (c0 + c) * D + tid), alpha_sh[c], o[c]);
+          }
+        }
+        if (tid < D) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c < cols) out[row_sh[c0 + c] * D + tid] = __float2bfloat16(o[c] / l_sh[c0 + c]);
+        }
+      }
+      soft_sync();
+    }
   }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D>
+cudaError_t encode_codes(CUtensorMap* map, const void* ptr, uint64_t rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {D, rows};
+  cuuint64_t strides[1] = {D};
+  cuuint32_t box[2] = {D, kPage};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+int grid_of(int num_sms) { return std::min(kCtasPerSm * num_sms, static_cast<int>(kCounterBytes / 4)); }
+
+template <int D, int NQ>
+cudaError_t launch(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
+  using C = Cfg<D, NQ>;
+  CUtensorMap tk, tv;
+  const uint64_t rows = static_cast<uint64_t>(a.bt.num_pages) * a.kv.n_kv_heads * kPage;
+  cudaError_t e = encode_codes<D>(&tk, a.kv.k, rows);
+  if (e == cudaSuccess) e = encode_codes<D>(&tv, a.kv.v, rows);
+  if (e == cudaSuccess) e = attn::set_smem(kv8_attn_kernel<D, NQ>, C::kDynSmem);
+  if (e != cudaSuccess) return e;
+  return attn::launch_pdl(kv8_attn_kernel<D, NQ>, dim3(grid_of(num_sms)), kThreads, C::kDynSmem, 0, stream, tk, tv, a);
+}
+
+// Rows that share a key head: up to 32 in one tile of 32, more in tiles of 64.
+bool narrow(int max_block_len, int n_heads, int n_kv_heads) {
+  return static_cast<int64_t>(max_block_len) * (n_heads / n_kv_heads) <= 32;
 }
 
 }  // namespace
 
-size_t kv8_attention_workspace_bytes(int, int, int, int, int) { return 4096; }
+size_t kv8_attention_workspace_bytes(int max_block_len, int n_heads, int n_kv_heads, int head_dim, int num_sms) {
+  const size_t nq = narrow(max_block_len, n_heads, n_kv_heads) ? 32 : 64;
+  return kCounterBytes + static_cast<size_t>(grid_of(num_sms)) * 2 * (nq * head_dim + 2 * nq) * sizeof(float);
+}
 
-cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, int, cudaStream_t stream) {
-  const dim3 grid(a.bt.batch, a.kv.n_kv_heads);
-  if (a.head_dim == 128) return attn::launch_pdl(kv8_attn_kernel<128>, grid, kWarps * 32, 0, 0, stream, a);
-  return attn::launch_pdl(kv8_attn_kernel<64>, grid, kWarps * 32, 0, 0, stream, a);
+cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
+  const bool n32 = narrow(a.bt.max_block_len, a.n_heads, a.kv.n_kv_heads);
+  if (a.head_dim == 128) return n32 ? launch<128, 32>(a, num_sms, stream) : launch<128, 64>(a, num_sms, stream);
+  return n32 ? launch<64, 32>(a, num_sms, stream) : launch<64, 64>(a, num_sms, stream);
 }
 
 }  // namespace dllm

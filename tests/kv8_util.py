@@ -78,13 +78,15 @@ def values(codes, scale):
 
 
 def attention(b: Batch, q, kv8, scale=None):
-    """float64 (o, lse, a): packed rows of the attention, the log-sum-exp, and the attention of |v| (what the rounding of the
-    weights is relative to); and the largest possible change of a score when q changes by 1."""
+    """float64 packed rows: the attention, the log-sum-exp, the attention of |v| (what the rounding of the weights is
+    relative to), the largest possible change of a score when q changes by 1, and the largest weight x value scale of
+    the row times the sum of |code| (what the weights' smallest step is relative to)."""
     H, d = q.shape[1], q.shape[2]
     kv = kv8.k.shape[1]
     scale = d ** -0.5 if scale is None else scale
     o = torch.zeros(b.M, H, d, dtype=torch.float64, device="cuda")
     a, lse = torch.zeros_like(o), torch.zeros(b.M, H, dtype=torch.float64, device="cuda")
+    small = torch.zeros_like(o)
     reach = torch.zeros(b.M, H, dtype=torch.float64, device="cuda")
     at = 0
     for i, (n, rows) in enumerate(zip(b.n, b.rows)):
@@ -103,22 +105,26 @@ def attention(b: Batch, q, kv8, scale=None):
         o[at:at + rows] = torch.einsum("hin,hnd->ihd", p, v)
         a[at:at + rows] = torch.einsum("hin,hnd->ihd", p, v.abs())
         lse[at:at + rows] = (m + torch.log(tot))[..., 0].T
+        vs = kv8.v_scale[ids].double().repeat_interleave(G, 2).transpose(0, 1).reshape(kv, -1)[:, :n].repeat_interleave(rep, 0)
+        most = (p * vs[:, None]).amax(-1)  # [H][rows]
+        small[at:at + rows] = torch.einsum("hi,hd->ihd", most, (v / vs[..., None]).abs().sum(1))
         reach[at:at + rows] = k.abs().sum(-1).amax(-1)[None] * scale
         at += rows
-    return o, lse, a, reach
+    return o, lse, a, reach, small
 
 
 def assert_attention(b, q, kv8, o, lse, scale=None, ref=None):
     """Bounds: the output is rounded to bf16 once (half a step: 2^-8 of the value).  The weights are rounded to 11 bits
-    (2^-11 of each, so 2^-11 of the attention of |v|), and as much again covers the rest: weights below 2^-27 of the
-    largest, 2^-22 of each exponential, 32-bit sums and a score's error e = 2^-19 max|q| sum|k| (q is held in two
-    8-bit parts: exact but for what is below 2^-11 of the row group's largest, and off by at most 2^-19 of that),
-    which moves a weight by a factor of exp(2 e) at most."""
-    o64, lse64, a64, reach = ref if ref is not None else attention(b, q, kv8, scale)
+    (2^-11 of each, so 2^-11 of the attention of |v|), and as much again covers 2^-22 of each exponential, 32-bit sums
+    and a score's error e = 2^-19 max|q| sum|k| (q is held in two 8-bit parts: exact but for what is below 2^-11 of the
+    row group's largest, and off by at most 2^-19 of that), which moves a weight by a factor of exp(2 e) at most.
+    A weight x value scale is held to an absolute 2^-17 besides (half of the smallest e5m2 step) in units in which the
+    row's largest is 2^12 or more: 2^-29 of that largest for each key, times |code|, summed over the keys."""
+    o64, lse64, a64, reach, small = ref if ref is not None else attention(b, q, kv8, scale)
     rows = sum(b.rows)
     e = 2.0 ** -19 * q.double().abs().max() * reach[:rows]
     got = o[:rows].double()
-    tol = 2.0 ** -8 * o64[:rows].abs() + (2.0 ** -10 + 2 * e)[..., None] * a64[:rows] + 1e-30
+    tol = 2.0 ** -8 * o64[:rows].abs() + (2.0 ** -10 + 2 * e)[..., None] * a64[:rows] + 2.0 ** -29 * small[:rows]
     bad = ~((got - o64[:rows]).abs() <= tol)
     assert not bad.any(), (int(bad.sum()), bad.nonzero()[0].tolist(), float(got[bad][0]), float(o64[:rows][bad][0]))
     if lse is not None:
