@@ -20,20 +20,22 @@
 // its weight before the split; the sum l takes the weight without it.
 //
 // The thread that holds a key's scores has its scales as two scalars; a row's
-// reference R is the same for all 128 threads.  R is set from a unit's first tile (so
+// reference R is the same for all 128 keys.  R is set from a unit's first tile (so
 // that the largest weight x value scale is 2^12) and raised only when one passes 2^15:
 // a vote per tile, and otherwise no reduction over keys at all until the unit's end,
 // where the 128 partial sums of each row are added.
 //
-// Roles of a CTA's six warps: 0-3 softmax (TMEM lane = key, then = column of O^T),
-// 4 TMA producer, 5 MMA issuer.  K and V tiles share one ring of 16 KB slots (8 KB for
+// Roles of a CTA's warps: groups of four softmax warps (TMEM lane = key, then = column of
+// O^T; 16 rows to a group), one TMA producer, one MMA issuer.  K and V tiles share one ring of 16 KB slots (8 KB for
 // d = 64); the scores are double-buffered in TMEM, so the tensor core runs S of the next
 // tile while the softmax works.  Two CTAs an SM cover each other's serial parts.
 //
 // Split: the tiles of all units form one line, cut into as many equal pieces as CTAs
 // (or fewer, where there are few tiles): a ragged batch or one long sequence loads all
-// SMs alike.  A unit cut by a border is joined from its pieces' (O, R, l) in the
-// workspace by the CTA that finishes last, in the order of the keys.
+// SMs alike.  A unit cut by a border leaves its pieces' (O, R, l) in the workspace, and a
+// second, small kernel joins them in the order of the keys, a warp for each row: with the
+// ring full, every dependent trip to memory (fence, counter, reads) costs the attention's
+// warps several microseconds, which a join inside the kernel had to wait for.
 #include <algorithm>
 
 #include "attn_common.cuh"
@@ -42,33 +44,39 @@
 namespace dllm {
 namespace {
 
-constexpr int kSoftWarps = 4;
-constexpr int kSoft = kSoftWarps * 32;
-constexpr int kProducerWarp = 4, kMmaWarp = 5;
-constexpr int kThreads = 192;
 constexpr int kTile = 128;  // keys per tile: two pages
 constexpr int kCtasPerSm = 2;
 constexpr uint32_t kTmemCols = 256;  // of a CTA: two fit an SM's 512
 constexpr int kScaleSlots = 8;       // tiles whose scales are in shared memory
-constexpr size_t kCounterBytes = 4096;
+constexpr int kMaxCtas = 1024;       // of a launch (records of the workspace)
+constexpr size_t kRecordBytes = kMaxCtas * sizeof(int2);
+constexpr int kScan = 128;           // threads that sum up the batch's work
+constexpr int kCols = 16;            // rows of the unit (columns of S^T) a softmax thread holds
 constexpr float kTop = 12.f;    // log2 of a row's largest weight x value scale when R is set
 constexpr float kLimit = 15.f;  // and where it is raised
 
+// NQ rows to a unit, handled by NQ / 16 groups of four softmax warps (a thread: one key, 16 rows).
 template <int D, int NQ>
 struct Cfg {
+  static constexpr int kGroups = NQ / kCols;
+  static constexpr int kSoft = 128 * kGroups;  // softmax threads
+  static constexpr int kProducerWarp = 4 * kGroups, kMmaWarp = kProducerWarp + 1;
+  static constexpr int kThreads = kSoft + 64;
   static constexpr int kSlotBytes = kTile * D;
-  static constexpr int kQBytes = NQ * D * 2;           // hi, lo
-  static constexpr bool kWide = NQ == 32;              // the three parts side by side in one 128-byte row
-  static constexpr int kPBytes = kWide ? kTile * 128 : 3 * kTile * 64;
-  static constexpr int kOCols = kWide ? 3 * NQ : NQ;   // TMEM columns of O
-  static constexpr int kBudget = 113 * 1024 - 1024 - 5120;  // two CTAs an SM: alignment slack, static shared memory
+  static constexpr int kQBytes = NQ * D * 2;                  // hi, lo
+  static constexpr bool kWide = NQ <= 32;                     // the three parts side by side in one row
+  static constexpr int kPRow = NQ == 32 ? 128 : 64;           // bytes of a row of P^T
+  static constexpr int kPBytes = kTile * kPRow * (kWide ? 1 : 3);
+  static constexpr int kOCols = kWide ? 3 * NQ : NQ;          // TMEM columns of O
+  static constexpr int kStatic = NQ == 64 ? 4608 : 3584;      // static shared memory, at most
+  static constexpr int kBudget = 113 * 1024 - 1024 - kStatic;  // two CTAs an SM; 1 KB to align
   static constexpr int kSlots0 = (kBudget - kQBytes - kPBytes) / kSlotBytes;
   static constexpr int kSlots = kSlots0 > 10 ? 10 : kSlots0;
   static constexpr int kDynSmem = kSlots * kSlotBytes + kQBytes + kPBytes + 1024;
   static_assert(kSlots >= 4, "a tile's K and V, and the next tile's");
   static_assert(kSlots / 2 + 2 < kScaleSlots, "scales stay until the softmax has read them");
   static_assert(2 * NQ + kOCols <= static_cast<int>(kTmemCols), "TMEM columns");
-  static constexpr size_t kPartFloats = static_cast<size_t>(NQ) * D + 2 * NQ;  // O, R, l
+  static constexpr size_t kPartFloats = static_cast<size_t>(NQ) * (D + 4);  // O, R, l, rows
 };
 
 // ------------------------------------------------------------ descriptors
@@ -98,25 +106,59 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// Barrier of the softmax warps that ORs a predicate over their threads.
+// Barrier of the softmax warps (N threads) that ORs a predicate over them, and the plain one.
+template <int N>
 __device__ __forceinline__ bool soft_any(bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
       "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "n"(kSoft)
+      : "r"(static_cast<uint32_t>(v)), "n"(N)
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void soft_sync() { named_barrier(1, kSoft); }
 
-// Reduce 32 values over the warp's lanes: lane i gets the result of v[i] (31 shuffles; v is destroyed).
+// Pairs of fp32 (one instruction for both).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Reduce 16 values over the warp's lanes: lanes i and i + 16 get the result of v[i] (v is destroyed).
 template <class Op>
-__device__ __forceinline__ float reduce_transposed(float (&v)[32], int lane, Op op) {
+__device__ __forceinline__ float reduce_transposed(float (&v)[kCols], int lane, Op op) {
 #pragma unroll
-  for (int w = 16; w > 0; w >>= 1) {
+  for (int w = kCols / 2; w > 0; w >>= 1) {
     const bool up = (lane & w) != 0;
 #pragma unroll
     for (int i = 0; i < w; ++i) {
@@ -124,10 +166,13 @@ __device__ __forceinline__ float reduce_transposed(float (&v)[32], int lane, Op 
       v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, w));
     }
   }
-  return v[0];
+  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
 // ------------------------------------------------------------ work
+// The workspace: for each CTA the record (pieces, rows) of the unit that begins in it and goes on in the next, (0, -) if
+// none does; then two parts for each CTA: of the unit that began before it, and of the one that goes on after it.
+
 struct Seq {
   int n, s, rows, cub, cus;
   int npages, tiles, nqt;  // tiles = 0: nothing to do
@@ -171,10 +216,8 @@ struct Walk {
   // the current part of a unit: tiles [t0, t1) of (b, h, qt), which lies at u0 on the line
   int h, qt, t0, t1;
   long long u0;
-  __device__ Walk(const Kv8AttnArgs& args, int b0, long long base0, long long lo, long long hi0)
-      : a(args), base(base0), pos(lo), hi(hi0), b(b0) {
-    if (pos < hi) q = load_seq<NQ>(a, b);
-  }
+  __device__ Walk(const Kv8AttnArgs& args, int b0, const Seq& q0, long long base0, long long lo, long long hi0)
+      : a(args), base(base0), pos(lo), hi(hi0), b(b0), q(q0) {}
   __device__ bool next() {
     if (pos >= hi) return false;
     long long w = seq_work<NQ>(a, q);
@@ -196,7 +239,7 @@ struct Walk {
 
 // ------------------------------------------------------------ the kernel
 template <int D, int NQ>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const Kv8AttnArgs a) {
   using C = Cfg<D, NQ>;
@@ -208,12 +251,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   __shared__ uint64_t scale_bar[kScaleSlots], drain_bar;
   __shared__ uint32_t tmem_sh;
   __shared__ __align__(16) float scales[kScaleSlots][2][8];  // K, V: two pages of four groups
-  __shared__ float ref_sh[NQ], alpha_sh[NQ], red_sh[kSoftWarps][NQ], l_sh[NQ];
-  __shared__ long long row_sh[NQ];  // element offset of a row's output, -1 for none
-  __shared__ float amax_sh[kSoftWarps];
-  __shared__ long long seg_sh[kThreads + 1];
+  // of each row: -R; what the sums so far are multiplied by where R is raised; the sum l and 1 / l
+  __shared__ __align__(16) float nref_sh[NQ], alpha_sh[NQ], l_sh[NQ], inv_sh[NQ];
+  __shared__ float red_sh[4][NQ];
+  __shared__ long long row_sh[NQ];  // row x head of the output
+  __shared__ float amax_sh[4 * C::kGroups];
+  __shared__ long long seg_sh[kScan + 1];
   __shared__ long long start_base;
-  __shared__ int start_b, last_sh;
+  __shared__ int start_b;
+  __shared__ Seq start_q;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const BatchArgs& bt = a.bt;
@@ -224,27 +270,29 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], kSoftWarps);
+      mbar_init(&s_free[i], 4 * C::kGroups);
     }
     for (int i = 0; i < kScaleSlots; ++i) mbar_init(&scale_bar[i], 1);
     mbar_init(&drain_bar, 1);
-    mbar_init(&p_ready, kSoft);
+    mbar_init(&p_ready, C::kSoft);
     mbar_init(&pv_done, 1);
-    mbar_init(&q_ready, kSoft);
+    mbar_init(&q_ready, C::kSoft);
     fence_barrier_init();
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (warp == kMmaWarp) tmem_alloc(&tmem_sh, kTmemCols);
+  if (warp == C::kMmaWarp) tmem_alloc(&tmem_sh, kTmemCols);
   griddep_wait();
   griddep_launch_dependents();
 
   // ---- the line of tiles: its length, and where this CTA's piece begins
-  const int per = (bt.batch + kThreads - 1) / kThreads;
-  {
+  const int per = (bt.batch + kScan - 1) / kScan;
+  Seq q0;  // the thread's only sequence, where it has but one
+  if (tid < kScan) {
     long long w = 0;
     for (int b = tid * per; b < min(bt.batch, (tid + 1) * per); ++b) {
       const Seq q = load_seq<NQ>(a, b);
+      q0 = q;
       if (q.bad && blockIdx.x == 0) report_error(bt.err, kErrBadShape);
       w += seq_work<NQ>(a, q);
     }
@@ -255,11 +303,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
   if (warp == 0) {
-    long long v[kThreads / 32], sum = 0;
+    constexpr int kEach = kScan / 32;
+    long long v[kEach], sum = 0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
+    for (int i = 0; i < kEach; ++i) {
       v[i] = sum;
-      sum += seg_sh[lane * (kThreads / 32) + i];
+      sum += seg_sh[lane * kEach + i];
     }
     long long incl = sum;
 #pragma unroll
@@ -269,99 +318,139 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) seg_sh[lane * (kThreads / 32) + i] = v[i] + incl - sum;
-    if (lane == 31) seg_sh[kThreads] = incl;
+    for (int i = 0; i < kEach; ++i) seg_sh[lane * kEach + i] = v[i] + incl - sum;
+    if (lane == 31) seg_sh[kScan] = incl;
   }
   __syncthreads();
-  const long long T = seg_sh[kThreads];
+  const long long T = seg_sh[kScan];
   const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), T));  // pieces: at least a tile each
   const int cta = blockIdx.x;
   const long long lo = cta < n_cta ? cta * T / n_cta : 0, hi = cta < n_cta ? (cta + 1) * T / n_cta : 0;
-  if (lo < hi && seg_sh[tid] <= lo && lo < seg_sh[tid + 1]) {
+  if (tid < kScan && lo < hi && seg_sh[tid] <= lo && lo < seg_sh[tid + 1]) {
     long long at = seg_sh[tid];
     int b = tid * per;
-    for (;; ++b) {
-      const long long w = seq_work<NQ>(a, load_seq<NQ>(a, b));
+    for (; per > 1; ++b) {
+      q0 = load_seq<NQ>(a, b);
+      const long long w = seq_work<NQ>(a, q0);
       if (lo < at + w) break;
       at += w;
     }
     start_b = b;
+    start_q = q0;
     start_base = at;
   }
   __syncthreads();
-  Walk<NQ> walk(a, start_b, start_base, lo, hi);
+  Walk<NQ> walk(a, start_b, start_q, start_base, lo, hi);
+  const int n_tiles = static_cast<int>(hi - lo);
+  // the ring's order: K of the next tile before V of this one, which is needed later
+  auto k_index = [](int n) { return n == 0 ? 0 : 2 * n - 1; };
+  auto v_index = [n_tiles](int n) { return n + 1 < n_tiles ? 2 * n + 2 : 2 * n + 1; };
   const int G = a.n_heads / a.kv.n_kv_heads;
 
-  if (warp == kProducerWarp) {
+  if (warp == C::kProducerWarp) {
     // ------------------------------------------------------------ TMA producer
     int slot = 0, phase = 0, issued = 0, nt = 0;
     bool ok = true;
     const uint64_t once = l2_evict_first_policy();
-    while (ok && walk.next()) {
-      const bool reread = walk.q.nqt > 1;  // other units read the same keys
-      const int32_t* row = bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages;
-      int ids = 0, first = -64;
-      for (int t = walk.t0; t < walk.t1 && ok; ++t, ++nt) {
-        if (2 * t - first >= 32) {  // the page ids of the next 16 tiles, one a lane
-          first = 2 * t;
-          const int p = first + lane;
-          ids = p < walk.q.npages ? __ldg(row + p) : 0;
-          if (ids < 0 || ids >= bt.num_pages) {
-            report_error(bt.err, kErrBadPage);
-            ids = 0;
-          }
+    auto page_ids = [&](const int32_t* row, int first, int npages) {  // of 16 tiles, one a lane (checked where used)
+      const int p = first + lane;
+      return p < npages ? __ldg(row + p) : 0;
+    };
+    struct Src {  // one tile of a pool
+      size_t at[2];
+      int pages;
+      bool reread;  // other units read the same keys
+    };
+    auto load = [&](const CUtensorMap* map, const Src& src, bool is_k) {
+      if (issued >= C::kSlots) ok = __shfl_sync(0xffffffffu, lane == 0 ? mbar_wait(&empty_bar[slot], phase ^ 1) : true, 0);
+      if (!ok) {
+        if (lane == 0) report_error(bt.err, kErrTimeout);
+        return;
+      }
+      if (lane == 0) {
+        uint64_t* const bar = &full_bar[slot];
+        uint8_t* const dst = smem + slot * C::kSlotBytes;
+        mbar_arrive_expect_tx(bar, src.pages * (kPage * D));
+        for (int p = 0; p < src.pages; ++p) {
+          const int y = static_cast<int>(src.at[p] * kPage);
+          if (src.reread)
+            tma_load_2d(dst + p * kPage * D, map, bar, 0, y);
+          else
+            tma_load_2d_hint(dst + p * kPage * D, map, bar, 0, y, once);
         }
-        const int pages = min(2, walk.q.npages - 2 * t);
-        const int id0 = __shfl_sync(0xffffffffu, ids, 2 * t - first), id1 = __shfl_sync(0xffffffffu, ids, 2 * t + 1 - first);
-        const size_t at[2] = {static_cast<size_t>(id0) * a.kv.n_kv_heads + walk.h,
-                              static_cast<size_t>(id1) * a.kv.n_kv_heads + walk.h};
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          if (issued >= C::kSlots) ok = __shfl_sync(0xffffffffu, lane == 0 ? mbar_wait(&empty_bar[slot], phase ^ 1) : true, 0);
-          if (!ok) {
-            if (lane == 0) report_error(bt.err, kErrTimeout);
-            break;
-          }
-          if (lane == 0) {
-            uint64_t* bar = &full_bar[slot];
-            uint8_t* dst = smem + slot * C::kSlotBytes;
-            uint64_t* const sbar = &scale_bar[nt % kScaleSlots];
-            mbar_arrive_expect_tx(bar, pages * (kPage * D));
-            if (kv == 0) mbar_arrive_expect_tx(sbar, pages * 32);
-            for (int p = 0; p < pages; ++p) {
-              const int y = static_cast<int>(at[p] * kPage);
-              if (reread)
-                tma_load_2d(dst + p * kPage * D, kv == 0 ? &tm_k : &tm_v, bar, 0, y);
-              else
-                tma_load_2d_hint(dst + p * kPage * D, kv == 0 ? &tm_k : &tm_v, bar, 0, y, once);
-              if (kv == 0) {
-                bulk_load(&scales[nt % kScaleSlots][0][4 * p], a.kv.k_scale + at[p] * kKv8Groups, 16, sbar);
-                bulk_load(&scales[nt % kScaleSlots][1][4 * p], a.kv.v_scale + at[p] * kKv8Groups, 16, sbar);
-              }
-            }
-          }
-          ++issued;
-          if (++slot == C::kSlots) {
-            slot = 0;
-            phase ^= 1;
+        if (is_k) {
+          const int z = nt % kScaleSlots;
+          mbar_arrive_expect_tx(&scale_bar[z], src.pages * 32);
+          for (int p = 0; p < src.pages; ++p) {
+            bulk_load(&scales[z][0][4 * p], a.kv.k_scale + src.at[p] * kKv8Groups, 16, &scale_bar[z]);
+            bulk_load(&scales[z][1][4 * p], a.kv.v_scale + src.at[p] * kKv8Groups, 16, &scale_bar[z]);
           }
         }
       }
+      ++issued;
+      if (++slot == C::kSlots) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    Src last = {};
+    bool have = walk.next();
+    int ids_next = have ? page_ids(bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages, 2 * walk.t0, walk.q.npages) : 0;
+    while (have && ok) {
+      // this part's values, while the walk goes on to the next: its page ids and rows of q are asked for a part ahead
+      const int32_t* const row = bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages;
+      const int t0 = walk.t0, t1 = walk.t1, h = walk.h, npages = walk.q.npages;
+      const bool reread = walk.q.nqt > 1;
+      int ids = ids_next, first = 2 * t0;
+      have = walk.next();
+      if (have) {
+        ids_next = page_ids(bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages, 2 * walk.t0, walk.q.npages);
+        for (int c = lane; c < NQ; c += 32) {
+          const int r = walk.qt * NQ + c;
+          if (r >= walk.q.rows * G) break;
+          const char* src = reinterpret_cast<const char*>(static_cast<const __nv_bfloat16*>(a.q) + (walk.q.cub + r / G) * a.q_row +
+                                                          static_cast<size_t>(walk.h * G + r % G) * D);
+          for (int z = 0; z < D * 2; z += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + z));
+        }
+      }
+      for (int t = t0; t < t1 && ok; ++t) {
+        if (2 * t - first >= 32) {
+          first = 2 * t;
+          ids = page_ids(row, first, npages);
+        }
+        Src src;
+        src.pages = min(2, npages - 2 * t);
+        src.reread = reread;
+        for (int p = 0; p < 2; ++p) {
+          int id = __shfl_sync(0xffffffffu, ids, 2 * t + p - first);
+          if (id < 0 || id >= bt.num_pages) {
+            if (lane == 0) report_error(bt.err, kErrBadPage);
+            id = 0;
+          }
+          src.at[p] = static_cast<size_t>(id) * a.kv.n_kv_heads + h;
+        }
+        load(&tm_k, src, true);
+        if (ok && nt > 0) load(&tm_v, last, false);
+        last = src;
+        ++nt;
+      }
     }
+    if (ok && nt > 0) load(&tm_v, last, false);
     if (lane == 0) {  // every copy has landed and every slot's last release has arrived before the CTA ends
-      const int tiles = (issued + 1) / 2;
-      for (int i = max(0, tiles - kScaleSlots); i < tiles; ++i)
+      for (int i = max(0, nt - kScaleSlots); i < nt; ++i)
         if (!mbar_wait(&scale_bar[i % kScaleSlots], (i / kScaleSlots) & 1)) report_error(bt.err, kErrTimeout);
       for (int i = max(0, issued - C::kSlots); i < issued; ++i)
         if (!mbar_wait(&full_bar[i % C::kSlots], (i / C::kSlots) & 1)) report_error(bt.err, kErrTimeout);
       for (int i = max(0, issued - C::kSlots); ok && i < issued; ++i)
         if (!mbar_wait(&empty_bar[i % C::kSlots], (i / C::kSlots) & 1)) report_error(bt.err, kErrTimeout);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t kIdescS = idesc_f8(kTile, NQ, false, false);
       constexpr uint32_t kIdescO = idesc_f8(kTile, C::kOCols, true, true);
       const uint32_t tm_o = tmem + 2 * NQ;
+      const uint64_t q_desc = desc_rows<D>(q_base), p_desc = desc_rows<C::kPRow>(p_base);
       int nt = 0, unit = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, int parity) {
@@ -373,17 +462,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       };
       bool pending = false, fresh = false;  // a tile whose P V is still to be issued; the first of its unit
       auto issue_pv = [&](int n) {          // tile number n of this CTA
-        const int i = 2 * n + 1, s = i % C::kSlots;
+        const int i = v_index(n), s = i % C::kSlots;
         if (!wait(&p_ready, n) || !wait(&full_bar[s], i / C::kSlots)) return;
         tc_fence_after();
-        const uint32_t v = ring + s * C::kSlotBytes;
+        const uint64_t v = desc_rows<D>(ring + s * C::kSlotBytes);  // (a step of n bytes adds n / 16 to the address field)
 #pragma unroll
         for (int part = 0; part < (C::kWide ? 1 : 3); ++part)
 #pragma unroll
           for (int k = 0; k < kTile / 32; ++k)
-            umma_e4m3(tm_o, desc_rows<D>(v + k * 32 * D),
-                      C::kWide ? desc_rows<128>(p_base + k * 32 * 128) : desc_rows<64>(p_base + part * kTile * 64 + k * 32 * 64),
-                      kIdescO, !fresh || part > 0 || k > 0);
+            umma_e4m3(tm_o, v + k * 2 * D, p_desc + (part * kTile + k * 32) * C::kPRow / 16, kIdescO, !fresh || part > 0 || k > 0);
         umma_commit(&empty_bar[s]);
         umma_commit(&pv_done);
       };
@@ -394,17 +481,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
         wait(&q_ready, unit);
         for (int t = walk.t0; t < walk.t1 && ok; ++t, ++nt) {
-          const int i = 2 * nt, s = i % C::kSlots, buf = nt & 1;
+          const int i = k_index(nt), s = i % C::kSlots, buf = nt & 1;
           if (!wait(&full_bar[s], i / C::kSlots)) break;
           if (nt >= 2 && !wait(&s_free[buf], (nt >> 1) - 1)) break;
           tc_fence_after();
-          const uint32_t k8 = ring + s * C::kSlotBytes;
+          const uint64_t k8 = desc_rows<D>(ring + s * C::kSlotBytes);
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
-              umma_e4m3(tmem + buf * NQ, desc_rows<D>(k8 + k * 32), desc_rows<D>(q_base + part * NQ * D + k * 32), kIdescS,
-                        part > 0 || k > 0);
+              umma_e4m3(tmem + buf * NQ, k8 + k * 2, q_desc + (part * NQ * D + k * 32) / 16, kIdescS, part > 0 || k > 0);
           umma_commit(&empty_bar[s]);
           umma_commit(&s_full[buf]);
           if (pending) issue_pv(nt - 1);
@@ -423,8 +509,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t tm_o = tmem + 2 * NQ + lane_base;
+    const int key = tid & 127, grp = tid >> 7, col0 = grp * kCols;  // this thread's key of a tile (column of O^T), and rows
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tm_o = tmem + 2 * NQ + lane_base + col0;
+    auto soft_sync = []() { named_barrier(1, C::kSoft); };
     int nt = 0;
     bool dead = false;
     auto wait = [&](uint64_t* bar, int parity) {  // a thread that gave up waits for nothing more, but meets every barrier
@@ -433,13 +521,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         dead = true;
       }
     };
+    int2 record = make_int2(0, 0);
+    float* const parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kRecordBytes);
     while (walk.next()) {
       const Seq& q = walk.q;
       const int r0 = walk.qt * NQ, cols = min(NQ, q.rows * G - r0);  // rows of this unit
       // ---- q: its largest magnitude, two e4m3 parts
       float f_q;
       {
-        constexpr int kPer = kSoft / NQ, kVec = D / 8 / kPer;  // threads and 16-byte pieces a row
+        constexpr int kPer = C::kSoft / NQ, kVec = D / 8 / kPer;  // threads and 16-byte pieces a row
         const int c = tid / kPer, piece = (tid % kPer) * kVec, r = r0 + c;
         uint4 x[kVec];
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (q.cub + r / G) * a.q_row +
@@ -460,7 +550,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) amax_sh[warp] = __uint_as_float(m << 16);
         soft_sync();  // (and the last unit's readers of the arrays below are done)
-        const float amax = fmaxf(fmaxf(amax_sh[0], amax_sh[1]), fmaxf(amax_sh[2], amax_sh[3]));
+        float amax = amax_sh[0];
+#pragma unroll
+        for (int i = 1; i < 4 * C::kGroups; ++i) amax = fmaxf(amax, amax_sh[i]);
         // 2^e with amax 2^-e in (224, 448]; 448 = 1.75 2^8
         const uint32_t bits = __float_as_uint(amax);
         int e = static_cast<int>(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
@@ -473,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           uint32_t hi2[2], lo2[2];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float v[2] = {__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)};
+            const float v[2] = {__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)};
             float d2[2];
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
@@ -503,63 +595,68 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if (tid < NQ) {
           const int rr = r0 + tid, i = rr / G;
           const long long row = a.full_rows ? static_cast<long long>(q.cus) + q.s + i : q.cub + i;
-          row_sh[tid] = tid < cols ? (row * a.n_heads + walk.h * G + rr % G) : -1;
-          ref_sh[tid] = 0.f;
+          row_sh[tid] = row * a.n_heads + walk.h * G + rr % G;
+          nref_sh[tid] = 0.f;
         }
       }
-      float l[NQ];
+      uint64_t l[kCols / 2];  // sums of pairs of rows over this thread's keys
 #pragma unroll
-      for (int c = 0; c < NQ; ++c) l[c] = 0.f;
+      for (int c = 0; c < kCols / 2; ++c) l[c] = 0;
+      soft_sync();  // nref_sh
 
       for (int t = walk.t0; t < walk.t1; ++t, ++nt) {
-        const int buf = nt & 1, si = 2 * nt;
+        const int buf = nt & 1;
         const bool first = t == walk.t0;
         const int valid = q.n - t * kTile;  // keys of this tile that there are
         wait(&scale_bar[nt % kScaleSlots], nt / kScaleSlots);
-        const float sv = tid < valid ? scales[nt % kScaleSlots][1][tid / kKv8Group] : 0.f;
-        const float f = tid < valid ? scales[nt % kScaleSlots][0][tid / kKv8Group] * f_q : 0.f;
-        const float lv = sv > 0.f ? log2f(sv) : attn::neg_inf();
+        const float sv = key < valid ? scales[nt % kScaleSlots][1][key / kKv8Group] : 0.f;
+        const float f = key < valid ? scales[nt % kScaleSlots][0][key / kKv8Group] * f_q : 0.f;
+        const float lv = sv > 0.f ? __log2f(sv) : attn::neg_inf();
         wait(&s_full[buf], nt >> 1);
         tc_fence_after();
-        float x[NQ];
-        auto scores = [&]() {  // x = f S - R
+        uint64_t x[kCols / 2];
+        for (bool raised = false;; raised = true) {
+          {
+            float s[kCols];
+            tmem_ld_32x32b_x16(tmem + lane_base + buf * NQ + col0, s);
+            const uint64_t f2 = pack2(f, f);
 #pragma unroll
-          for (int c0 = 0; c0 < NQ; c0 += 32) {
-            float s[32];
-            tmem_ld_32x32b_x32(tmem + lane_base + buf * NQ + c0, s);
+            for (int c = 0; c < kCols; c += 4) {  // x = f S - R
+              const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&nref_sh[col0 + c]);
+              x[c / 2] = fma2(pack2(s[c], s[c + 1]), f2, r.x);
+              x[c / 2 + 1] = fma2(pack2(s[c + 2], s[c + 3]), f2, r.y);
+            }
+            if (key >= valid) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) x[c0 + c] = fmaf(s[c], f, -ref_sh[c0 + c]);
+              for (int c = 0; c < kCols / 2; ++c) x[c] = pack2(attn::neg_inf(), attn::neg_inf());
+            }
           }
-          if (tid >= valid) {
+          if (raised) break;
+          if (!first) {
+            float xm = attn::neg_inf();
 #pragma unroll
-            for (int c = 0; c < NQ; ++c) x[c] = attn::neg_inf();
+            for (int c = 0; c < kCols / 2; ++c) {
+              const float2 v = unpack2(x[c]);
+              xm = fmaxf(xm, fmaxf(v.x, v.y));
+            }
+            if (!soft_any<C::kSoft>(xm + lv > kLimit)) break;
           }
-        };
-        bool raise = first;
-        if (first) soft_sync();  // ref_sh is set
-        scores();
-        if (!first) {
-          float xm = attn::neg_inf();
-#pragma unroll
-          for (int c = 0; c < NQ; ++c) xm = fmaxf(xm, x[c]);
-          raise = soft_any(xm + lv > kLimit);
-        }
-        if (raise) {
           // the largest weight x value scale of each row in this tile
+          float u[kCols];
 #pragma unroll
-          for (int c0 = 0; c0 < NQ; c0 += 32) {
-            float u[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) u[c] = x[c0 + c] + lv;
-            const float m = reduce_transposed(u, lane, [](float p, float r) { return fmaxf(p, r); });
-            red_sh[warp][c0 + lane] = m;
+          for (int c = 0; c < kCols / 2; ++c) {
+            const float2 v = unpack2(x[c]);
+            u[2 * c] = v.x + lv;
+            u[2 * c + 1] = v.y + lv;
           }
+          const float m = reduce_transposed(u, lane, [](float p, float r) { return fmaxf(p, r); });
+          if (lane < kCols) red_sh[warp & 3][col0 + lane] = m;
           soft_sync();
           if (tid < NQ) {
-            const float m = fmaxf(fmaxf(red_sh[0][tid], red_sh[1][tid]), fmaxf(red_sh[2][tid], red_sh[3][tid]));
+            const float top = fmaxf(fmaxf(red_sh[0][tid], red_sh[1][tid]), fmaxf(red_sh[2][tid], red_sh[3][tid]));
             float up = 0.f;  // what R grows by
-            if ((first || m > kLimit) && fabsf(m) < INFINITY) up = m - kTop;
-            ref_sh[tid] += up;
+            if ((first || top > kLimit) && fabsf(top) < INFINITY) up = top - kTop;
+            nref_sh[tid] -= up;
             alpha_sh[tid] = first ? 0.f : exp2f(-up);
           }
           if (!first) wait(&pv_done, nt - 1);
@@ -567,46 +664,47 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           if (!first) {
             tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < NQ; ++c) l[c] *= alpha_sh[c];
+            for (int c = 0; c < kCols / 2; ++c) l[c] = mul2(l[c], pack2(alpha_sh[col0 + 2 * c], alpha_sh[col0 + 2 * c + 1]));
+#pragma unroll 1
+            for (int z = 0; z < (C::kWide ? 3 : 1); ++z) {
+              float o[kCols];
+              tmem_ld_32x32b_x16(tm_o + z * NQ, o);
 #pragma unroll
-            for (int c0 = 0; c0 < C::kOCols; c0 += 32) {
-              float o[32];
-              tmem_ld_32x32b_x32(tm_o + c0, o);
-#pragma unroll
-              for (int c = 0; c < 32; ++c) o[c] *= alpha_sh[(c0 + c) % NQ];
-              tmem_st_32x32b_x32(tm_o + c0, o);
+              for (int c = 0; c < kCols; ++c) o[c] *= alpha_sh[col0 + c];
+              tmem_st_32x32b_x16(tm_o + z * NQ, o);
             }
             tmem_st_wait();
           }
-          scores();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[buf]);  // the scores are in registers
+        const uint64_t sv2 = pack2(sv, sv);
 #pragma unroll
-        for (int c = 0; c < NQ; ++c) {
-          const float p = attn::fast_exp2(x[c]);
-          l[c] += p;
-          x[c] = p * sv;
+        for (int c = 0; c < kCols / 2; ++c) {
+          const float2 v = unpack2(x[c]);
+          const uint64_t p = pack2(attn::fast_exp2(v.x), attn::fast_exp2(v.y));
+          l[c] = add2(l[c], p);
+          x[c] = mul2(p, sv2);
         }
         if (nt > 0) wait(&pv_done, nt - 1);  // P's buffer is free
         if (valid < kTile) {                  // what lies behind the end must not meet a weight, not even 0
-          const int vi = si + 1;
+          const int vi = v_index(nt);
           wait(&full_bar[vi % C::kSlots], vi / C::kSlots);
-          if (tid >= valid) {
-#pragma unroll
+          if (tid >= valid && tid < kTile) {
+#pragma unroll 1
             for (int i = 0; i < D / 16; ++i) st_shared_v4(ring + (vi % C::kSlots) * C::kSlotBytes + tid * D + i * 16, 0, 0, 0, 0);
           }
         }
-#pragma unroll
-        for (int c0 = 0; c0 < NQ; c0 += 16) {
+        {
           uint32_t part[3][4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t w[3][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint32_t h = pack_f16x2(x[c0 + 4 * j + 2 * k], x[c0 + 4 * j + 2 * k + 1]);
+              const float2 v = unpack2(x[2 * j + k]);
+              const uint32_t h = pack_f16x2(v.x, v.y);
               // e5m2 is fp16's upper byte: round to it by adding half of the lower one
               const uint32_t hi8 = (h + 0x00800080u) & 0xff00ff00u;
               const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&hi8));
@@ -622,7 +720,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           }
 #pragma unroll
           for (int z = 0; z < 3; ++z) {
-            const uint32_t at = C::kWide ? p_base + swz<128>(tid, z * 2 + c0 / 16) : p_base + z * kTile * 64 + swz<64>(tid, c0 / 16);
+            const uint32_t at = C::kWide ? p_base + swz<C::kPRow>(key, z * C::kGroups + grp)
+                                         : p_base + z * kTile * C::kPRow + swz<C::kPRow>(key, grp);
             st_shared_v4(at, part[z][0], part[z][1], part[z][2], part[z][3]);
           }
         }
@@ -632,120 +731,123 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
 
       // ---- the end of this part of the unit
+      {
+        float u[kCols];
 #pragma unroll
-      for (int c0 = 0; c0 < NQ; c0 += 32) {
-        float u[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) u[c] = l[c0 + c];
-        red_sh[warp][c0 + lane] = reduce_transposed(u, lane, [](float p, float r) { return p + r; });
+        for (int c = 0; c < kCols / 2; ++c) {
+          const float2 v = unpack2(l[c]);
+          u[2 * c] = v.x;
+          u[2 * c + 1] = v.y;
+        }
+        const float sum = reduce_transposed(u, lane, [](float p, float r) { return p + r; });
+        if (lane < kCols) red_sh[warp & 3][col0 + lane] = sum;
       }
       wait(&pv_done, nt - 1);
       soft_sync();
       tc_fence_after();
-      if (tid < NQ) l_sh[tid] = (red_sh[0][tid] + red_sh[1][tid]) + (red_sh[2][tid] + red_sh[3][tid]);
+      if (tid < NQ) {
+        const float sum = (red_sh[0][tid] + red_sh[1][tid]) + (red_sh[2][tid] + red_sh[3][tid]);
+        l_sh[tid] = sum;
+        inv_sh[tid] = 1.f / sum;
+      }
       soft_sync();
-      auto load_o = [&](int c0, float (&o)[32]) {  // columns c0 .. c0 + 32 of O^T, this thread's lane
-        tmem_ld_32x32b_x32(tm_o + c0, o);
-        if (C::kWide) {
-          float o2[32];
-          tmem_ld_32x32b_x32(tm_o + NQ + c0, o2);
+      float o[kCols];  // column `key` of this thread's rows
+      tmem_ld_32x32b_x16(tm_o, o);
+      if (C::kWide) {
+#pragma unroll 1
+        for (int z = 1; z < 3; ++z) {
+          float more[kCols];
+          tmem_ld_32x32b_x16(tm_o + z * NQ, more);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] += o2[c];
-          tmem_ld_32x32b_x32(tm_o + 2 * NQ + c0, o2);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) o[c] += o2[c];
+          for (int c = 0; c < kCols; ++c) o[c] += more[c];
         }
-      };
-      __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o);
-      if (walk.t0 == 0 && walk.t1 == q.tiles) {
-        if (a.lse != nullptr && tid < cols) a.lse[row_sh[tid]] = (ref_sh[tid] + log2f(l_sh[tid])) * attn::kLn2;
+      }
+      const bool began = walk.t0 == 0, goes_on = walk.t1 < q.tiles;
+      if (began && !goes_on) {
+        __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o);
+        if (a.lse != nullptr && tid < cols) a.lse[row_sh[tid]] = (log2f(l_sh[tid]) - nref_sh[tid]) * attn::kLn2;
+        if (key < D) {
 #pragma unroll
-        for (int c0 = 0; c0 < NQ; c0 += 32) {
-          float o[32];
-          load_o(c0, o);
-          if (tid < D) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (c0 + c < cols) out[row_sh[c0 + c] * D + tid] = __float2bfloat16(o[c] / l_sh[c0 + c]);
-          }
+          for (int c = 0; c < kCols; ++c)
+            if (col0 + c < cols) out[row_sh[col0 + c] * D + key] = __float2bfloat16(o[c] * inv_sh[col0 + c]);
         }
         continue;
       }
-      // ---- a piece: (O, R, l) to the workspace; the last of the unit's CTAs joins them
-      float* const parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kCounterBytes);
-      const int c_first = static_cast<int>(((walk.u0 + 1) * n_cta - 1) / T);
-      const int c_last = static_cast<int>(((walk.u0 + q.tiles) * n_cta - 1) / T);
-      auto part_of = [&](int c) { return parts + (static_cast<size_t>(c) * 2 + (c == c_first ? 1 : 0)) * C::kPartFloats; };
-      {
-        float* const mine = part_of(cta);
+      // ---- a piece: (O, R, l) to the workspace
+      float* const mine = parts + (static_cast<size_t>(cta) * 2 + (began ? 1 : 0)) * C::kPartFloats;
+      if (key < D) {
 #pragma unroll
-        for (int c0 = 0; c0 < NQ; c0 += 32) {
-          float o[32];
-          load_o(c0, o);
-          if (tid < D) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (c0 + c < cols) __stcg(mine + (c0 + c) * D + tid, o[c]);
-          }
-        }
-        if (tid < cols) {
-          __stcg(mine + NQ * D + tid, ref_sh[tid]);
-          __stcg(mine + NQ * D + NQ + tid, l_sh[tid]);
-        }
+        for (int c = 0; c < kCols; ++c)
+          if (col0 + c < cols) mine[(col0 + c) * D + key] = o[c];
       }
-      __threadfence();
-      soft_sync();
-      if (tid == 0) {
-        int32_t* const counter = static_cast<int32_t*>(a.ws) + c_first;
-        const int before = atomicAdd(counter, 1);
-        last_sh = before == c_last - c_first;
-        if (last_sh) *counter = 0;
-        __threadfence();
-      }
-      soft_sync();
-      if (!last_sh) continue;
-      __threadfence();
-      // per row: the largest R, the sum of l in it, and (in red_sh, per piece) the weight of each piece
-      float top = attn::neg_inf(), total = 0.f;
       if (tid < cols) {
-        for (int c = c_first; c <= c_last; ++c) {
-          const float r = __ldcg(part_of(c) + NQ * D + tid), lp = __ldcg(part_of(c) + NQ * D + NQ + tid);
-          const float now = fmaxf(top, r);
-          total = total * exp2f(top - now) + lp * exp2f(r - now);
-          top = now;
-        }
-        l_sh[tid] = total;
-        ref_sh[tid] = top;
-        if (a.lse != nullptr) a.lse[row_sh[tid]] = (top + log2f(total)) * attn::kLn2;
+        mine[NQ * D + tid] = -nref_sh[tid];
+        mine[NQ * (D + 1) + tid] = l_sh[tid];
+        if (began) reinterpret_cast<long long*>(mine + NQ * (D + 2))[tid] = row_sh[tid];
       }
-      soft_sync();
-      for (int c0 = 0; c0 < cols; c0 += 32) {
-        float o[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) o[c] = 0.f;
-        for (int p = c_first; p <= c_last; ++p) {
-          const float* const from = part_of(p);
-          soft_sync();  // alpha_sh of the last piece has been read
-          if (tid < 32 && c0 + tid < cols) alpha_sh[tid] = exp2f(__ldcg(from + NQ * D + c0 + tid) - ref_sh[c0 + tid]);
-          soft_sync();
-          if (tid < D) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (c0 + c < cols) o[c] = fmaf(__ldcg(from + (c0 + c) * D + tid), alpha_sh[c], o[c]);
-          }
-        }
-        if (tid < D) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c0 + c < cols) out[row_sh[c0 + c] * D + tid] = __float2bfloat16(o[c] / l_sh[c0 + c]);
-        }
+      if (began && goes_on && tid == 0) {
+        const int c_last = static_cast<int>(((walk.u0 + q.tiles) * n_cta - 1) / T);
+        record = make_int2(c_last - cta + 1, cols);
       }
-      soft_sync();
     }
+    if (tid == 0) static_cast<int2*>(a.ws)[cta] = record;
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if (warp == C::kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+// A warp joins one row of the unit that begins in piece blockIdx.x and goes on in the next ones.
+constexpr int kJoinWarps = 8;
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const Kv8AttnArgs a) {
+  using C = Cfg<D, NQ>;
+  constexpr int kE = D / 32;
+  const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31, cta = blockIdx.x;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int2 record = __ldcg(static_cast<const int2*>(a.ws) + cta);
+  if (r >= record.y) return;
+  const float* const parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + kRecordBytes);
+  const float* const first = parts + (static_cast<size_t>(cta) * 2 + 1) * C::kPartFloats;
+  auto part = [&](int i) { return i == 0 ? first : parts + static_cast<size_t>(cta + i) * 2 * C::kPartFloats; };
+  const long long row = __ldcg(reinterpret_cast<const long long*>(first + NQ * (D + 2)) + r);
+  float top = attn::neg_inf();
+  for (int i = lane; i < record.x; i += 32) top = fmaxf(top, __ldcg(part(i) + NQ * D + r));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  float o[kE], total = 0.f;
+#pragma unroll
+  for (int e = 0; e < kE; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < record.x; ++i) {
+    const float* const p = part(i);
+    const float w = exp2f(__ldcg(p + NQ * D + r) - top);
+    total = fmaf(w, __ldcg(p + NQ * (D + 1) + r), total);
+    const float* const src = p + r * D + lane * kE;
+    if constexpr (kE == 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+      o[0] = fmaf(w, v.x, o[0]);
+      o[1] = fmaf(w, v.y, o[1]);
+      o[2] = fmaf(w, v.z, o[2]);
+      o[3] = fmaf(w, v.w, o[3]);
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+      o[0] = fmaf(w, v.x, o[0]);
+      o[1] = fmaf(w, v.y, o[1]);
+    }
+  }
+  const float inv = 1.f / total;
+  __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o) + row * D + lane * kE;
+  uint32_t w[kE / 2];
+#pragma unroll
+  for (int e = 0; e < kE / 2; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  if constexpr (kE == 4)
+    *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(out) = w[0];
+  if (a.lse != nullptr && lane == 0) a.lse[row] = (top + log2f(total)) * attn::kLn2;
 }
 
 template <int D>
@@ -762,7 +864,7 @@ cudaError_t encode_codes(CUtensorMap* map, const void* ptr, uint64_t rows) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-int grid_of(int num_sms) { return std::min(kCtasPerSm * num_sms, static_cast<int>(kCounterBytes / 4)); }
+int grid_of(int num_sms) { return std::min(kCtasPerSm * num_sms, kMaxCtas); }
 
 template <int D, int NQ>
 cudaError_t launch(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
@@ -773,25 +875,37 @@ cudaError_t launch(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
   if (e == cudaSuccess) e = encode_codes<D>(&tv, a.kv.v, rows);
   if (e == cudaSuccess) e = attn::set_smem(kv8_attn_kernel<D, NQ>, C::kDynSmem);
   if (e != cudaSuccess) return e;
-  return attn::launch_pdl(kv8_attn_kernel<D, NQ>, dim3(grid_of(num_sms)), kThreads, C::kDynSmem, 0, stream, tk, tv, a);
+  const int grid = grid_of(num_sms);
+  e = attn::launch_pdl(kv8_attn_kernel<D, NQ>, dim3(grid), C::kThreads, C::kDynSmem, 0, stream, tk, tv, a);
+  if (e != cudaSuccess) return e;
+  const int64_t most = static_cast<int64_t>(a.bt.max_block_len) * (a.n_heads / a.kv.n_kv_heads);
+  const int joined = static_cast<int>(std::min<int64_t>(NQ, most));
+  return attn::launch_pdl(kv8_join_kernel<D, NQ>, dim3(grid, (joined + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, 0,
+                          stream, a);
 }
 
-// Rows that share a key head: up to 32 in one tile of 32, more in tiles of 64.
-bool narrow(int max_block_len, int n_heads, int n_kv_heads) {
-  return static_cast<int64_t>(max_block_len) * (n_heads / n_kv_heads) <= 32;
+// Rows that share a key head, at most: the smallest of 16, 32 and 64 that holds them, and units of 64 beyond.  A tile
+// costs the softmax its NQ columns whether they are rows or not, so the narrow units are what keeps single tokens and
+// blocks of 32 bound by memory; a unit wider than 64 rows would read the keys fewer times, but does not fit twice on an SM.
+int unit_rows(int max_block_len, int n_heads, int n_kv_heads) {
+  const int64_t rows = static_cast<int64_t>(max_block_len) * (n_heads / n_kv_heads);
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
 }  // namespace
 
 size_t kv8_attention_workspace_bytes(int max_block_len, int n_heads, int n_kv_heads, int head_dim, int num_sms) {
-  const size_t nq = narrow(max_block_len, n_heads, n_kv_heads) ? 32 : 64;
-  return kCounterBytes + static_cast<size_t>(grid_of(num_sms)) * 2 * (nq * head_dim + 2 * nq) * sizeof(float);
+  const size_t nq = unit_rows(max_block_len, n_heads, n_kv_heads);
+  return kRecordBytes + static_cast<size_t>(grid_of(num_sms)) * 2 * nq * (head_dim + 4) * sizeof(float);
 }
 
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
-  const bool n32 = narrow(a.bt.max_block_len, a.n_heads, a.kv.n_kv_heads);
-  if (a.head_dim == 128) return n32 ? launch<128, 32>(a, num_sms, stream) : launch<128, 64>(a, num_sms, stream);
-  return n32 ? launch<64, 32>(a, num_sms, stream) : launch<64, 64>(a, num_sms, stream);
+  const int nq = unit_rows(a.bt.max_block_len, a.n_heads, a.kv.n_kv_heads);
+  if (a.head_dim == 128)
+    return nq == 16 ? launch<128, 16>(a, num_sms, stream)
+                    : nq == 32 ? launch<128, 32>(a, num_sms, stream) : launch<128, 64>(a, num_sms, stream);
+  return nq == 16 ? launch<64, 16>(a, num_sms, stream)
+                  : nq == 32 ? launch<64, 32>(a, num_sms, stream) : launch<64, 64>(a, num_sms, stream);
 }
 
 }  // namespace dllm

@@ -489,9 +489,8 @@ dllm_status dllm_kv8_write_pool(const dllm_layer_desc* desc, const dllm_batch* b
  *   o: device bf16 rows of [n_heads][head_dim], 16-byte aligned; lse: device
  *   fp32 rows of [n_heads], nullable; both as o_rows (DLLM_ROWS_*) says.  Rows
  *   of no block are left as they are.
- *   ws: dllm_kv8_attention_workspace_size bytes, 256-byte aligned; its first
- *   4 KB (counters) must be zero before the first use, and every call leaves
- *   them zero.  Calls that may run at the same time need workspaces of their own. */
+ *   ws: dllm_kv8_attention_workspace_size bytes, 256-byte aligned scratch.
+ *   Calls that may run at the same time need workspaces of their own. */
 dllm_status dllm_kv8_attention_workspace_size(const dllm_layer_desc* desc, const dllm_batch* batch,
                                               const dllm_kv8_cache* kv8, size_t* bytes);
 dllm_status dllm_kv8_attention(const dllm_layer_desc* desc, const dllm_batch* batch, const void* q,

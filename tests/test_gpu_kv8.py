@@ -517,7 +517,7 @@ def test_attention_not_a_number_stays_in_its_head():
         assert torch.equal(o[:8, 2:], want[:8, 2:]) and torch.equal(o[8:], want[8:])
 
 
-def test_attention_repeats_bit_for_bit_and_leaves_its_counters_zero():
+def test_attention_repeats_bit_for_bit_whatever_the_workspace_holds():
     b = Batch([40000, 3, 700], [39990, 0, 5], [4, 3, 64], seed=3)
     kv8 = random_pools(b.num_pages, 2, 128, 5)
     q = _q(b.M, 8, 128, 6)
@@ -526,7 +526,7 @@ def test_attention_repeats_bit_for_bit_and_leaves_its_counters_zero():
     for _ in range(5):
         again = _attend(b, q, kv8, ws)
         assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
-        assert not ws[:4096].any()
+        ws.fill_(0xFF)
     assert_attention(b, q, kv8, *first)
     # the workspace serves another shape next
     c = Batch([900, 12000], [0, 11000], [1, 1], seed=4)
