@@ -349,58 +349,46 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
 
   if (warp == C::kProducerWarp) {
     // ------------------------------------------------------------ TMA producer
+    // The copies of a tile are issued by lanes of one instruction each (K or V: a page a lane; the four pieces of scales):
+    // a single thread that issued them one after the other was the slowest part of the CTA.
     int slot = 0, phase = 0, issued = 0, nt = 0;
     bool ok = true;
-    const uint64_t once = l2_evict_first_policy();
+    uint64_t once, again;  // keys that no other unit reads, and others
+    once = l2_evict_first_policy();
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
     auto page_ids = [&](const int32_t* row, int first, int npages) {  // of 16 tiles, one a lane (checked where used)
       const int p = first + lane;
       return p < npages ? __ldg(row + p) : 0;
     };
-    struct Src {  // one tile of a pool
-      size_t at[2];
-      int pages;
-      bool reread;  // other units read the same keys
-    };
-    auto load = [&](const CUtensorMap* map, const Src& src, bool is_k) {
-      if (issued >= C::kSlots) ok = __shfl_sync(0xffffffffu, lane == 0 ? mbar_wait(&empty_bar[slot], phase ^ 1) : true, 0);
-      if (!ok) {
-        if (lane == 0) report_error(bt.err, kErrTimeout);
-        return;
-      }
-      if (lane == 0) {
-        uint64_t* const bar = &full_bar[slot];
-        uint8_t* const dst = smem + slot * C::kSlotBytes;
-        mbar_arrive_expect_tx(bar, src.pages * (kPage * D));
-        for (int p = 0; p < src.pages; ++p) {
-          const int y = static_cast<int>(src.at[p] * kPage);
-          if (src.reread)
-            tma_load_2d(dst + p * kPage * D, map, bar, 0, y);
-          else
-            tma_load_2d_hint(dst + p * kPage * D, map, bar, 0, y, once);
-        }
-        if (is_k) {
-          const int z = nt % kScaleSlots;
-          mbar_arrive_expect_tx(&scale_bar[z], src.pages * 32);
-          for (int p = 0; p < src.pages; ++p) {
-            bulk_load(&scales[z][0][4 * p], a.kv.k_scale + src.at[p] * kKv8Groups, 16, &scale_bar[z]);
-            bulk_load(&scales[z][1][4 * p], a.kv.v_scale + src.at[p] * kKv8Groups, 16, &scale_bar[z]);
-          }
-        }
-      }
+    const int page = lane & 1;
+    auto next_slot = [&]() {
       ++issued;
       if (++slot == C::kSlots) {
         slot = 0;
         phase ^= 1;
       }
     };
-    Src last = {};
+    auto load_codes = [&](const CUtensorMap* map, int pages, int y, uint64_t policy) {
+      if (issued >= C::kSlots) ok = mbar_wait(&empty_bar[slot], phase ^ 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        if (lane == 0) report_error(bt.err, kErrTimeout);
+        return;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&full_bar[slot], pages * (kPage * D));
+      __syncwarp();
+      if (lane < pages) tma_load_2d_hint(smem + slot * C::kSlotBytes + page * (kPage * D), map, &full_bar[slot], 0, y, policy);
+      next_slot();
+    };
+    int y_last = 0, pages_last = 0;  // the last tile, whose V is still to be asked for
+    uint64_t policy_last = again;
     bool have = walk.next();
     int ids_next = have ? page_ids(bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages, 2 * walk.t0, walk.q.npages) : 0;
     while (have && ok) {
       // this part's values, while the walk goes on to the next: its page ids and rows of q are asked for a part ahead
       const int32_t* const row = bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages;
       const int t0 = walk.t0, t1 = walk.t1, h = walk.h, npages = walk.q.npages;
-      const bool reread = walk.q.nqt > 1;
+      const uint64_t policy = walk.q.nqt > 1 ? again : once;
       int ids = ids_next, first = 2 * t0;
       have = walk.next();
       if (have) {
@@ -418,24 +406,29 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
           first = 2 * t;
           ids = page_ids(row, first, npages);
         }
-        Src src;
-        src.pages = min(2, npages - 2 * t);
-        src.reread = reread;
-        for (int p = 0; p < 2; ++p) {
-          int id = __shfl_sync(0xffffffffu, ids, 2 * t + p - first);
-          if (id < 0 || id >= bt.num_pages) {
-            if (lane == 0) report_error(bt.err, kErrBadPage);
-            id = 0;
-          }
-          src.at[p] = static_cast<size_t>(id) * a.kv.n_kv_heads + h;
+        const int pages = min(2, npages - 2 * t);
+        int id = __shfl_sync(0xffffffffu, ids, 2 * t + page - first);
+        if (id < 0 || id >= bt.num_pages) {
+          if (lane < 2) report_error(bt.err, kErrBadPage);
+          id = 0;
         }
-        load(&tm_k, src, true);
-        if (ok && nt > 0) load(&tm_v, last, false);
-        last = src;
+        const int unit = id * a.kv.n_kv_heads + h;  // 64 units of rows fit 31 bits
+        load_codes(&tm_k, pages, unit * kPage, policy);
+        if (!ok) break;
+        const int z = nt % kScaleSlots;
+        if (lane == 0) mbar_arrive_expect_tx(&scale_bar[z], pages * 32);
+        __syncwarp();
+        if (lane < 4 && page < pages)  // lanes 0, 1: K's, 2, 3: V's
+          bulk_load(&scales[z][lane >> 1][4 * page], (lane < 2 ? a.kv.k_scale : a.kv.v_scale) + static_cast<size_t>(unit) * kKv8Groups,
+                    16, &scale_bar[z]);
+        if (nt > 0) load_codes(&tm_v, pages_last, y_last, policy_last);
+        y_last = unit * kPage;
+        pages_last = pages;
+        policy_last = policy;
         ++nt;
       }
     }
-    if (ok && nt > 0) load(&tm_v, last, false);
+    if (ok && nt > 0) load_codes(&tm_v, pages_last, y_last, policy_last);
     if (lane == 0) {  // every copy has landed and every slot's last release has arrived before the CTA ends
       for (int i = max(0, nt - kScaleSlots); i < nt; ++i)
         if (!mbar_wait(&scale_bar[i % kScaleSlots], (i / kScaleSlots) & 1)) report_error(bt.err, kErrTimeout);
