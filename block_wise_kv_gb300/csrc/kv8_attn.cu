@@ -32,7 +32,9 @@
 //
 // Split: the tiles of all units form one line, cut into as many equal pieces as CTAs
 // (or fewer, where there are few tiles): a ragged batch or one long sequence loads all
-// SMs alike.  A unit cut by a border leaves its pieces' (O, R, l) in the workspace, and a
+// SMs alike.  Each unit stands there with kUnitTiles more than it has: what q, the first
+// reference and the output cost.  (Without them the CTAs that got the many short units of
+// a ragged batch took 1.6 times the mean.)  A unit cut by a border leaves its pieces' (O, R, l) in the workspace, and a
 // second, small kernel joins them in the order of the keys, a warp for each row: with the
 // ring full, every dependent trip to memory (fence, counter, reads) costs the attention's
 // warps several microseconds, which a join inside the kernel had to wait for.
@@ -50,14 +52,15 @@ constexpr uint32_t kTmemCols = 256;  // of a CTA: two fit an SM's 512
 constexpr int kScaleSlots = 8;       // tiles whose scales are in shared memory
 constexpr int kMaxCtas = 1024;       // of a launch (records of the workspace)
 constexpr size_t kRecordBytes = kMaxCtas * sizeof(int2);
+constexpr int kUnitTiles = 3;        // what a unit's beginning and end cost, in tiles (see the split above)
 constexpr int kScan = 128;           // threads that sum up the batch's work
-constexpr int kCols = 16;            // rows of the unit (columns of S^T) a softmax thread holds
 constexpr float kTop = 12.f;    // log2 of a row's largest weight x value scale when R is set
 constexpr float kLimit = 15.f;  // and where it is raised
 
-// NQ rows to a unit, handled by NQ / 16 groups of four softmax warps (a thread: one key, 16 rows).
+// NQ rows to a unit, handled by NQ / kCols groups of four softmax warps (a thread: one key, kCols rows).
 template <int D, int NQ>
 struct Cfg {
+  static constexpr int kCols = NQ == 64 ? 32 : 16;
   static constexpr int kGroups = NQ / kCols;
   static constexpr int kSoft = 128 * kGroups;  // softmax threads
   static constexpr int kProducerWarp = 4 * kGroups, kMmaWarp = kProducerWarp + 1;
@@ -154,11 +157,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Reduce 16 values over the warp's lanes: lanes i and i + 16 get the result of v[i] (v is destroyed).
-template <class Op>
-__device__ __forceinline__ float reduce_transposed(float (&v)[kCols], int lane, Op op) {
+// Reduce N values over the warp's lanes: every lane i mod N gets the result of v[i] (v is destroyed).
+template <int N, class Op>
+__device__ __forceinline__ float reduce_transposed(float (&v)[N], int lane, Op op) {
 #pragma unroll
-  for (int w = kCols / 2; w > 0; w >>= 1) {
+  for (int w = N / 2; w > 0; w >>= 1) {
     const bool up = (lane & w) != 0;
 #pragma unroll
     for (int i = 0; i < w; ++i) {
@@ -166,7 +169,22 @@ __device__ __forceinline__ float reduce_transposed(float (&v)[kCols], int lane, 
       v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, w));
     }
   }
-  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+  if (N == 16) v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+  return v[0];
+}
+// A thread's N columns of its TMEM lane.
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[16]) { tmem_ld_32x32b_x16(taddr, v); }
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[32]) { tmem_ld_32x32b_x32(taddr, v); }
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&v)[16]) { tmem_st_32x32b_x16(taddr, v); }
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&v)[32]) { tmem_st_32x32b_x32(taddr, v); }
+
+// Wait for the phase with the given parity, at most 2^18 tries of up to 20 us each (seconds), in few instructions: the
+// kernel's roles share the instruction cache.  False where it gave up.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < (1 << 18); ++i)
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+  return false;
 }
 
 // ------------------------------------------------------------ work
@@ -203,7 +221,7 @@ __device__ __forceinline__ Seq load_seq(const Kv8AttnArgs& a, int b) {
 }
 template <int NQ>
 __device__ __forceinline__ long long seq_work(const Kv8AttnArgs& a, const Seq& q) {
-  return static_cast<long long>(a.kv.n_kv_heads) * q.nqt * q.tiles;
+  return q.tiles == 0 ? 0 : static_cast<long long>(a.kv.n_kv_heads) * q.nqt * (q.tiles + kUnitTiles);
 }
 
 // A CTA's piece [lo, hi) of the line of tiles, walked unit by unit by every role alike.
@@ -213,7 +231,7 @@ struct Walk {
   long long base, pos, hi;  // where sequence b begins on the line; the next tile; the end
   int b;
   Seq q;
-  // the current part of a unit: tiles [t0, t1) of (b, h, qt), which lies at u0 on the line
+  // the current part of a unit: tiles [t0, t1) of (b, h, qt), whose first tile lies at u0 on the line
   int h, qt, t0, t1;
   long long u0;
   __device__ Walk(const Kv8AttnArgs& args, int b0, const Seq& q0, long long base0, long long lo, long long hi0)
@@ -226,12 +244,13 @@ struct Walk {
       q = load_seq<NQ>(a, ++b);
       w = seq_work<NQ>(a, q);
     }
-    const int x = static_cast<int>((pos - base) / q.tiles);  // unit of the sequence
+    const int x = static_cast<int>((pos - base) / (q.tiles + kUnitTiles));  // unit of the sequence
     h = x / q.nqt;
     qt = x % q.nqt;
-    u0 = base + static_cast<long long>(x) * q.tiles;
-    t0 = static_cast<int>(pos - u0);
+    u0 = base + static_cast<long long>(x) * (q.tiles + kUnitTiles) + kUnitTiles;
+    t0 = static_cast<int>(max(pos - u0, 0ll));
     t1 = static_cast<int>(min(static_cast<long long>(q.tiles), hi - u0));
+    if (t1 <= 0) return false;  // the piece ends before the unit's first tile
     pos = u0 + t1;
     return true;
   }
@@ -341,10 +360,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
   }
   __syncthreads();
   Walk<NQ> walk(a, start_b, start_q, start_base, lo, hi);
-  const int n_tiles = static_cast<int>(hi - lo);
-  // the ring's order: K of the next tile before V of this one, which is needed later
+  // the ring's order: K of the next tile before V of this one, which is needed later (the last tile's V leaves the place
+  // of the K that does not follow empty)
   auto k_index = [](int n) { return n == 0 ? 0 : 2 * n - 1; };
-  auto v_index = [n_tiles](int n) { return n + 1 < n_tiles ? 2 * n + 2 : 2 * n + 1; };
+  auto v_index = [](int n) { return 2 * n + 2; };
   const int G = a.n_heads / a.kv.n_kv_heads;
 
   if (warp == C::kProducerWarp) {
@@ -369,7 +388,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       }
     };
     auto load_codes = [&](const CUtensorMap* map, int pages, int y, uint64_t policy) {
-      if (issued >= C::kSlots) ok = mbar_wait(&empty_bar[slot], phase ^ 1);
+      if (issued >= C::kSlots) ok = wait_phase(&empty_bar[slot], phase ^ 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
         if (lane == 0) report_error(bt.err, kErrTimeout);
@@ -428,14 +447,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         ++nt;
       }
     }
-    if (ok && nt > 0) load_codes(&tm_v, pages_last, y_last, policy_last);
+    if (ok && nt > 0) {
+      next_slot();
+      load_codes(&tm_v, pages_last, y_last, policy_last);
+    }
     if (lane == 0) {  // every copy has landed and every slot's last release has arrived before the CTA ends
       for (int i = max(0, nt - kScaleSlots); i < nt; ++i)
-        if (!mbar_wait(&scale_bar[i % kScaleSlots], (i / kScaleSlots) & 1)) report_error(bt.err, kErrTimeout);
+        if (!wait_phase(&scale_bar[i % kScaleSlots], (i / kScaleSlots) & 1)) report_error(bt.err, kErrTimeout);
+      const int none = ok ? 2 * nt - 1 : -1;
       for (int i = max(0, issued - C::kSlots); i < issued; ++i)
-        if (!mbar_wait(&full_bar[i % C::kSlots], (i / C::kSlots) & 1)) report_error(bt.err, kErrTimeout);
+        if (i != none && !wait_phase(&full_bar[i % C::kSlots], (i / C::kSlots) & 1)) report_error(bt.err, kErrTimeout);
       for (int i = max(0, issued - C::kSlots); ok && i < issued; ++i)
-        if (!mbar_wait(&empty_bar[i % C::kSlots], (i / C::kSlots) & 1)) report_error(bt.err, kErrTimeout);
+        if (i != none && !wait_phase(&empty_bar[i % C::kSlots], (i / C::kSlots) & 1)) report_error(bt.err, kErrTimeout);
     }
   } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
@@ -447,7 +470,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       int nt = 0, unit = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, int parity) {
-        if (ok && !mbar_wait(bar, parity & 1)) {
+        if (ok && !wait_phase(bar, parity & 1)) {
           report_error(bt.err, kErrTimeout);
           ok = false;
         }
@@ -497,11 +520,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       // products that were issued end before the CTA does
       if (!ok) {
         umma_commit(&drain_bar);
-        if (!mbar_wait(&drain_bar, 0)) report_error(bt.err, kErrTimeout);
+        if (!wait_phase(&drain_bar, 0)) report_error(bt.err, kErrTimeout);
       }
     }
   } else {
     // ------------------------------------------------------------ softmax
+    constexpr int kCols = C::kCols;
     const int key = tid & 127, grp = tid >> 7, col0 = grp * kCols;  // this thread's key of a tile (column of O^T), and rows
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tm_o = tmem + 2 * NQ + lane_base + col0;
@@ -509,7 +533,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     int nt = 0;
     bool dead = false;
     auto wait = [&](uint64_t* bar, int parity) {  // a thread that gave up waits for nothing more, but meets every barrier
-      if (!dead && !mbar_wait(bar, parity & 1)) {
+      if (!dead && !wait_phase(bar, parity & 1)) {
         report_error(bt.err, kErrTimeout);
         dead = true;
       }
@@ -611,7 +635,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         for (bool raised = false;; raised = true) {
           {
             float s[kCols];
-            tmem_ld_32x32b_x16(tmem + lane_base + buf * NQ + col0, s);
+            tmem_load(tmem + lane_base + buf * NQ + col0, s);
             const uint64_t f2 = pack2(f, f);
 #pragma unroll
             for (int c = 0; c < kCols; c += 4) {  // x = f S - R
@@ -661,10 +685,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
 #pragma unroll 1
             for (int z = 0; z < (C::kWide ? 3 : 1); ++z) {
               float o[kCols];
-              tmem_ld_32x32b_x16(tm_o + z * NQ, o);
+              tmem_load(tm_o + z * NQ, o);
 #pragma unroll
               for (int c = 0; c < kCols; ++c) o[c] *= alpha_sh[col0 + c];
-              tmem_st_32x32b_x16(tm_o + z * NQ, o);
+              tmem_store(tm_o + z * NQ, o);
             }
             tmem_st_wait();
           }
@@ -689,14 +713,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
             for (int i = 0; i < D / 16; ++i) st_shared_v4(ring + (vi % C::kSlots) * C::kSlotBytes + tid * D + i * 16, 0, 0, 0, 0);
           }
         }
-        {
+#pragma unroll
+        for (int c0 = 0; c0 < kCols; c0 += 16) {
           uint32_t part[3][4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t w[3][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float2 v = unpack2(x[2 * j + k]);
+              const float2 v = unpack2(x[c0 / 2 + 2 * j + k]);
               const uint32_t h = pack_f16x2(v.x, v.y);
               // e5m2 is fp16's upper byte: round to it by adding half of the lower one
               const uint32_t hi8 = (h + 0x00800080u) & 0xff00ff00u;
@@ -711,10 +736,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
 #pragma unroll
             for (int z = 0; z < 3; ++z) part[z][j] = __byte_perm(w[z][0], w[z][1], 0x7531);
           }
+          const int chunk = (col0 + c0) / 16;
 #pragma unroll
           for (int z = 0; z < 3; ++z) {
-            const uint32_t at = C::kWide ? p_base + swz<C::kPRow>(key, z * C::kGroups + grp)
-                                         : p_base + z * kTile * C::kPRow + swz<C::kPRow>(key, grp);
+            const uint32_t at = C::kWide ? p_base + swz<C::kPRow>(key, z * (NQ / 16) + chunk)
+                                         : p_base + z * kTile * C::kPRow + swz<C::kPRow>(key, chunk);
             st_shared_v4(at, part[z][0], part[z][1], part[z][2], part[z][3]);
           }
         }
@@ -745,12 +771,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       }
       soft_sync();
       float o[kCols];  // column `key` of this thread's rows
-      tmem_ld_32x32b_x16(tm_o, o);
+      tmem_load(tm_o, o);
       if (C::kWide) {
 #pragma unroll 1
         for (int z = 1; z < 3; ++z) {
           float more[kCols];
-          tmem_ld_32x32b_x16(tm_o + z * NQ, more);
+          tmem_load(tm_o + z * NQ, more);
 #pragma unroll
           for (int c = 0; c < kCols; ++c) o[c] += more[c];
         }
