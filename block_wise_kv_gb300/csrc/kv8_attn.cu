@@ -15,13 +15,13 @@
 // bf16's 8 exactly down to 2^-11 of the largest, and below that to 2^-19 of it.
 // A weight is rounded to fp16 (11 bits) and split into three e5m2 parts, which is
 // exact (3 bits each, rounded to nearest) but for an absolute 2^-17, half of the
-// smallest e5m2 step, where a row's largest is 2^12 or more: a softmax with one large
+// smallest e5m2 step, where a row's largest is 2^10 or more: a softmax with one large
 // weight and a long flat tail that together weighs as much keeps its tail.  The value scale of a key multiplies
 // its weight before the split; the sum l takes the weight without it.
 //
 // The thread that holds a key's scores has its scales as two scalars; a row's
 // reference R is the same for all 128 keys.  R is set from a unit's first tile (so
-// that the largest weight x value scale is 2^12) and raised only when one passes 2^15:
+// that the largest weight x value scale is 2^10) and raised only when one passes 2^15:
 // a vote per tile, and otherwise no reduction over keys at all until the unit's end,
 // where the 128 partial sums of each row are added.
 //
@@ -54,7 +54,7 @@ constexpr int kMaxCtas = 1024;       // of a launch (records of the workspace)
 constexpr size_t kRecordBytes = kMaxCtas * sizeof(int2);
 constexpr int kUnitTiles = 3;        // what a unit's beginning and end cost, in tiles (see the split above)
 constexpr int kScan = 128;           // threads that sum up the batch's work
-constexpr float kTop = 12.f;    // log2 of a row's largest weight x value scale when R is set
+constexpr float kTop = 10.f;    // log2 of a row's largest weight x value scale when R is set
 constexpr float kLimit = 15.f;  // and where it is raised
 
 // NQ rows to a unit, handled by NQ / kCols groups of four softmax warps (a thread: one key, kCols rows).
