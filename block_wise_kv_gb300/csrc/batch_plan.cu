@@ -55,6 +55,18 @@ __device__ __forceinline__ int last_not_above(const long long* v, int n, long lo
   return lo;
 }
 
+// Those of the four entries of a row map from j0 (a multiple of 4) on that lie in [lo, hi).
+__device__ __forceinline__ void store4(int32_t* map, long long j0, const int (&v)[4], long long lo, long long hi) {
+  if (map == nullptr) return;
+  if (j0 >= lo && j0 + 4 <= hi) {
+    *reinterpret_cast<int4*>(map + j0) = make_int4(v[0], v[1], v[2], v[3]);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (j0 + e >= lo && j0 + e < hi) map[j0 + e] = v[e];
+}
+
 __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) {
   __shared__ Chunk c;
   __shared__ Sums warp_sums[kWarps + 1];
@@ -63,6 +75,7 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) 
   const int cta = blockIdx.x, n_cta = gridDim.x;
   griddep_wait();
 
+  const long long first = static_cast<long long>(cta) * kThreads + t, stride = static_cast<long long>(n_cta) * kThreads;
   int head = a.state[0], count = a.state[1];
   int err = 0;
   if (head < 0 || head >= a.num_pages || count < 0 || count > a.num_pages) {
@@ -149,21 +162,15 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) 
     const Sums total = carry + warp_sums[kWarps];
     const int nb = min(kChunk, a.batch - b0);
 
-    // the ids handed out, and those given back: unit u of 1024 ids belongs to CTA u mod n_cta
+    // the ids handed out, and those given back: CTA c has every n_cta-th stretch of 1024 of this chunk's
     const long long take_end = min(total.take, static_cast<long long>(count));
-    for (long long u = carry.take / kThreads; u * kThreads < take_end; ++u) {
-      if (u % n_cta != cta) continue;
-      const long long i = u * kThreads + t;
-      if (i < carry.take || i >= take_end) continue;
+    for (long long i = carry.take + first; i < take_end; i += stride) {
       const int k = last_not_above(c.take0, nb, i);
       if (c.now[k] <= c.held[k]) continue;  // asked for more than was free
       const int id = ring_id(i);
       a.table[static_cast<size_t>(b0 + k) * a.max_pages + c.held[k] + (i - c.take0[k])] = id;
     }
-    for (long long u = carry.give / kThreads; u * kThreads < total.give; ++u) {
-      if (u % n_cta != cta) continue;
-      const long long i = u * kThreads + t;
-      if (i < carry.give || i >= total.give) continue;
+    for (long long i = carry.give + first; i < total.give; i += stride) {
       const int k = last_not_above(c.give0, nb, i);
       int id = a.table[static_cast<size_t>(b0 + k) * a.max_pages + c.now[k] + (i - c.give0[k])];
       if (id < 0 || id >= a.num_pages) {
@@ -176,27 +183,32 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) 
       }
       a.ring[ring_at(count + i)] = id;
     }
-    // the rows
+    // the rows: four in a row to a thread, one search for all, 16-byte stores where all four are of this chunk
     const long long row_end = min(total.rows, static_cast<long long>(a.cap_rows));
-    for (long long u = carry.rows / kThreads; u * kThreads < row_end; ++u) {
-      if (u % n_cta != cta) continue;
-      const long long j = u * kThreads + t;
-      if (j < carry.rows || j >= row_end) continue;
-      const int k = last_not_above(c.row0, nb, j);
-      const int pos = c.start[k] + static_cast<int>(j - c.row0[k]);
-      const int pg = pos / kPage;
-      int slot = -1;
-      if (pg < c.now[k] && a.row_slot != nullptr) {
-        const int id = pg < c.held[k] ? a.table[static_cast<size_t>(b0 + k) * a.max_pages + pg]
-                                      : ring_id(c.take0[k] + pg - c.held[k]);
-        if (id >= 0 && id < a.num_pages)
-          slot = id * kPage + pos % kPage;
-        else
-          err |= kErrBadPage;
+    for (long long j0 = carry.rows / 4 * 4 + 4 * first; j0 < row_end; j0 += 4 * stride) {
+      int k = last_not_above(c.row0, nb, max(j0, carry.rows));
+      int slot[4], seq[4], pos[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const long long j = j0 + e;
+        slot[e] = seq[e] = pos[e] = -1;
+        if (j < carry.rows || j >= row_end) continue;
+        while (k + 1 < nb && c.row0[k + 1] <= j) ++k;
+        const int p = c.start[k] + static_cast<int>(j - c.row0[k]), pg = p / kPage;
+        seq[e] = b0 + k;
+        pos[e] = p;
+        if (pg < c.now[k] && a.row_slot != nullptr) {
+          const int id = pg < c.held[k] ? a.table[static_cast<size_t>(b0 + k) * a.max_pages + pg]
+                                        : ring_id(c.take0[k] + pg - c.held[k]);
+          if (id >= 0 && id < a.num_pages)
+            slot[e] = id * kPage + p % kPage;
+          else
+            err |= kErrBadPage;
+        }
       }
-      if (a.row_slot != nullptr) a.row_slot[j] = slot;
-      if (a.row_seq != nullptr) a.row_seq[j] = b0 + k;
-      if (a.row_pos != nullptr) a.row_pos[j] = pos;
+      store4(a.row_slot, j0, slot, carry.rows, row_end);
+      store4(a.row_seq, j0, seq, carry.rows, row_end);
+      store4(a.row_pos, j0, pos, carry.rows, row_end);
     }
     carry = total;
   }
@@ -215,8 +227,7 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) 
     }
   }
   if (carry.rows > a.cap_rows || carry.seq > a.cap_seq) err |= kErrBadShape;
-  for (long long j = carry.rows + static_cast<long long>(cta) * kThreads + t; j < a.cap_rows;
-       j += static_cast<long long>(n_cta) * kThreads) {
+  for (long long j = carry.rows + first; j < a.cap_rows; j += stride) {
     if (a.row_slot != nullptr) a.row_slot[j] = -1;
     if (a.row_seq != nullptr) a.row_seq[j] = -1;
     if (a.row_pos != nullptr) a.row_pos[j] = -1;

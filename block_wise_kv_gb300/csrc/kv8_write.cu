@@ -8,11 +8,12 @@
 // unless the result is an e4m3 subnormal.  A scale of amax / 448 would fill the
 // last bit of the range, but every growth would round all kept rows again.
 //
-// Bound: HBM, 6 bytes a value (read 2, write 1, for K and for V).  A warp takes
-// one group of K and of V: 16 rows of 256 bytes each, every load in flight before
-// the first is used, 8-byte code stores.  Groups start where a block starts or
+// Bound: HBM, 3 bytes a value (read 2, write 1).  A warp takes one group of K or of V:
+// 16 rows of 256 bytes, every load in flight before the first is used, 8-byte code stores.  Groups start where a block starts or
 // where a position is a multiple of 16, so a CTA takes a slice of packed rows,
 // finds the groups that begin in it, and deals (group, head) items to its warps.
+#include <algorithm>
+
 #include "attn_common.cuh"
 #include "kv8.cuh"
 
@@ -21,6 +22,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 4;
 constexpr int kMaxSlice = 64;  // packed rows a CTA looks at, at most
 constexpr int kCuInSmem = 1024;  // batches up to this many sequences are searched in shared memory
 
@@ -137,7 +139,7 @@ __device__ __forceinline__ void quantise(const uint4 (&x)[D / 16], const Group& 
 }
 
 template <int D, bool POOL>
-__global__ void __launch_bounds__(kThreads) kv8_write_kernel(const Kv8WriteArgs a, int slice, int heads_per_cta) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv8_write_kernel(const Kv8WriteArgs a, int slice, int heads_per_cta) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIter = 16 / kRows;
   __shared__ int cu[kCuInSmem + 1];
   __shared__ Group groups[kMaxSlice];
@@ -194,32 +196,31 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(const Kv8WriteArgs 
     }
   }
   __syncthreads();
+  // an item is a group of one head's K or V
   const int h0 = blockIdx.y * heads_per_cta, nh = min(heads_per_cta, a.kv.n_kv_heads - h0);
-  const int items = n_groups * nh;
+  const int items = n_groups * nh * 2;
   const int sub = lane / kLanes, col = (lane % kLanes) * 8;
   for (int it = warp; it < items; it += kWarps) {
-    const Group g = groups[it / nh];
-    const int h = h0 + it % nh;
-    const size_t slot = (static_cast<size_t>(g.page) * a.kv.n_kv_heads + h) * kPage + g.quarter * kKv8Group;
-    uint4 k[kIter], v[kIter];
+    const bool is_k = (it & 1) == 0;
+    const Group g = groups[(it >> 1) / nh];
+    const int h = h0 + (it >> 1) % nh;
+    const size_t unit = static_cast<size_t>(g.page) * a.kv.n_kv_heads + h, slot = unit * kPage + g.quarter * kKv8Group;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_k ? a.k_src : a.v_src) + col;
+    int64_t row = D;
+    if (POOL) {
+      src += slot * D;
+    } else {
+      row = is_k ? a.k_row : a.v_row;
+      src += (g.row - g.t0) * row + h * (is_k ? a.k_head : a.v_head);
+    }
+    uint4 x[kIter];
 #pragma unroll
     for (int i = 0; i < kIter; ++i) {
       const int tt = i * kRows + sub;
-      const bool on = tt >= g.t0 && tt < g.t0 + g.n;
-      size_t ko, vo;
-      if (POOL) {
-        ko = vo = (slot + tt) * D + col;
-      } else {
-        const long long j = g.row + tt - g.t0;
-        ko = static_cast<size_t>(j * a.k_row + h * a.k_head + col);
-        vo = static_cast<size_t>(j * a.v_row + h * a.v_head + col);
-      }
-      k[i] = on ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.k_src) + ko)) : make_uint4(0, 0, 0, 0);
-      v[i] = on ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.v_src) + vo)) : make_uint4(0, 0, 0, 0);
+      x[i] = tt >= g.t0 && tt < g.t0 + g.n ? __ldg(reinterpret_cast<const uint4*>(src + tt * row)) : make_uint4(0, 0, 0, 0);
     }
-    const size_t sc = (static_cast<size_t>(g.page) * a.kv.n_kv_heads + h) * kKv8Groups + g.quarter;
-    quantise<D>(k, g, a.kv.k + slot * D, a.kv.k_scale + sc, lane, err);
-    quantise<D>(v, g, a.kv.v + slot * D, a.kv.v_scale + sc, lane, err);
+    quantise<D>(x, g, (is_k ? a.kv.k : a.kv.v) + slot * D, (is_k ? a.kv.k_scale : a.kv.v_scale) + unit * kKv8Groups + g.quarter,
+                lane, err);
   }
   if (err) report_error(bt.err, err);
 }
@@ -228,11 +229,18 @@ __global__ void __launch_bounds__(kThreads) kv8_write_kernel(const Kv8WriteArgs 
 
 cudaError_t launch_kv8_write(const Kv8WriteArgs& a, int num_sms, cudaStream_t stream) {
   const int rows = a.bt.total_block_rows, heads = a.kv.n_kv_heads;
-  // Slices of 64 rows and four heads where that fills the GPU twice over (16 items and more for a CTA's eight
-  // warps), else 16 rows and one head: single tokens make every row a group of its own.
-  const long long wide = static_cast<long long>((rows + 63) / 64) * ((heads + 3) / 4);
-  const bool big = wide >= 2 * num_sms;
-  const int slice = big ? 64 : 16, hc = big ? 4 : 1;
+  // Rows to a group, by the mean block: single tokens make every row a group of its own.
+  const int mean = std::min(kKv8Group, std::max(1, rows / a.bt.batch));
+  const long long items = 2ll * heads * ((rows + mean - 1) / mean), resident = static_cast<long long>(kCtasPerSm) * num_sms;
+  int slice, hc;
+  if (items >= 4 * kWarps * resident) {  // enough for every resident warp several times over: one wave of CTAs, slices of 64 rows
+    slice = kMaxSlice;
+    hc = static_cast<int>((static_cast<long long>(heads) * ((rows + slice - 1) / slice) + resident - 1) / resident);
+  } else {  // latency: about an item to a warp
+    slice = std::min(16, 4 * mean);
+    hc = std::max(1, kWarps * mean / (2 * slice));
+  }
+  hc = std::min(hc, heads);
   const dim3 grid((rows + slice - 1) / slice, (heads + hc - 1) / hc);
   if (a.head_dim == 128)
     return a.from_pool ? attn::launch_pdl(kv8_write_kernel<128, true>, grid, kThreads, 0, 0, stream, a, slice, hc)
