@@ -23,7 +23,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCtasPerSm = 4;
-constexpr int kMaxSlice = 64;  // packed rows a CTA looks at, at most
+constexpr int kMaxSlice = 32;  // packed rows a CTA looks at, at most
 constexpr int kCuInSmem = 1024;  // batches up to this many sequences are searched in shared memory
 
 struct Group {
@@ -58,37 +58,60 @@ __device__ __forceinline__ uint32_t only_nan(uint32_t u) {
   return u;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Eight codes of eight bf16 values x / s (s a power of two, inv = 1 / s: exact products).
+__device__ __forceinline__ uint2 codes_of(const uint4& x, uint64_t inv2) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint16_t c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(w[k] << 16), "r"(w[k] & 0xffff0000u));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(v), "l"(inv2));
+    float lo, hi;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+    c[k] = cvt_e4m3x2(lo, hi);
+  }
+  return make_uint2(c[0] | (static_cast<uint32_t>(c[1]) << 16), c[2] | (static_cast<uint32_t>(c[3]) << 16));
+}
+
 // The group of one pool: the lane's pieces x[i] are rows kRows * i + lane / kLanes, 8 columns from 8 * (lane % kLanes).
+// Groups with nothing out of the ordinary take the short way; what is rare is kept out of its registers and reads the
+// rows again from src (row t of the group at src + t * row, at this lane's columns).
 template <int D>
-__device__ __forceinline__ void quantise(const uint4 (&x)[D / 16], const Group& g, uint8_t* codes, float* scale,
-                                         int lane, int& err) {
+__device__ __forceinline__ void quantise(const uint4 (&x)[D / 16], const __nv_bfloat16* src, int64_t row, const Group& g,
+                                         uint8_t* codes, float* scale, int lane, int& err) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes, kIter = 16 / kRows;
   const int sub = lane / kLanes, col = (lane % kLanes) * 8;
+  uint8_t* const mine = codes + sub * D + col;  // row sub; row kRows * i + sub is kRows * D * i further
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < kIter; ++i)
-    m = __vmaxu2(__vmaxu2(m, __vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu)),
-                 __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
-  bool odd = (m & 0xffffu) >= 0x7f80u || (m >> 16) >= 0x7f80u;
-  odd = __any_sync(0xffffffffu, odd);
+    m = max_u16x2(m, max_u16x2(max_u16x2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                               max_u16x2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  uint32_t amax = max(m & 0xffffu, m >> 16);
+  const bool odd = amax >= 0x7f80u;
   if (odd) {  // a value that is not finite takes no part in the scale
     err |= kErrRange;
-    m = 0;
-#pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t a = w[k] & 0x7fff7fffu;
-        if ((a & 0xffffu) >= 0x7f80u) a &= 0xffff0000u;
-        if ((a >> 16) >= 0x7f80u) a &= 0xffffu;
-        m = __vmaxu2(m, a);
+    amax = 0;
+#pragma unroll 1
+    for (int t = sub; t < 16; t += kRows) {
+      if (t < g.t0 || t >= g.t0 + g.n) continue;
+#pragma unroll 1
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t v = __ldg(reinterpret_cast<const uint16_t*>(src + t * row) + k) & 0x7fffu;
+        if (v < 0x7f80u) amax = max(amax, v);
       }
     }
+    __syncwarp();
+    amax = __reduce_max_sync(0xffffffffu, amax);
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const uint32_t amax = max(m & 0xffffu, m >> 16);
   if (amax > (static_cast<uint32_t>(127 + 8 + kKv8MaxExp) << 7) + 96u) err |= kErrRange;  // beyond 448 * 2^60
   float s = two_to(scale_exponent(amax));
   const bool keeps = g.keep_lo > 0 || g.keep_hi > g.t0 + g.n;
@@ -98,11 +121,11 @@ __device__ __forceinline__ void quantise(const uint4 (&x)[D / 16], const Group& 
       s = old;
     } else if (old < s) {
       const float ratio = __fdiv_rn(old, s);
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < kIter; ++i) {
         const int t = i * kRows + sub;
         if (t < g.keep_lo || (t >= g.t0 + g.n && t < g.keep_hi)) {
-          uint2* p = reinterpret_cast<uint2*>(codes + t * D + col);
+          uint2* p = reinterpret_cast<uint2*>(mine + i * kRows * D);
           const uint2 c = *p;
           uint32_t out[2];
           const uint32_t in[2] = {c.x, c.y};
@@ -117,22 +140,27 @@ __device__ __forceinline__ void quantise(const uint4 (&x)[D / 16], const Group& 
       }
     }
   }
-  const float inv = __frcp_rn(s);  // exact for this library's scales; a present scale of another kind is divided by
-  const bool exact = (__float_as_uint(s) & 0x7fffffu) == 0;
+  const bool exact = (__float_as_uint(s) & 0x7fffffu) == 0;  // else a present scale of another kind: divided by
+  if (exact && !odd) {
+    const float inv = __frcp_rn(s);
+    uint64_t inv2;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(inv2) : "f"(inv));
 #pragma unroll
-  for (int i = 0; i < kIter; ++i) {
-    const int t = i * kRows + sub;
-    if (t < g.t0 || t >= g.t0 + g.n) continue;
-    uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    uint16_t c[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (odd) w[k] = only_nan(w[k]);
-      const float2 f = bf16x2_f32(w[k]);
-      c[k] = exact ? cvt_e4m3x2(f.x * inv, f.y * inv) : cvt_e4m3x2(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
+    for (int i = 0; i < kIter; ++i) {
+      const int t = i * kRows + sub;
+      const uint2 c = codes_of(x[i], inv2);
+      if (t >= g.t0 && t < g.t0 + g.n) *reinterpret_cast<uint2*>(mine + i * kRows * D) = c;
     }
-    *reinterpret_cast<uint2*>(codes + t * D + col) =
-        make_uint2(c[0] | (static_cast<uint32_t>(c[1]) << 16), c[2] | (static_cast<uint32_t>(c[3]) << 16));
+  } else {
+#pragma unroll 1
+    for (int t = sub; t < 16; t += kRows) {
+      if (t < g.t0 || t >= g.t0 + g.n) continue;
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {  // a pair of values at a time
+        const float2 f = bf16x2_f32(only_nan(__ldg(reinterpret_cast<const uint32_t*>(src + t * row) + k)));
+        *reinterpret_cast<uint16_t*>(codes + t * D + col + 2 * k) = cvt_e4m3x2(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
+      }
+    }
   }
   __syncwarp();  // every lane has read the old scale
   if (lane == 0) *scale = s;
@@ -219,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv8_write_kernel(const K
       const int tt = i * kRows + sub;
       x[i] = tt >= g.t0 && tt < g.t0 + g.n ? __ldg(reinterpret_cast<const uint4*>(src + tt * row)) : make_uint4(0, 0, 0, 0);
     }
-    quantise<D>(x, g, (is_k ? a.kv.k : a.kv.v) + slot * D, (is_k ? a.kv.k_scale : a.kv.v_scale) + unit * kKv8Groups + g.quarter,
+    quantise<D>(x, src, row, g, (is_k ? a.kv.k : a.kv.v) + slot * D, (is_k ? a.kv.k_scale : a.kv.v_scale) + unit * kKv8Groups + g.quarter,
                 lane, err);
   }
   if (err) report_error(bt.err, err);
@@ -233,9 +261,9 @@ cudaError_t launch_kv8_write(const Kv8WriteArgs& a, int num_sms, cudaStream_t st
   const int mean = std::min(kKv8Group, std::max(1, rows / a.bt.batch));
   const long long items = 2ll * heads * ((rows + mean - 1) / mean), resident = static_cast<long long>(kCtasPerSm) * num_sms;
   int slice, hc;
-  if (items >= 4 * kWarps * resident) {  // enough for every resident warp several times over: one wave of CTAs, slices of 64 rows
+  if (items >= 4 * kWarps * resident) {  // enough for every resident warp several times over
     slice = kMaxSlice;
-    hc = static_cast<int>((static_cast<long long>(heads) * ((rows + slice - 1) / slice) + resident - 1) / resident);
+    hc = 4;
   } else {  // latency: about an item to a warp
     slice = std::min(16, 4 * mean);
     hc = std::max(1, kWarps * mean / (2 * slice));
