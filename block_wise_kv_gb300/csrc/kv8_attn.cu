@@ -53,7 +53,8 @@ constexpr int kScaleSlots = 8;       // tiles whose scales are in shared memory
 constexpr int kMaxCtas = 1024;       // of a launch (records of the workspace)
 constexpr size_t kRecordBytes = kMaxCtas * sizeof(int2);
 constexpr int kUnitTiles = 3;        // what a unit's beginning and end cost, in tiles (see the split above)
-constexpr int kScan = 128;           // threads that sum up the batch's work
+constexpr int kScan = 128;           // threads that sum up a large batch's work
+constexpr int kParts = 16;           // parts of units in shared memory: the producer is fewer than 8 tiles ahead
 constexpr float kTop = 10.f;    // log2 of a row's largest weight x value scale when R is set
 constexpr float kLimit = 15.f;  // and where it is raised
 
@@ -71,7 +72,7 @@ struct Cfg {
   static constexpr int kPRow = NQ == 32 ? 128 : 64;           // bytes of a row of P^T
   static constexpr int kPBytes = kTile * kPRow * (kWide ? 1 : 3);
   static constexpr int kOCols = kWide ? 3 * NQ : NQ;          // TMEM columns of O
-  static constexpr int kStatic = NQ == 64 ? 4608 : 3584;      // static shared memory, at most
+  static constexpr int kStatic = NQ == 64 ? 5632 : NQ == 32 ? 4352 : 3456;  // static shared memory, at most
   static constexpr int kBudget = 113 * 1024 - 1024 - kStatic;  // two CTAs an SM; 1 KB to align
   static constexpr int kSlots0 = (kBudget - kQBytes - kPBytes) / kSlotBytes;
   static constexpr int kSlots = kSlots0 > 10 ? 10 : kSlots0;
@@ -157,6 +158,23 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Two fp16 to two e4m3 codes (nearest even) and back.
+__device__ __forceinline__ uint32_t e4m3x2_of(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(codes)));
+  return r;
+}
+
 // Reduce N values over the warp's lanes: every lane i mod N gets the result of v[i] (v is destroyed).
 template <int N, class Op>
 __device__ __forceinline__ float reduce_transposed(float (&v)[N], int lane, Op op) {
@@ -224,7 +242,23 @@ __device__ __forceinline__ long long seq_work(const Kv8AttnArgs& a, const Seq& q
   return q.tiles == 0 ? 0 : static_cast<long long>(a.kv.n_kv_heads) * q.nqt * (q.tiles + kUnitTiles);
 }
 
-// A CTA's piece [lo, hi) of the line of tiles, walked unit by unit by every role alike.
+// a / b for a >= 0, b > 0 (almost always of 31 bits).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 31) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
+// A part of a unit as the producer hands it to the other roles.
+struct Part {
+  int n;             // keys of the sequence
+  int t0, t1;        // the part's tiles; t1 = 0: there is no further part
+  int tiles;         // of the unit
+  int h, r0, cols;   // key head; the unit's first row and its rows
+  int cub, s, cus;   // the sequence's places
+  int c_last;        // the CTA that has the unit's last tile
+};
+
+// A CTA's piece [lo, hi) of the line of tiles, walked unit by unit (by the producer).
 template <int NQ>
 struct Walk {
   const Kv8AttnArgs& a;
@@ -244,7 +278,7 @@ struct Walk {
       q = load_seq<NQ>(a, ++b);
       w = seq_work<NQ>(a, q);
     }
-    const int x = static_cast<int>((pos - base) / (q.tiles + kUnitTiles));  // unit of the sequence
+    const int x = static_cast<int>(quotient(pos - base, q.tiles + kUnitTiles));  // unit of the sequence
     h = x / q.nqt;
     qt = x % q.nqt;
     u0 = base + static_cast<long long>(x) * (q.tiles + kUnitTiles) + kUnitTiles;
@@ -270,15 +304,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
   __shared__ uint64_t scale_bar[kScaleSlots], drain_bar;
   __shared__ uint32_t tmem_sh;
   __shared__ __align__(16) float scales[kScaleSlots][2][8];  // K, V: two pages of four groups
+  __shared__ Part part_sh[kParts];
+  __shared__ uint64_t part_bar[kParts];
   // of each row: -R; what the sums so far are multiplied by where R is raised; the sum l and 1 / l
-  __shared__ __align__(16) float nref_sh[NQ], alpha_sh[NQ], l_sh[NQ], inv_sh[NQ];
+  // (two of what the end of a unit still reads when the next has begun)
+  __shared__ __align__(16) float nref_sh[2][NQ], alpha_sh[NQ], l_sh[NQ], inv_sh[NQ];
   __shared__ float red_sh[4][NQ];
-  __shared__ long long row_sh[NQ];  // row x head of the output
+  __shared__ int row_sh[2][NQ];  // row of the output
   __shared__ float amax_sh[4 * C::kGroups];
   __shared__ long long seg_sh[kScan + 1];
-  __shared__ long long start_base;
-  __shared__ int start_b;
-  __shared__ Seq start_q;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
   const BatchArgs& bt = a.bt;
@@ -292,6 +326,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       mbar_init(&s_free[i], 4 * C::kGroups);
     }
     for (int i = 0; i < kScaleSlots; ++i) mbar_init(&scale_bar[i], 1);
+    for (int i = 0; i < kParts; ++i) mbar_init(&part_bar[i], 1);
     mbar_init(&drain_bar, 1);
     mbar_init(&p_ready, C::kSoft);
     mbar_init(&pv_done, 1);
@@ -304,62 +339,101 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
   griddep_wait();
   griddep_launch_dependents();
 
-  // ---- the line of tiles: its length, and where this CTA's piece begins
-  const int per = (bt.batch + kScan - 1) / kScan;
-  Seq q0;  // the thread's only sequence, where it has but one
-  if (tid < kScan) {
-    long long w = 0;
-    for (int b = tid * per; b < min(bt.batch, (tid + 1) * per); ++b) {
-      const Seq q = load_seq<NQ>(a, b);
-      q0 = q;
-      if (q.bad && blockIdx.x == 0) report_error(bt.err, kErrBadShape);
-      w += seq_work<NQ>(a, q);
+  // ---- the line of tiles: its length T, and the sequence in which this CTA's piece begins (for the producer warp)
+  const int cta = blockIdx.x;
+  long long T = 0, len = 1, lo = 0, start_base = 0;
+  int start_b = 0;
+  auto cut = [&]() {  // into pieces of len
+    len = quotient(T + gridDim.x - 1, gridDim.x);
+    lo = min(cta * len, T);
+  };
+  if (bt.batch <= kScan) {
+    if (warp == C::kProducerWarp) {  // up to four sequences a lane
+      constexpr int kEach = kScan / 32;
+      const int per = (bt.batch + 31) / 32;
+      long long w[kEach], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        w[i] = 0;
+        const int b = lane * per + i;
+        if (i >= per || b >= bt.batch) continue;
+        const Seq q = load_seq<NQ>(a, b);
+        if (q.bad && cta == 0) report_error(bt.err, kErrBadShape);
+        w[i] = seq_work<NQ>(a, q);
+        sum += w[i];
+      }
+      long long incl = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      T = __shfl_sync(0xffffffffu, incl, 31);
+      cut();
+      long long at = incl - sum;
+      int b = lane * per;
+      const unsigned mine = __ballot_sync(0xffffffffu, at <= lo && lo < incl);
+      bool passing = true;  // the lane's sequences that end at or before lo
+#pragma unroll
+      for (int i = 0; i < kEach - 1; ++i) {
+        passing = passing && lo >= at + w[i];
+        if (passing) {
+          at += w[i];
+          ++b;
+        }
+      }
+      const int src = mine != 0 ? __ffs(mine) - 1 : 0;
+      start_b = __shfl_sync(0xffffffffu, b, src);
+      start_base = __shfl_sync(0xffffffffu, at, src);
     }
-    seg_sh[tid] = w;
+  } else {
+    const int per = (bt.batch + kScan - 1) / kScan;
+    if (tid < kScan) {
+      long long w = 0;
+      for (int b = tid * per; b < min(bt.batch, (tid + 1) * per); ++b) {
+        const Seq q = load_seq<NQ>(a, b);
+        if (q.bad && cta == 0) report_error(bt.err, kErrBadShape);
+        w += seq_work<NQ>(a, q);
+      }
+      seg_sh[tid] = w;
+    }
+    __syncthreads();
+    if (warp == C::kProducerWarp) {
+      constexpr int kEach = kScan / 32;
+      long long w[kEach], sum = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        w[i] = seg_sh[lane * kEach + i];
+        sum += w[i];
+      }
+      long long incl = sum;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+      }
+      T = __shfl_sync(0xffffffffu, incl, 31);
+      cut();
+      long long at = incl - sum;
+      const unsigned mine = __ballot_sync(0xffffffffu, at <= lo && lo < incl);
+      int b = lane * kEach * per;
+      if (at <= lo && lo < incl) {
+#pragma unroll 1
+        for (;; ++b) {
+          const long long next = at + seq_work<NQ>(a, load_seq<NQ>(a, b));
+          if (lo < next) break;
+          at = next;
+        }
+      }
+      const int src = mine != 0 ? __ffs(mine) - 1 : 0;
+      start_b = __shfl_sync(0xffffffffu, b, src);
+      start_base = __shfl_sync(0xffffffffu, at, src);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_sh;
-  if (warp == 0) {
-    constexpr int kEach = kScan / 32;
-    long long v[kEach], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      v[i] = sum;
-      sum += seg_sh[lane * kEach + i];
-    }
-    long long incl = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += o;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) seg_sh[lane * kEach + i] = v[i] + incl - sum;
-    if (lane == 31) seg_sh[kScan] = incl;
-  }
-  __syncthreads();
-  const long long T = seg_sh[kScan];
-  const int n_cta = static_cast<int>(min(static_cast<long long>(gridDim.x), T));  // pieces: at least a tile each
-  const int cta = blockIdx.x;
-  const long long lo = cta < n_cta ? cta * T / n_cta : 0, hi = cta < n_cta ? (cta + 1) * T / n_cta : 0;
-  if (tid < kScan && lo < hi && seg_sh[tid] <= lo && lo < seg_sh[tid + 1]) {
-    long long at = seg_sh[tid];
-    int b = tid * per;
-    for (; per > 1; ++b) {
-      q0 = load_seq<NQ>(a, b);
-      const long long w = seq_work<NQ>(a, q0);
-      if (lo < at + w) break;
-      at += w;
-    }
-    start_b = b;
-    start_q = q0;
-    start_base = at;
-  }
-  __syncthreads();
-  Walk<NQ> walk(a, start_b, start_q, start_base, lo, hi);
   // the ring's order: K of the next tile before V of this one, which is needed later (the last tile's V leaves the place
   // of the K that does not follow empty)
   auto k_index = [](int n) { return n == 0 ? 0 : 2 * n - 1; };
@@ -370,8 +444,24 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     // ------------------------------------------------------------ TMA producer
     // The copies of a tile are issued by lanes of one instruction each (K or V: a page a lane; the four pieces of scales):
     // a single thread that issued them one after the other was the slowest part of the CTA.
-    int slot = 0, phase = 0, issued = 0, nt = 0;
+    const long long hi = min(lo + len, T);
+    Walk<NQ> walk(a, start_b, lo < hi ? load_seq<NQ>(a, start_b) : Seq{}, start_base, lo, hi);
+    int slot = 0, phase = 0, issued = 0, nt = 0, n_parts = 0;
     bool ok = true;
+    auto hand_over = [&](bool any) {  // the walk's part, or that there is no more
+      if (lane == 0) {
+        Part& p = part_sh[n_parts % kParts];
+        p.t1 = 0;
+        if (any) {
+          const Seq& q = walk.q;
+          const int r0 = walk.qt * NQ;
+          p = Part{q.n, walk.t0, walk.t1, q.tiles, walk.h, r0, min(NQ, q.rows * G - r0), q.cub, q.s, q.cus,
+                   static_cast<int>(quotient(walk.u0 + q.tiles - 1, len))};
+        }
+        mbar_arrive(&part_bar[n_parts % kParts]);
+      }
+      ++n_parts;
+    };
     uint64_t once, again;  // keys that no other unit reads, and others
     once = l2_evict_first_policy();
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(again));
@@ -402,6 +492,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     int y_last = 0, pages_last = 0;  // the last tile, whose V is still to be asked for
     uint64_t policy_last = again;
     bool have = walk.next();
+    hand_over(have);
     int ids_next = have ? page_ids(bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages, 2 * walk.t0, walk.q.npages) : 0;
     while (have && ok) {
       // this part's values, while the walk goes on to the next: its page ids and rows of q are asked for a part ahead
@@ -410,6 +501,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       const uint64_t policy = walk.q.nqt > 1 ? again : once;
       int ids = ids_next, first = 2 * t0;
       have = walk.next();
+      hand_over(have);
       if (have) {
         ids_next = page_ids(bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages, 2 * walk.t0, walk.q.npages);
         for (int c = lane; c < NQ; c += 32) {
@@ -490,13 +582,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         umma_commit(&empty_bar[s]);
         umma_commit(&pv_done);
       };
-      while (ok && walk.next()) {
+      for (;; ++unit) {
         if (pending) {
           issue_pv(nt - 1);
           pending = false;
         }
-        wait(&q_ready, unit);
-        for (int t = walk.t0; t < walk.t1 && ok; ++t, ++nt) {
+        if (!wait(&part_bar[unit % kParts], unit / kParts)) break;
+        const int t0 = part_sh[unit % kParts].t0, t1 = part_sh[unit % kParts].t1;
+        if (t1 == 0 || !wait(&q_ready, unit)) break;
+        for (int t = t0; t < t1 && ok; ++t, ++nt) {
           const int i = k_index(nt), s = i % C::kSlots, buf = nt & 1;
           if (!wait(&full_bar[s], i / C::kSlots)) break;
           if (nt >= 2 && !wait(&s_free[buf], (nt >> 1) - 1)) break;
@@ -511,11 +605,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
           umma_commit(&s_full[buf]);
           if (pending) issue_pv(nt - 1);
           pending = true;
-          fresh = t == walk.t0;
+          fresh = t == t0;
         }
-        ++unit;
       }
-      if (pending && ok) issue_pv(nt - 1);
       // the softmax warps wait for the last S and P V, the producer for the releases; where a wait gave up, the
       // products that were issued end before the CTA does
       if (!ok) {
@@ -539,34 +631,76 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       }
     };
     int2 record = make_int2(0, 0);
-    float* const parts = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kRecordBytes);
-    while (walk.next()) {
-      const Seq& q = walk.q;
-      const int r0 = walk.qt * NQ, cols = min(NQ, q.rows * G - r0);  // rows of this unit
-      // ---- q: its largest magnitude, two e4m3 parts
-      float f_q;
-      {
-        constexpr int kPer = C::kSoft / NQ, kVec = D / 8 / kPer;  // threads and 16-byte pieces a row
-        const int c = tid / kPer, piece = (tid % kPer) * kVec, r = r0 + c;
-        uint4 x[kVec];
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (q.cub + r / G) * a.q_row +
-                                   static_cast<size_t>(walk.h * G + r % G) * D;
+    float f_q = 0.f;
+
+    // The rows of q of part u: asked for while the last tile of the part before is still to be done (in narrow units, where
+    // there are registers for it).
+    constexpr int kPer = C::kSoft / NQ, kVec = D / 8 / kPer;  // threads and 16-byte pieces a row
+    constexpr bool kAhead = NQ <= 32;
+    const int q_row = tid / kPer, q_piece = (tid % kPer) * kVec;
+    uint4 qv[kVec];
+    auto ask_q = [&](int u) {
+      wait(&part_bar[u % kParts], u / kParts);
+      const Part& part = part_sh[u % kParts];
+      const bool on = !dead && part.t1 > 0 && q_row < part.cols;
+      const int r = part.r0 + q_row, i = r / G;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (part.cub + i) * a.q_row +
+                                 static_cast<size_t>(part.h * G + r - i * G) * D;
+#pragma unroll
+      for (int k = 0; k < kVec; ++k)
+        qv[k] = on ? __ldg(reinterpret_cast<const uint4*>(src) + q_piece + k) : make_uint4(0, 0, 0, 0);
+    };
+
+    // One turn: the next part's q, then the end of the part before it, then the next part's tiles.  So the tensor core
+    // has the next scores to work on while the end goes on.
+    uint64_t l[kCols / 2];  // sums of pairs of rows over this thread's keys
+    for (int u = 0;; ++u) {
+      const Part& part = part_sh[u % kParts];
+      const int par = u & 1;
+      if (!kAhead || u == 0) ask_q(u);
+      const bool have = !soft_any<C::kSoft>(dead || part.t1 == 0);  // (the same for all, whoever gave up)
+      if (u > 0) {
+        float v[kCols];
+#pragma unroll
+        for (int c = 0; c < kCols / 2; ++c) {
+          const float2 p = unpack2(l[c]);
+          v[2 * c] = p.x;
+          v[2 * c + 1] = p.y;
+        }
+        const float sum = reduce_transposed(v, lane, [](float p, float r) { return p + r; });
+        if (lane < kCols) red_sh[warp & 3][col0 + lane] = sum;
+      }
+      if (have) {
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-          x[i] = c < cols ? __ldg(reinterpret_cast<const uint4*>(src) + piece + i) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int i = 0; i < kVec; ++i)
+          m = max_u16x2(m, max_u16x2(max_u16x2(qv[i].x & 0x7fff7fffu, qv[i].y & 0x7fff7fffu),
+                                     max_u16x2(qv[i].z & 0x7fff7fffu, qv[i].w & 0x7fff7fffu)));
+        m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+        if (m >= 0x7f80u) {  // values that are not finite take no part, and make their row, and no other, not a number
+          m = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {  // values that are not finite take no part
-            const uint32_t u = w[k] & 0x7fff7fffu;
-            m = max(m, (u & 0xffffu) < 0x7f80u ? u & 0xffffu : 0u);
-            m = max(m, (u >> 16) < 0x7f80u ? u >> 16 : 0u);
+          for (int i = 0; i < kVec; ++i) {
+            uint32_t* const w = reinterpret_cast<uint32_t*>(&qv[i]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t lo = w[k] & 0x7fffu, hi = (w[k] >> 16) & 0x7fffu;
+              m = max(m, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+              w[k] |= (lo < 0x7f80u ? 0u : 0x7fu) | (hi < 0x7f80u ? 0u : 0x7f0000u);
+            }
           }
+          m = __reduce_max_sync(0xffffffffu, m);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (lane == 0) amax_sh[warp] = __uint_as_float(m << 16);
-        soft_sync();  // (and the last unit's readers of the arrays below are done)
+        if (tid < NQ) {
+          const int i = (part.r0 + tid) / G;
+          row_sh[par][tid] = a.full_rows ? part.cus + part.s + i : part.cub + i;
+          nref_sh[par][tid] = 0.f;
+        }
+      }
+      soft_sync();
+      if (have) {
+        // q in two e4m3 parts
         float amax = amax_sh[0];
 #pragma unroll
         for (int i = 1; i < 4 * C::kGroups; ++i) amax = fmaxf(amax, amax_sh[i]);
@@ -576,55 +710,102 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         e = max(e, -118);
         const float down = __int_as_float((127 - e) << 23);
         f_q = a.scale_log2 * __int_as_float((127 + e) << 23);
+        const uint64_t down2 = pack2(down, down);
 #pragma unroll
-        for (int i = 0; i < kVec; i += 1) {
-          const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int i = 0; i < kVec; ++i) {
+          const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
           uint32_t hi2[2], lo2[2];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float v[2] = {__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)};
-            float d2[2];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              d2[z] = v[z] * down;
-              if (!(fabsf(v[z]) < INFINITY)) d2[z] = __int_as_float(0x7fffffff);  // not a number in its row alone
-            }
-            const uint16_t hc = cvt_e4m3x2(d2[0], d2[1]);
-            uint32_t h16;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h16) : "h"(hc));
-            const float2 hf = __half22float2(*reinterpret_cast<__half2*>(&h16));
-            const uint16_t lc = cvt_e4m3x2(d2[0] - hf.x, d2[1] - hf.y);
+            const float2 v = unpack2(mul2(pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u)), down2));
+            // 8 bits fit fp16's 11, down to 2^-24 of a unit whose last e4m3 step is 2^-9
+            const uint32_t h = pack_f16x2(v.x, v.y);
+            const uint32_t hc = e4m3x2_of(h), back = f16x2_of(hc);
+            const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&back));
+            const uint32_t lc = e4m3x2_of(*reinterpret_cast<const uint32_t*>(&rest));
             if (k & 1) {
-              hi2[k >> 1] |= static_cast<uint32_t>(hc) << 16;
-              lo2[k >> 1] |= static_cast<uint32_t>(lc) << 16;
+              hi2[k >> 1] |= hc << 16;
+              lo2[k >> 1] |= lc << 16;
             } else {
               hi2[k >> 1] = hc;
               lo2[k >> 1] = lc;
             }
           }
-          const int byte = (piece + i) * 8;  // eight codes of row c
-          const uint32_t at = q_base + swz<D>(c, byte >> 4) + (byte & 8);
+          const int byte = (q_piece + i) * 8;  // eight codes of row q_row
+          const uint32_t at = q_base + swz<D>(q_row, byte >> 4) + (byte & 8);
           asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(hi2[0]), "r"(hi2[1]) : "memory");
           asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + NQ * D), "r"(lo2[0]), "r"(lo2[1]) : "memory");
         }
         fence_async_smem();
         mbar_arrive(&q_ready);
+      }
+      if (u > 0) {
+        // ---- the end of the part before: l over all keys, then O / l, or (O, R, l) to the workspace
+        const Part& done = part_sh[(u - 1) % kParts];
+        const int cols = done.cols, was = par ^ 1;
         if (tid < NQ) {
-          const int rr = r0 + tid, i = rr / G;
-          const long long row = a.full_rows ? static_cast<long long>(q.cus) + q.s + i : q.cub + i;
-          row_sh[tid] = row * a.n_heads + walk.h * G + rr % G;
-          nref_sh[tid] = 0.f;
+          const float sum = (red_sh[0][tid] + red_sh[1][tid]) + (red_sh[2][tid] + red_sh[3][tid]);
+          l_sh[tid] = sum;
+          inv_sh[tid] = 1.f / sum;
+        }
+        wait(&pv_done, nt - 1);
+        soft_sync();
+        tc_fence_after();
+        float o[kCols];  // column `key` of this thread's rows
+        tmem_load(tm_o, o);
+        if (C::kWide) {
+#pragma unroll 1
+          for (int z = 1; z < 3; ++z) {
+            float more[kCols];
+            tmem_load(tm_o + z * NQ, more);
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) o[c] += more[c];
+          }
+        }
+        const bool began = done.t0 == 0, whole = began && done.t1 == done.tiles;
+        const int head = done.h * G, r0 = done.r0;
+        if (whole) {
+          __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o) + key;
+          if (a.lse != nullptr && tid < cols)
+            a.lse[static_cast<size_t>(row_sh[was][tid]) * a.n_heads + head + (r0 + tid) % G] =
+                (log2f(l_sh[tid]) - nref_sh[was][tid]) * attn::kLn2;
+          if (key < D) {
+            int j = (r0 + col0) % G;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+              if (col0 + c < cols)
+                out[(static_cast<size_t>(row_sh[was][col0 + c]) * a.n_heads + head + j) * D] = __float2bfloat16(o[c] * inv_sh[col0 + c]);
+              if (++j == G) j = 0;
+            }
+          }
+        } else {
+          float* const mine = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kRecordBytes) +
+                              (static_cast<size_t>(cta) * 2 + (began ? 1 : 0)) * C::kPartFloats;
+          if (key < D) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c)
+              if (col0 + c < cols) mine[(col0 + c) * D + key] = o[c];
+          }
+          if (tid < cols) {
+            mine[NQ * D + tid] = -nref_sh[was][tid];
+            mine[NQ * (D + 1) + tid] = l_sh[tid];
+            if (began)
+              reinterpret_cast<long long*>(mine + NQ * (D + 2))[tid] =
+                  static_cast<long long>(row_sh[was][tid]) * a.n_heads + head + (r0 + tid) % G;
+          }
+          if (began) record = make_int2(done.c_last - cta + 1, cols);
         }
       }
-      uint64_t l[kCols / 2];  // sums of pairs of rows over this thread's keys
+      if (!have) break;
 #pragma unroll
       for (int c = 0; c < kCols / 2; ++c) l[c] = 0;
-      soft_sync();  // nref_sh
+      const int t0 = part.t0, t1 = part.t1, n = part.n;
 
-      for (int t = walk.t0; t < walk.t1; ++t, ++nt) {
+      for (int t = t0; t < t1; ++t, ++nt) {
         const int buf = nt & 1;
-        const bool first = t == walk.t0;
-        const int valid = q.n - t * kTile;  // keys of this tile that there are
+        const bool first = t == t0;
+        if (kAhead && t + 1 == t1) ask_q(u + 1);
+        const int valid = n - t * kTile;  // keys of this tile that there are
         wait(&scale_bar[nt % kScaleSlots], nt / kScaleSlots);
         const float sv = key < valid ? scales[nt % kScaleSlots][1][key / kKv8Group] : 0.f;
         const float f = key < valid ? scales[nt % kScaleSlots][0][key / kKv8Group] * f_q : 0.f;
@@ -639,7 +820,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
             const uint64_t f2 = pack2(f, f);
 #pragma unroll
             for (int c = 0; c < kCols; c += 4) {  // x = f S - R
-              const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&nref_sh[col0 + c]);
+              const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&nref_sh[par][col0 + c]);
               x[c / 2] = fma2(pack2(s[c], s[c + 1]), f2, r.x);
               x[c / 2 + 1] = fma2(pack2(s[c + 2], s[c + 3]), f2, r.y);
             }
@@ -673,7 +854,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
             const float top = fmaxf(fmaxf(red_sh[0][tid], red_sh[1][tid]), fmaxf(red_sh[2][tid], red_sh[3][tid]));
             float up = 0.f;  // what R grows by
             if ((first || top > kLimit) && fabsf(top) < INFINITY) up = top - kTop;
-            nref_sh[tid] -= up;
+            nref_sh[par][tid] -= up;
             alpha_sh[tid] = first ? 0.f : exp2f(-up);
           }
           if (!first) wait(&pv_done, nt - 1);
@@ -747,66 +928,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         tc_fence_before();
         fence_async_smem();
         mbar_arrive(&p_ready);
-      }
-
-      // ---- the end of this part of the unit
-      {
-        float u[kCols];
-#pragma unroll
-        for (int c = 0; c < kCols / 2; ++c) {
-          const float2 v = unpack2(l[c]);
-          u[2 * c] = v.x;
-          u[2 * c + 1] = v.y;
-        }
-        const float sum = reduce_transposed(u, lane, [](float p, float r) { return p + r; });
-        if (lane < kCols) red_sh[warp & 3][col0 + lane] = sum;
-      }
-      wait(&pv_done, nt - 1);
-      soft_sync();
-      tc_fence_after();
-      if (tid < NQ) {
-        const float sum = (red_sh[0][tid] + red_sh[1][tid]) + (red_sh[2][tid] + red_sh[3][tid]);
-        l_sh[tid] = sum;
-        inv_sh[tid] = 1.f / sum;
-      }
-      soft_sync();
-      float o[kCols];  // column `key` of this thread's rows
-      tmem_load(tm_o, o);
-      if (C::kWide) {
-#pragma unroll 1
-        for (int z = 1; z < 3; ++z) {
-          float more[kCols];
-          tmem_load(tm_o + z * NQ, more);
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) o[c] += more[c];
-        }
-      }
-      const bool began = walk.t0 == 0, goes_on = walk.t1 < q.tiles;
-      if (began && !goes_on) {
-        __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o);
-        if (a.lse != nullptr && tid < cols) a.lse[row_sh[tid]] = (log2f(l_sh[tid]) - nref_sh[tid]) * attn::kLn2;
-        if (key < D) {
-#pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            if (col0 + c < cols) out[row_sh[col0 + c] * D + key] = __float2bfloat16(o[c] * inv_sh[col0 + c]);
-        }
-        continue;
-      }
-      // ---- a piece: (O, R, l) to the workspace
-      float* const mine = parts + (static_cast<size_t>(cta) * 2 + (began ? 1 : 0)) * C::kPartFloats;
-      if (key < D) {
-#pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          if (col0 + c < cols) mine[(col0 + c) * D + key] = o[c];
-      }
-      if (tid < cols) {
-        mine[NQ * D + tid] = -nref_sh[tid];
-        mine[NQ * (D + 1) + tid] = l_sh[tid];
-        if (began) reinterpret_cast<long long*>(mine + NQ * (D + 2))[tid] = row_sh[tid];
-      }
-      if (began && goes_on && tid == 0) {
-        const int c_last = static_cast<int>(((walk.u0 + q.tiles) * n_cta - 1) / T);
-        record = make_int2(c_last - cta + 1, cols);
       }
     }
     if (tid == 0) static_cast<int2*>(a.ws)[cta] = record;
