@@ -27,8 +27,8 @@
 //
 // Roles of a CTA's warps: groups of four softmax warps (TMEM lane = key, then = column of
 // O^T; 16 rows to a group), one TMA producer, one MMA issuer.  K and V tiles share one ring of 16 KB slots (8 KB for
-// d = 64); the scores are double-buffered in TMEM, so the tensor core runs S of the next
-// tile while the softmax works.  Two CTAs an SM cover each other's serial parts.
+// d = 64).  The tensor core has the next tile's S done, from the moment the scores are in
+// registers, while the softmax works.  Two CTAs an SM cover each other's serial parts.
 //
 // Split: the tiles of all units form one line, cut into as many equal pieces as CTAs
 // (or fewer, where there are few tiles): a ragged batch or one long sequence loads all
@@ -48,7 +48,6 @@ namespace {
 
 constexpr int kTile = 128;  // keys per tile: two pages
 constexpr int kCtasPerSm = 2;
-constexpr uint32_t kTmemCols = 256;  // of a CTA: two fit an SM's 512
 constexpr int kScaleSlots = 8;       // tiles whose scales are in shared memory
 constexpr int kMaxCtas = 1024;       // of a launch (records of the workspace)
 constexpr size_t kRecordBytes = kMaxCtas * sizeof(int2);
@@ -64,14 +63,15 @@ struct Cfg {
   static constexpr int kCols = NQ == 64 ? 32 : 16;
   static constexpr int kGroups = NQ / kCols;
   static constexpr int kSoft = 128 * kGroups;  // softmax threads
+  static constexpr uint32_t kTmemCols = 2 * NQ;  // S^T, O^T
   static constexpr int kProducerWarp = 4 * kGroups, kMmaWarp = kProducerWarp + 1;
   static constexpr int kThreads = kSoft + 64;
   static constexpr int kSlotBytes = kTile * D;
   static constexpr int kQBytes = NQ * D * 2;                  // hi, lo
-  static constexpr bool kWide = NQ <= 32;                     // the three parts side by side in one row
-  static constexpr int kPRow = NQ == 32 ? 128 : 64;           // bytes of a row of P^T
-  static constexpr int kPBytes = kTile * kPRow * (kWide ? 1 : 3);
-  static constexpr int kOCols = kWide ? 3 * NQ : NQ;          // TMEM columns of O
+  // P^T's rows of 64 or 128 bytes: up to NQ = 32 the three parts of a weight side by side, else three planes.
+  static constexpr bool kPlanes = NQ == 64;
+  static constexpr int kPRow = NQ == 32 ? 128 : 64;
+  static constexpr int kPBytes = kTile * kPRow * (kPlanes ? 3 : 1);
   static constexpr int kStatic = NQ == 64 ? 5632 : NQ == 32 ? 4352 : 3456;  // static shared memory, at most
   static constexpr int kBudget = 113 * 1024 - 1024 - kStatic;  // two CTAs an SM; 1 KB to align
   static constexpr int kSlots0 = (kBudget - kQBytes - kPBytes) / kSlotBytes;
@@ -79,7 +79,6 @@ struct Cfg {
   static constexpr int kDynSmem = kSlots * kSlotBytes + kQBytes + kPBytes + 1024;
   static_assert(kSlots >= 4, "a tile's K and V, and the next tile's");
   static_assert(kSlots / 2 + 2 < kScaleSlots, "scales stay until the softmax has read them");
-  static_assert(2 * NQ + kOCols <= static_cast<int>(kTmemCols), "TMEM columns");
   static constexpr size_t kPartFloats = static_cast<size_t>(NQ) * (D + 4);  // O, R, l, rows
 };
 
@@ -94,8 +93,7 @@ __device__ __forceinline__ uint64_t desc_rows(uint32_t saddr) {
   d |= static_cast<uint64_t>(1) << 46;             // descriptor version for tcgen05
   d |= static_cast<uint64_t>(ROW == 128 ? 2 : 4) << 61;
   return d;
-  // leading byte offset 0: no operand here has a second swizzle row along its contiguous dimension.  (V of d = 64
-  // is taken as M = 128 with the offset 0: lanes 64-127 of O^T repeat lanes 0-63 and are not read.)
+  // (V of d = 64 is taken as M = 128 with a leading offset of 0: lanes 64-127 of O^T repeat lanes 0-63 and are not read)
 }
 // kind::f8f6f4, fp32 accumulator: A e4m3, B e4m3 or e5m2; either operand K-major or MN-major.
 __host__ __device__ constexpr uint32_t idesc_f8(int m, int n, bool b_e5m2, bool mn) {
@@ -300,7 +298,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* const smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   const uint32_t ring = smem_u32(smem), p_base = ring + C::kSlots * C::kSlotBytes, q_base = p_base + C::kPBytes;
-  __shared__ uint64_t full_bar[C::kSlots], empty_bar[C::kSlots], s_full[2], s_free[2], p_ready, pv_done, q_ready;
+  __shared__ uint64_t full_bar[C::kSlots], empty_bar[C::kSlots], s_full, s_free, p_ready, pv_done, q_ready;
   __shared__ uint64_t scale_bar[kScaleSlots], drain_bar;
   __shared__ uint32_t tmem_sh;
   __shared__ __align__(16) float scales[kScaleSlots][2][8];  // K, V: two pages of four groups
@@ -321,10 +319,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 4 * C::kGroups);
-    }
+    mbar_init(&s_full, 1);
+    mbar_init(&s_free, 4 * C::kGroups);
     for (int i = 0; i < kScaleSlots; ++i) mbar_init(&scale_bar[i], 1);
     for (int i = 0; i < kParts; ++i) mbar_init(&part_bar[i], 1);
     mbar_init(&drain_bar, 1);
@@ -335,7 +331,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (warp == C::kMmaWarp) tmem_alloc(&tmem_sh, kTmemCols);
+  if (warp == C::kMmaWarp) tmem_alloc(&tmem_sh, C::kTmemCols);
   griddep_wait();
   griddep_launch_dependents();
 
@@ -556,8 +552,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t kIdescS = idesc_f8(kTile, NQ, false, false);
-      constexpr uint32_t kIdescO = idesc_f8(kTile, C::kOCols, true, true);
-      const uint32_t tm_o = tmem + 2 * NQ;
+      constexpr uint32_t kIdescO = idesc_f8(kTile, NQ, true, true);
+      const uint32_t tm_o = tmem + NQ;
       const uint64_t q_desc = desc_rows<D>(q_base), p_desc = desc_rows<C::kPRow>(p_base);
       int nt = 0, unit = 0;
       bool ok = true;
@@ -575,10 +571,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         tc_fence_after();
         const uint64_t v = desc_rows<D>(ring + s * C::kSlotBytes);  // (a step of n bytes adds n / 16 to the address field)
 #pragma unroll
-        for (int part = 0; part < (C::kWide ? 1 : 3); ++part)
+        for (int z = 0; z < 3; ++z)
 #pragma unroll
           for (int k = 0; k < kTile / 32; ++k)
-            umma_e4m3(tm_o, v + k * 2 * D, p_desc + (part * kTile + k * 32) * C::kPRow / 16, kIdescO, !fresh || part > 0 || k > 0);
+            umma_e4m3(tm_o, v + k * 2 * D, p_desc + ((C::kPlanes ? z * kTile * C::kPRow : z * NQ) + k * 32 * C::kPRow) / 16, kIdescO,
+                      !fresh || z > 0 || k > 0);
         umma_commit(&empty_bar[s]);
         umma_commit(&pv_done);
       };
@@ -591,18 +588,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         const int t0 = part_sh[unit % kParts].t0, t1 = part_sh[unit % kParts].t1;
         if (t1 == 0 || !wait(&q_ready, unit)) break;
         for (int t = t0; t < t1 && ok; ++t, ++nt) {
-          const int i = k_index(nt), s = i % C::kSlots, buf = nt & 1;
+          const int i = k_index(nt), s = i % C::kSlots;
           if (!wait(&full_bar[s], i / C::kSlots)) break;
-          if (nt >= 2 && !wait(&s_free[buf], (nt >> 1) - 1)) break;
+          if (nt > 0 && !wait(&s_free, nt - 1)) break;
           tc_fence_after();
           const uint64_t k8 = desc_rows<D>(ring + s * C::kSlotBytes);
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
-              umma_e4m3(tmem + buf * NQ, k8 + k * 2, q_desc + (part * NQ * D + k * 32) / 16, kIdescS, part > 0 || k > 0);
+              umma_e4m3(tmem, k8 + k * 2, q_desc + (part * NQ * D + k * 32) / 16, kIdescS, part > 0 || k > 0);
           umma_commit(&empty_bar[s]);
-          umma_commit(&s_full[buf]);
+          umma_commit(&s_full);
           if (pending) issue_pv(nt - 1);
           pending = true;
           fresh = t == t0;
@@ -620,7 +617,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     constexpr int kCols = C::kCols;
     const int key = tid & 127, grp = tid >> 7, col0 = grp * kCols;  // this thread's key of a tile (column of O^T), and rows
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tm_o = tmem + 2 * NQ + lane_base + col0;
+    const uint32_t tm_s = tmem + lane_base + col0, tm_o = tm_s + NQ;
     auto soft_sync = []() { named_barrier(1, C::kSoft); };
     int nt = 0;
     bool dead = false;
@@ -753,15 +750,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         tc_fence_after();
         float o[kCols];  // column `key` of this thread's rows
         tmem_load(tm_o, o);
-        if (C::kWide) {
-#pragma unroll 1
-          for (int z = 1; z < 3; ++z) {
-            float more[kCols];
-            tmem_load(tm_o + z * NQ, more);
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) o[c] += more[c];
-          }
-        }
         const bool began = done.t0 == 0, whole = began && done.t1 == done.tiles;
         const int head = done.h * G, r0 = done.r0;
         if (whole) {
@@ -802,7 +790,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       const int t0 = part.t0, t1 = part.t1, n = part.n;
 
       for (int t = t0; t < t1; ++t, ++nt) {
-        const int buf = nt & 1;
         const bool first = t == t0;
         if (kAhead && t + 1 == t1) ask_q(u + 1);
         const int valid = n - t * kTile;  // keys of this tile that there are
@@ -810,24 +797,22 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         const float sv = key < valid ? scales[nt % kScaleSlots][1][key / kKv8Group] : 0.f;
         const float f = key < valid ? scales[nt % kScaleSlots][0][key / kKv8Group] * f_q : 0.f;
         const float lv = sv > 0.f ? __log2f(sv) : attn::neg_inf();
-        wait(&s_full[buf], nt >> 1);
+        wait(&s_full, nt);
         tc_fence_after();
         uint64_t x[kCols / 2];
         for (bool raised = false;; raised = true) {
-          {
-            float s[kCols];
-            tmem_load(tmem + lane_base + buf * NQ + col0, s);
-            const uint64_t f2 = pack2(f, f);
+          const uint64_t f2 = pack2(f, f);
+          float s[kCols];
+          tmem_load(tm_s, s);
 #pragma unroll
-            for (int c = 0; c < kCols; c += 4) {  // x = f S - R
-              const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&nref_sh[par][col0 + c]);
-              x[c / 2] = fma2(pack2(s[c], s[c + 1]), f2, r.x);
-              x[c / 2 + 1] = fma2(pack2(s[c + 2], s[c + 3]), f2, r.y);
-            }
-            if (key >= valid) {
+          for (int c = 0; c < kCols; c += 4) {  // x = f S - R
+            const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&nref_sh[par][col0 + c]);
+            x[c / 2] = fma2(pack2(s[c], s[c + 1]), f2, r.x);
+            x[c / 2 + 1] = fma2(pack2(s[c + 2], s[c + 3]), f2, r.y);
+          }
+          if (key >= valid) {
 #pragma unroll
-              for (int c = 0; c < kCols / 2; ++c) x[c] = pack2(attn::neg_inf(), attn::neg_inf());
-            }
+            for (int c = 0; c < kCols / 2; ++c) x[c] = pack2(attn::neg_inf(), attn::neg_inf());
           }
           if (raised) break;
           if (!first) {
@@ -863,28 +848,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < kCols / 2; ++c) l[c] = mul2(l[c], pack2(alpha_sh[col0 + 2 * c], alpha_sh[col0 + 2 * c + 1]));
-#pragma unroll 1
-            for (int z = 0; z < (C::kWide ? 3 : 1); ++z) {
-              float o[kCols];
-              tmem_load(tm_o + z * NQ, o);
+            float o[kCols];
+            tmem_load(tm_o, o);
 #pragma unroll
-              for (int c = 0; c < kCols; ++c) o[c] *= alpha_sh[col0 + c];
-              tmem_store(tm_o + z * NQ, o);
-            }
+            for (int c = 0; c < kCols; ++c) o[c] *= alpha_sh[col0 + c];
+            tmem_store(tm_o, o);
             tmem_st_wait();
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[buf]);  // the scores are in registers
-        const uint64_t sv2 = pack2(sv, sv);
-#pragma unroll
-        for (int c = 0; c < kCols / 2; ++c) {
-          const float2 v = unpack2(x[c]);
-          const uint64_t p = pack2(attn::fast_exp2(v.x), attn::fast_exp2(v.y));
-          l[c] = add2(l[c], p);
-          x[c] = mul2(p, sv2);
-        }
+        if (lane == 0) mbar_arrive(&s_free);  // the scores are in registers
         if (nt > 0) wait(&pv_done, nt - 1);  // P's buffer is free
         if (valid < kTile) {                  // what lies behind the end must not meet a weight, not even 0
           const int vi = v_index(nt);
@@ -894,6 +868,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
             for (int i = 0; i < D / 16; ++i) st_shared_v4(ring + (vi % C::kSlots) * C::kSlotBytes + tid * D + i * 16, 0, 0, 0, 0);
           }
         }
+        const uint64_t sv2 = pack2(sv, sv);
 #pragma unroll
         for (int c0 = 0; c0 < kCols; c0 += 16) {
           uint32_t part[3][4];
@@ -902,8 +877,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
             uint32_t w[3][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const float2 v = unpack2(x[c0 / 2 + 2 * j + k]);
-              const uint32_t h = pack_f16x2(v.x, v.y);
+              const int c = c0 / 2 + 2 * j + k;
+              const float2 v = unpack2(x[c]);
+              const uint64_t p = pack2(attn::fast_exp2(v.x), attn::fast_exp2(v.y));
+              l[c] = add2(l[c], p);
+              const float2 w2 = unpack2(mul2(p, sv2));
+              const uint32_t h = pack_f16x2(w2.x, w2.y);
               // e5m2 is fp16's upper byte: round to it by adding half of the lower one
               const uint32_t hi8 = (h + 0x00800080u) & 0xff00ff00u;
               const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&hi8));
@@ -920,8 +899,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
           const int chunk = (col0 + c0) / 16;
 #pragma unroll
           for (int z = 0; z < 3; ++z) {
-            const uint32_t at = C::kWide ? p_base + swz<C::kPRow>(key, z * (NQ / 16) + chunk)
-                                         : p_base + z * kTile * C::kPRow + swz<C::kPRow>(key, chunk);
+            const uint32_t at = C::kPlanes ? p_base + z * kTile * C::kPRow + swz<C::kPRow>(key, chunk)
+                                           : p_base + swz<C::kPRow>(key, z * (NQ / 16) + chunk);
             st_shared_v4(at, part[z][0], part[z][1], part[z][2], part[z][3]);
           }
         }
@@ -934,7 +913,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == C::kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+  if (warp == C::kMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 // A warp joins one row of the unit that begins in piece blockIdx.x and goes on in the next ones.
