@@ -661,7 +661,7 @@ dllm_status dllm_kv8_attention(const dllm_layer_desc* desc, const dllm_batch* ba
   if (!aligned(o, 16) || (lse != nullptr && !aligned(lse, 4))) return DLLM_ERR_INVALID_ARGUMENT;
   if (ws_bytes < need) return DLLM_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned(ws, 256)) return DLLM_ERR_INVALID_ARGUMENT;
-  Kv8AttnArgs a;
+  Kv8AttnArgs a = {};
   a.bt = kv8_batch(batch, kv8->num_pages);
   a.kv = kv8_pools(kv8);
   a.q = q;

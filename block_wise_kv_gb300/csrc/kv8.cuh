@@ -65,6 +65,7 @@ struct Kv8AttnArgs {
   int32_t head_dim;
   float scale_log2;     // softmax scale * log2(e)
   void* ws;
+  int32_t whole_units;  // set by the launcher: units are not split over CTAs
 };
 size_t kv8_attention_workspace_bytes(int max_block_len, int n_heads, int n_kv_heads, int head_dim, int num_sms);
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream);

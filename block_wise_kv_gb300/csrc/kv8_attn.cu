@@ -35,7 +35,8 @@
 // SMs alike.  Each unit stands there with kUnitTiles more than it has: what q, the first
 // reference and the output cost.  (Without them the CTAs that got the many short units of
 // a ragged batch took 1.6 times the mean.)  A unit cut by a border leaves its pieces' (O, R, l) in the workspace, and a
-// second, small kernel joins them in the order of the keys, a warp for each row: with the
+// second, small kernel joins them in the order of the keys, a warp for each row (not
+// launched, and no unit cut, where no sequence has more than kWholeTiles tiles): with the
 // ring full, every dependent trip to memory (fence, counter, reads) costs the attention's
 // warps several microseconds, which a join inside the kernel had to wait for.
 #include <algorithm>
@@ -52,6 +53,9 @@ constexpr int kScaleSlots = 8;       // tiles whose scales are in shared memory
 constexpr int kMaxCtas = 1024;       // of a launch (records of the workspace)
 constexpr size_t kRecordBytes = kMaxCtas * sizeof(int2);
 constexpr int kUnitTiles = 3;        // what a unit's beginning and end cost, in tiles (see the split above)
+// Sequences of up to this many tiles are not cut: three more tiles in a row take about what the second launch does
+// (320 tokens of 4 heads: 10.4 us cut and joined, 9.8 whole, and a launch less).
+constexpr int kWholeTiles = 4;
 constexpr int kScan = 128;           // threads that sum up a large batch's work
 constexpr int kParts = 16;           // parts of units in shared memory: the producer is fewer than 8 tiles ahead
 constexpr float kTop = 10.f;    // log2 of a row's largest weight x value scale when R is set
@@ -263,25 +267,33 @@ struct Walk {
   long long base, pos, hi;  // where sequence b begins on the line; the next tile; the end
   int b;
   Seq q;
+  bool whole;      // units are not cut: the piece has those that begin in it
   // the current part of a unit: tiles [t0, t1) of (b, h, qt), whose first tile lies at u0 on the line
   int h, qt, t0, t1;
   long long u0;
   __device__ Walk(const Kv8AttnArgs& args, int b0, const Seq& q0, long long base0, long long lo, long long hi0)
-      : a(args), base(base0), pos(lo), hi(hi0), b(b0), q(q0) {}
+      : a(args), base(base0), pos(lo), hi(hi0), b(b0), q(q0), whole(args.whole_units != 0) {}
   __device__ bool next() {
-    if (pos >= hi) return false;
-    long long w = seq_work<NQ>(a, q);
-    while (pos >= base + w) {
-      base += w;
-      q = load_seq<NQ>(a, ++b);
-      w = seq_work<NQ>(a, q);
+    int span, x;
+    for (;;) {
+      if (pos >= hi) return false;
+      long long w = seq_work<NQ>(a, q);
+      while (pos >= base + w) {
+        base += w;
+        q = load_seq<NQ>(a, ++b);
+        w = seq_work<NQ>(a, q);
+      }
+      span = q.tiles + kUnitTiles;
+      x = static_cast<int>(quotient(pos - base, span));  // unit of the sequence
+      const long long begins = base + static_cast<long long>(x) * span;
+      if (!whole || pos == begins) break;
+      pos = begins + span;  // it began in the piece before
     }
-    const int x = static_cast<int>(quotient(pos - base, q.tiles + kUnitTiles));  // unit of the sequence
     h = x / q.nqt;
     qt = x % q.nqt;
-    u0 = base + static_cast<long long>(x) * (q.tiles + kUnitTiles) + kUnitTiles;
+    u0 = base + static_cast<long long>(x) * span + kUnitTiles;
     t0 = static_cast<int>(max(pos - u0, 0ll));
-    t1 = static_cast<int>(min(static_cast<long long>(q.tiles), hi - u0));
+    t1 = whole ? q.tiles : static_cast<int>(min(static_cast<long long>(q.tiles), hi - u0));
     if (t1 <= 0) return false;  // the piece ends before the unit's first tile
     pos = u0 + t1;
     return true;
@@ -922,7 +934,7 @@ constexpr int kJoinWarps = 8;
 template <int D, int NQ>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const Kv8AttnArgs a) {
   using C = Cfg<D, NQ>;
-  constexpr int kE = D / 32;
+  constexpr int kE = D / 32, kFlight = 4;
   const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31, cta = blockIdx.x;
   griddep_wait();
   griddep_launch_dependents();
@@ -932,29 +944,43 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const Kv8Attn
   const float* const first = parts + (static_cast<size_t>(cta) * 2 + 1) * C::kPartFloats;
   auto part = [&](int i) { return i == 0 ? first : parts + static_cast<size_t>(cta + i) * 2 * C::kPartFloats; };
   const long long row = __ldcg(reinterpret_cast<const long long*>(first + NQ * (D + 2)) + r);
-  float top = attn::neg_inf();
-  for (int i = lane; i < record.x; i += 32) top = fmaxf(top, __ldcg(part(i) + NQ * D + r));
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  float o[kE], total = 0.f;
+  float top = attn::neg_inf(), o[kE], total = 0.f;
 #pragma unroll
   for (int e = 0; e < kE; ++e) o[e] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < record.x; ++i) {
-    const float* const p = part(i);
-    const float w = exp2f(__ldcg(p + NQ * D + r) - top);
-    total = fmaf(w, __ldcg(p + NQ * (D + 1) + r), total);
-    const float* const src = p + r * D + lane * kE;
-    if constexpr (kE == 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-      o[0] = fmaf(w, v.x, o[0]);
-      o[1] = fmaf(w, v.y, o[1]);
-      o[2] = fmaf(w, v.z, o[2]);
-      o[3] = fmaf(w, v.w, o[3]);
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-      o[0] = fmaf(w, v.x, o[0]);
-      o[1] = fmaf(w, v.y, o[1]);
+  for (int i0 = 0; i0 < record.x; i0 += 32) {  // a piece a lane for R and l, then the pieces' rows, kFlight under way at a time
+    const int n = min(32, record.x - i0);
+    const float* const mine = part(i0 + min(lane, n - 1)) + NQ * D + r;
+    const float ref = lane < n ? __ldcg(mine) : attn::neg_inf(), sum = lane < n ? __ldcg(mine + NQ) : 0.f;
+    float now = ref;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+    now = fmaxf(now, top);
+    const float keep = exp2f(top - now), w = exp2f(ref - now);
+    top = now;
+    float add = w * sum;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
+    total = fmaf(total, keep, add);
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] *= keep;
+    for (int j0 = 0; j0 < n; j0 += kFlight) {
+      float v[kFlight][kE];
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j) {
+        if (j0 + j >= n) break;
+        const float* const src = part(i0 + j0 + j) + r * D + lane * kE;
+        if constexpr (kE == 4)
+          *reinterpret_cast<float4*>(v[j]) = __ldcg(reinterpret_cast<const float4*>(src));
+        else
+          *reinterpret_cast<float2*>(v[j]) = __ldcg(reinterpret_cast<const float2*>(src));
+      }
+#pragma unroll
+      for (int j = 0; j < kFlight; ++j) {
+        if (j0 + j >= n) break;
+        const float wj = __shfl_sync(0xffffffffu, w, j0 + j);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] = fmaf(wj, v[j][e], o[e]);
+      }
     }
   }
   const float inv = 1.f / total;
@@ -996,7 +1022,7 @@ cudaError_t launch(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int grid = grid_of(num_sms);
   e = attn::launch_pdl(kv8_attn_kernel<D, NQ>, dim3(grid), C::kThreads, C::kDynSmem, 0, stream, tk, tv, a);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.whole_units) return e;
   const int64_t most = static_cast<int64_t>(a.bt.max_block_len) * (a.n_heads / a.kv.n_kv_heads);
   const int joined = static_cast<int>(std::min<int64_t>(NQ, most));
   return attn::launch_pdl(kv8_join_kernel<D, NQ>, dim3(grid, (joined + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, 0,
@@ -1018,7 +1044,9 @@ size_t kv8_attention_workspace_bytes(int max_block_len, int n_heads, int n_kv_he
   return kRecordBytes + static_cast<size_t>(grid_of(num_sms)) * 2 * nq * (head_dim + 4) * sizeof(float);
 }
 
-cudaError_t launch_kv8_attention(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_kv8_attention(const Kv8AttnArgs& args, int num_sms, cudaStream_t stream) {
+  Kv8AttnArgs a = args;
+  a.whole_units = a.bt.max_seq_len <= kWholeTiles * kTile ? 1 : 0;
   const int nq = unit_rows(a.bt.max_block_len, a.n_heads, a.kv.n_kv_heads);
   if (a.head_dim == 128)
     return nq == 16 ? launch<128, 16>(a, num_sms, stream)
