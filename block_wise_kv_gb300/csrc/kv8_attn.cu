@@ -67,7 +67,7 @@ struct Cfg {
   static constexpr int kCols = NQ == 64 ? 32 : 16;
   static constexpr int kGroups = NQ / kCols;
   static constexpr int kSoft = 128 * kGroups;  // softmax threads
-  static constexpr uint32_t kTmemCols = 2 * NQ;  // S^T, O^T
+  static constexpr uint32_t kTmemCols = 4 * NQ;  // S^T, O^T of the three parts
   static constexpr int kProducerWarp = 4 * kGroups, kMmaWarp = kProducerWarp + 1;
   static constexpr int kThreads = kSoft + 64;
   static constexpr int kSlotBytes = kTile * D;
@@ -88,11 +88,13 @@ struct Cfg {
 
 // ------------------------------------------------------------ descriptors
 // Tiles of 64- or 128-byte rows with the swizzle of that width: 8-row atoms one after the other.
+// `block`: bytes from one row's worth of the contiguous dimension to the next, where an operand has more than one.
 template <int ROW>
-__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr) {
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr, uint32_t block = 0) {
   static_assert(ROW == 64 || ROW == 128, "swizzled rows");
   uint64_t d = 0;
   d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(block >> 4) << 16;    // leading byte offset
   d |= static_cast<uint64_t>(ROW * 8 >> 4) << 32;  // stride byte offset: one 8-row atom
   d |= static_cast<uint64_t>(1) << 46;             // descriptor version for tcgen05
   d |= static_cast<uint64_t>(ROW == 128 ? 2 : 4) << 61;
@@ -196,7 +198,6 @@ __device__ __forceinline__ float reduce_transposed(float (&v)[N], int lane, Op o
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[16]) { tmem_ld_32x32b_x16(taddr, v); }
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[32]) { tmem_ld_32x32b_x32(taddr, v); }
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&v)[16]) { tmem_st_32x32b_x16(taddr, v); }
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&v)[32]) { tmem_st_32x32b_x32(taddr, v); }
 
 // Wait for the phase with the given parity, at most 2^18 tries of up to 20 us each (seconds), in few instructions: the
 // kernel's roles share the instruction cache.  False where it gave up.
@@ -564,9 +565,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t kIdescS = idesc_f8(kTile, NQ, false, false);
-      constexpr uint32_t kIdescO = idesc_f8(kTile, NQ, true, true);
+      constexpr uint32_t kIdescO = idesc_f8(kTile, 3 * NQ, true, true);
       const uint32_t tm_o = tmem + NQ;
-      const uint64_t q_desc = desc_rows<D>(q_base), p_desc = desc_rows<C::kPRow>(p_base);
+      const uint64_t q_desc = desc_rows<D>(q_base), p_desc = desc_rows<C::kPRow>(p_base, C::kPlanes ? kTile * C::kPRow : 0);
       int nt = 0, unit = 0;
       bool ok = true;
       auto wait = [&](uint64_t* bar, int parity) {
@@ -583,11 +584,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         tc_fence_after();
         const uint64_t v = desc_rows<D>(ring + s * C::kSlotBytes);  // (a step of n bytes adds n / 16 to the address field)
 #pragma unroll
-        for (int z = 0; z < 3; ++z)
-#pragma unroll
-          for (int k = 0; k < kTile / 32; ++k)
-            umma_e4m3(tm_o, v + k * 2 * D, p_desc + ((C::kPlanes ? z * kTile * C::kPRow : z * NQ) + k * 32 * C::kPRow) / 16, kIdescO,
-                      !fresh || z > 0 || k > 0);
+        for (int k = 0; k < kTile / 32; ++k) umma_e4m3(tm_o, v + k * 2 * D, p_desc + k * 2 * C::kPRow, kIdescO, !fresh || k > 0);
         umma_commit(&empty_bar[s]);
         umma_commit(&pv_done);
       };
@@ -760,32 +757,42 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         wait(&pv_done, nt - 1);
         soft_sync();
         tc_fence_after();
-        float o[kCols];  // column `key` of this thread's rows
-        tmem_load(tm_o, o);
         const bool began = done.t0 == 0, whole = began && done.t1 == done.tiles;
         const int head = done.h * G, r0 = done.r0;
+        float* const mine = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kRecordBytes) +
+                            (static_cast<size_t>(cta) * 2 + (began ? 1 : 0)) * C::kPartFloats;
+#pragma unroll 1
+        for (int c0 = col0; c0 < col0 + kCols; c0 += 16) {
+          float o[16];  // column `key` of sixteen rows
+          tmem_load(tm_o + c0 - col0, o);
+#pragma unroll 1
+          for (int z = 1; z < 3; ++z) {
+            float more[16];
+            tmem_load(tm_o + c0 - col0 + z * NQ, more);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] += more[c];
+          }
+          if (key >= D) continue;
+          if (whole) {
+            __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o) + key;
+            int j = (r0 + c0) % G;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              if (c0 + c < cols)
+                out[(static_cast<size_t>(row_sh[was][c0 + c]) * a.n_heads + head + j) * D] = __float2bfloat16(o[c] * inv_sh[c0 + c]);
+              if (++j == G) j = 0;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (c0 + c < cols) mine[(c0 + c) * D + key] = o[c];
+          }
+        }
         if (whole) {
-          __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o) + key;
           if (a.lse != nullptr && tid < cols)
             a.lse[static_cast<size_t>(row_sh[was][tid]) * a.n_heads + head + (r0 + tid) % G] =
                 (log2f(l_sh[tid]) - nref_sh[was][tid]) * attn::kLn2;
-          if (key < D) {
-            int j = (r0 + col0) % G;
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-              if (col0 + c < cols)
-                out[(static_cast<size_t>(row_sh[was][col0 + c]) * a.n_heads + head + j) * D] = __float2bfloat16(o[c] * inv_sh[col0 + c]);
-              if (++j == G) j = 0;
-            }
-          }
         } else {
-          float* const mine = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kRecordBytes) +
-                              (static_cast<size_t>(cta) * 2 + (began ? 1 : 0)) * C::kPartFloats;
-          if (key < D) {
-#pragma unroll
-            for (int c = 0; c < kCols; ++c)
-              if (col0 + c < cols) mine[(col0 + c) * D + key] = o[c];
-          }
           if (tid < cols) {
             mine[NQ * D + tid] = -nref_sh[was][tid];
             mine[NQ * (D + 1) + tid] = l_sh[tid];
@@ -837,15 +844,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
             if (!soft_any<C::kSoft>(xm + lv > kLimit)) break;
           }
           // the largest weight x value scale of each row in this tile
-          float u[kCols];
 #pragma unroll
-          for (int c = 0; c < kCols / 2; ++c) {
-            const float2 v = unpack2(x[c]);
-            u[2 * c] = v.x + lv;
-            u[2 * c + 1] = v.y + lv;
+          for (int c0 = 0; c0 < kCols; c0 += 16) {  // sixteen at a time: the rare way must not cost the common one registers
+            float u[16];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              const float2 v = unpack2(x[c0 / 2 + c]);
+              u[2 * c] = v.x + lv;
+              u[2 * c + 1] = v.y + lv;
+            }
+            const float m = reduce_transposed(u, lane, [](float p, float r) { return fmaxf(p, r); });
+            if (lane < 16) red_sh[warp & 3][col0 + c0 + lane] = m;
           }
-          const float m = reduce_transposed(u, lane, [](float p, float r) { return fmaxf(p, r); });
-          if (lane < kCols) red_sh[warp & 3][col0 + lane] = m;
           soft_sync();
           if (tid < NQ) {
             const float top = fmaxf(fmaxf(red_sh[0][tid], red_sh[1][tid]), fmaxf(red_sh[2][tid], red_sh[3][tid]));
@@ -860,11 +870,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < kCols / 2; ++c) l[c] = mul2(l[c], pack2(alpha_sh[col0 + 2 * c], alpha_sh[col0 + 2 * c + 1]));
-            float o[kCols];
-            tmem_load(tm_o, o);
+#pragma unroll 1
+            for (int k = 0; k < 3 * kCols / 16; ++k) {
+              const int z = k % 3, c0 = k / 3 * 16;
+              float o[16];
+              tmem_load(tm_o + z * NQ + c0, o);
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) o[c] *= alpha_sh[col0 + c];
-            tmem_store(tm_o, o);
+              for (int c = 0; c < 16; ++c) o[c] *= alpha_sh[col0 + c0 + c];
+              tmem_store(tm_o + z * NQ + c0, o);
+            }
             tmem_st_wait();
           }
         }
