@@ -122,15 +122,15 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const float (
       : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// Barrier of the softmax warps (N threads) that ORs a predicate over them, and the plain one.
+// Barrier `id` of N threads that ORs a predicate over them.
 template <int N>
-__device__ __forceinline__ bool soft_any(bool v) {
+__device__ __forceinline__ bool barrier_any(int id, bool v) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, %3, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(v)), "n"(N)
+      : "r"(static_cast<uint32_t>(v)), "n"(N), "r"(id)
       : "memory");
   return r != 0;
 }
@@ -627,7 +627,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     const int key = tid & 127, grp = tid >> 7, col0 = grp * kCols;  // this thread's key of a tile (column of O^T), and rows
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tm_s = tmem + lane_base + col0, tm_o = tm_s + NQ;
+    // barrier 1 is all softmax warps', 2 + grp a group's: R is a row's own, so groups go through a unit's tiles apart
     auto soft_sync = []() { named_barrier(1, C::kSoft); };
+    auto group_sync = [grp]() { named_barrier(2 + grp, 128); };
     int nt = 0;
     bool dead = false;
     auto wait = [&](uint64_t* bar, int parity) {  // a thread that gave up waits for nothing more, but meets every barrier
@@ -664,7 +666,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       const Part& part = part_sh[u % kParts];
       const int par = u & 1;
       if (!kAhead || u == 0) ask_q(u);
-      const bool have = !soft_any<C::kSoft>(dead || part.t1 == 0);  // (the same for all, whoever gave up)
+      const bool have = !barrier_any<C::kSoft>(1, dead || part.t1 == 0);  // (the same for all, whoever gave up)
       if (u > 0) {
         float v[kCols];
 #pragma unroll
@@ -841,7 +843,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
               const float2 v = unpack2(x[c]);
               xm = fmaxf(xm, fmaxf(v.x, v.y));
             }
-            if (!soft_any<C::kSoft>(xm + lv > kLimit)) break;
+            if (!barrier_any<128>(2 + grp, xm + lv > kLimit)) break;
           }
           // the largest weight x value scale of each row in this tile
 #pragma unroll
@@ -856,16 +858,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
             const float m = reduce_transposed(u, lane, [](float p, float r) { return fmaxf(p, r); });
             if (lane < 16) red_sh[warp & 3][col0 + c0 + lane] = m;
           }
-          soft_sync();
-          if (tid < NQ) {
-            const float top = fmaxf(fmaxf(red_sh[0][tid], red_sh[1][tid]), fmaxf(red_sh[2][tid], red_sh[3][tid]));
+          group_sync();
+          if (key < kCols) {
+            const int c = col0 + key;
+            const float top = fmaxf(fmaxf(red_sh[0][c], red_sh[1][c]), fmaxf(red_sh[2][c], red_sh[3][c]));
             float up = 0.f;  // what R grows by
             if ((first || top > kLimit) && fabsf(top) < INFINITY) up = top - kTop;
-            nref_sh[par][tid] -= up;
-            alpha_sh[tid] = first ? 0.f : exp2f(-up);
+            nref_sh[par][c] -= up;
+            alpha_sh[c] = first ? 0.f : exp2f(-up);
           }
           if (!first) wait(&pv_done, nt - 1);
-          soft_sync();
+          group_sync();
           if (!first) {
             tc_fence_after();
 #pragma unroll
