@@ -32,7 +32,7 @@
 //
 // Split: the tiles of all units form one line, cut into as many equal pieces as CTAs
 // (or fewer, where there are few tiles): a ragged batch or one long sequence loads all
-// SMs alike.  Each unit stands there with kUnitTiles more than it has: what q, the first
+// SMs alike.  Each unit stands there with two to four more than it has: what q, the first
 // reference and the output cost.  (Without them the CTAs that got the many short units of
 // a ragged batch took 1.6 times the mean.)  A unit cut by a border leaves its pieces' (O, R, l) in the workspace, and a
 // second, small kernel joins them in the order of the keys, a warp for each row (not
@@ -52,14 +52,17 @@ constexpr int kCtasPerSm = 2;
 constexpr int kScaleSlots = 8;       // tiles whose scales are in shared memory
 constexpr int kMaxCtas = 1024;       // of a launch (records of the workspace)
 constexpr size_t kRecordBytes = kMaxCtas * sizeof(int2);
-constexpr int kUnitTiles = 3;        // what a unit's beginning and end cost, in tiles (see the split above)
 // Sequences of up to this many tiles are not cut: three more tiles in a row take about what the second launch does
 // (320 tokens of 4 heads: 10.4 us cut and joined, 9.8 whole, and a launch less).
 constexpr int kWholeTiles = 4;
 constexpr int kScan = 128;           // threads that sum up a large batch's work
 constexpr int kParts = 16;           // parts of units in shared memory: the producer is fewer than 8 tiles ahead
 constexpr float kTop = 10.f;    // log2 of a row's largest weight x value scale when R is set
-constexpr float kLimit = 15.f;  // and where it is raised
+constexpr float kLimitLog2 = 15.f;
+constexpr float kLimit = 32768.f;  // what a weight x value scale may reach before R is raised
+
+// What a unit's beginning and end cost, in tiles (see the split above; 4.2, 1.7 and 1.9 by a fit to the CTAs' times).
+__host__ __device__ constexpr int unit_tiles(int nq) { return nq == 64 ? 4 : 2; }
 
 // NQ rows to a unit, handled by NQ / kCols groups of four softmax warps (a thread: one key, kCols rows).
 template <int D, int NQ>
@@ -199,6 +202,24 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[16]) { tmem
 __device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[32]) { tmem_ld_32x32b_x32(taddr, v); }
 __device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&v)[16]) { tmem_st_32x32b_x16(taddr, v); }
 
+// The sum of sixteen columns of three blocks `step` columns apart (three loads under way, one wait).
+__device__ __forceinline__ void tmem_load3(uint32_t taddr, uint32_t step, float (&v)[16]) {
+  uint32_t r[3][16];
+#pragma unroll
+  for (int z = 0; z < 3; ++z)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[z][0]), "=r"(r[z][1]), "=r"(r[z][2]), "=r"(r[z][3]), "=r"(r[z][4]), "=r"(r[z][5]), "=r"(r[z][6]),
+          "=r"(r[z][7]), "=r"(r[z][8]), "=r"(r[z][9]), "=r"(r[z][10]), "=r"(r[z][11]), "=r"(r[z][12]), "=r"(r[z][13]),
+          "=r"(r[z][14]), "=r"(r[z][15])
+        : "r"(taddr + z * step)
+        : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int c = 0; c < 16; ++c) v[c] = (__uint_as_float(r[0][c]) + __uint_as_float(r[1][c])) + __uint_as_float(r[2][c]);
+}
+
 // Wait for the phase with the given parity, at most 2^18 tries of up to 20 us each (seconds), in few instructions: the
 // kernel's roles share the instruction cache.  False where it gave up.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
@@ -242,7 +263,7 @@ __device__ __forceinline__ Seq load_seq(const Kv8AttnArgs& a, int b) {
 }
 template <int NQ>
 __device__ __forceinline__ long long seq_work(const Kv8AttnArgs& a, const Seq& q) {
-  return q.tiles == 0 ? 0 : static_cast<long long>(a.kv.n_kv_heads) * q.nqt * (q.tiles + kUnitTiles);
+  return q.tiles == 0 ? 0 : static_cast<long long>(a.kv.n_kv_heads) * q.nqt * (q.tiles + unit_tiles(NQ));
 }
 
 // a / b for a >= 0, b > 0 (almost always of 31 bits).
@@ -284,7 +305,7 @@ struct Walk {
         q = load_seq<NQ>(a, ++b);
         w = seq_work<NQ>(a, q);
       }
-      span = q.tiles + kUnitTiles;
+      span = q.tiles + unit_tiles(NQ);
       x = static_cast<int>(quotient(pos - base, span));  // unit of the sequence
       const long long begins = base + static_cast<long long>(x) * span;
       if (!whole || pos == begins) break;
@@ -292,7 +313,7 @@ struct Walk {
     }
     h = x / q.nqt;
     qt = x % q.nqt;
-    u0 = base + static_cast<long long>(x) * span + kUnitTiles;
+    u0 = base + static_cast<long long>(x) * span + unit_tiles(NQ);
     t0 = static_cast<int>(max(pos - u0, 0ll));
     t1 = whole ? q.tiles : static_cast<int>(min(static_cast<long long>(q.tiles), hi - u0));
     if (t1 <= 0) return false;  // the piece ends before the unit's first tile
@@ -504,23 +525,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     hand_over(have);
     int ids_next = have ? page_ids(bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages, 2 * walk.t0, walk.q.npages) : 0;
     while (have && ok) {
-      // this part's values, while the walk goes on to the next: its page ids and rows of q are asked for a part ahead
+      // this part's values: the walk goes on to the next before its end, whose page ids and rows of q are asked for ahead
       const int32_t* const row = bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages;
       const int t0 = walk.t0, t1 = walk.t1, h = walk.h, npages = walk.q.npages;
       const uint64_t policy = walk.q.nqt > 1 ? again : once;
       int ids = ids_next, first = 2 * t0;
-      have = walk.next();
-      hand_over(have);
-      if (have) {
-        ids_next = page_ids(bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages, 2 * walk.t0, walk.q.npages);
-        for (int c = lane; c < NQ; c += 32) {
-          const int r = walk.qt * NQ + c;
-          if (r >= walk.q.rows * G) break;
-          const char* src = reinterpret_cast<const char*>(static_cast<const __nv_bfloat16*>(a.q) + (walk.q.cub + r / G) * a.q_row +
-                                                          static_cast<size_t>(walk.h * G + r % G) * D);
-          for (int z = 0; z < D * 2; z += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + z));
-        }
-      }
       for (int t = t0; t < t1 && ok; ++t) {
         if (2 * t - first >= 32) {
           first = 2 * t;
@@ -546,6 +555,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         pages_last = pages;
         policy_last = policy;
         ++nt;
+        if (t == t0) {  // the next part, while this one's first tile is on its way
+          have = walk.next();
+          hand_over(have);
+          if (have) {
+            ids_next = page_ids(bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages, 2 * walk.t0, walk.q.npages);
+            for (int c = lane; c < NQ; c += 32) {
+              const int r = walk.qt * NQ + c;
+              if (r >= walk.q.rows * G) break;
+              const char* src = reinterpret_cast<const char*>(static_cast<const __nv_bfloat16*>(a.q) + (walk.q.cub + r / G) * a.q_row +
+                                                              static_cast<size_t>(walk.h * G + r % G) * D);
+              for (int z = 0; z < D * 2; z += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + z));
+            }
+          }
+        }
       }
     }
     if (ok && nt > 0) {
@@ -667,17 +690,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       const int par = u & 1;
       if (!kAhead || u == 0) ask_q(u);
       const bool have = !barrier_any<C::kSoft>(1, dead || part.t1 == 0);  // (the same for all, whoever gave up)
-      if (u > 0) {
-        float v[kCols];
-#pragma unroll
-        for (int c = 0; c < kCols / 2; ++c) {
-          const float2 p = unpack2(l[c]);
-          v[2 * c] = p.x;
-          v[2 * c + 1] = p.y;
-        }
-        const float sum = reduce_transposed(v, lane, [](float p, float r) { return p + r; });
-        if (lane < kCols) red_sh[warp & 3][col0 + lane] = sum;
-      }
       if (have) {
         uint32_t m = 0;
 #pragma unroll
@@ -706,8 +718,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
           nref_sh[par][tid] = 0.f;
         }
       }
-      soft_sync();
       if (have) {
+        soft_sync();
         // q in two e4m3 parts
         float amax = amax_sh[0];
 #pragma unroll
@@ -751,6 +763,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         // ---- the end of the part before: l over all keys, then O / l, or (O, R, l) to the workspace
         const Part& done = part_sh[(u - 1) % kParts];
         const int cols = done.cols, was = par ^ 1;
+        {
+          float v[kCols];
+  #pragma unroll
+          for (int c = 0; c < kCols / 2; ++c) {
+            const float2 p = unpack2(l[c]);
+            v[2 * c] = p.x;
+            v[2 * c + 1] = p.y;
+          }
+          const float sum = reduce_transposed(v, lane, [](float p, float r) { return p + r; });
+          if (lane < kCols) red_sh[warp & 3][col0 + lane] = sum;
+        }
+        soft_sync();
         if (tid < NQ) {
           const float sum = (red_sh[0][tid] + red_sh[1][tid]) + (red_sh[2][tid] + red_sh[3][tid]);
           l_sh[tid] = sum;
@@ -766,14 +790,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
 #pragma unroll 1
         for (int c0 = col0; c0 < col0 + kCols; c0 += 16) {
           float o[16];  // column `key` of sixteen rows
-          tmem_load(tm_o + c0 - col0, o);
-#pragma unroll 1
-          for (int z = 1; z < 3; ++z) {
-            float more[16];
-            tmem_load(tm_o + c0 - col0 + z * NQ, more);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] += more[c];
-          }
+          tmem_load3(tm_o + c0 - col0, NQ, o);
           if (key >= D) continue;
           if (whole) {
             __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o) + key;
@@ -817,7 +834,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         wait(&scale_bar[nt % kScaleSlots], nt / kScaleSlots);
         const float sv = key < valid ? scales[nt % kScaleSlots][1][key / kKv8Group] : 0.f;
         const float f = key < valid ? scales[nt % kScaleSlots][0][key / kKv8Group] * f_q : 0.f;
-        const float lv = sv > 0.f ? __log2f(sv) : attn::neg_inf();
         wait(&s_full, nt);
         tc_fence_after();
         uint64_t x[kCols / 2];
@@ -843,9 +859,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
               const float2 v = unpack2(x[c]);
               xm = fmaxf(xm, fmaxf(v.x, v.y));
             }
-            if (!barrier_any<128>(2 + grp, xm + lv > kLimit)) break;
+            if (!barrier_any<128>(2 + grp, attn::fast_exp2(xm) * sv > kLimit)) break;
           }
-          // the largest weight x value scale of each row in this tile
+          // the largest weight x value scale of each row in this tile, as its logarithm
+          const float lv = sv > 0.f ? __log2f(sv) : attn::neg_inf();
 #pragma unroll
           for (int c0 = 0; c0 < kCols; c0 += 16) {  // sixteen at a time: the rare way must not cost the common one registers
             float u[16];
@@ -863,7 +880,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
             const int c = col0 + key;
             const float top = fmaxf(fmaxf(red_sh[0][c], red_sh[1][c]), fmaxf(red_sh[2][c], red_sh[3][c]));
             float up = 0.f;  // what R grows by
-            if ((first || top > kLimit) && fabsf(top) < INFINITY) up = top - kTop;
+            if ((first || top > kLimitLog2) && fabsf(top) < INFINITY) up = top - kTop;
             nref_sh[par][c] -= up;
             alpha_sh[c] = first ? 0.f : exp2f(-up);
           }
