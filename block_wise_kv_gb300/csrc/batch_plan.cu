@@ -22,7 +22,8 @@
 namespace dllm {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
+constexpr int kCtasPerSm = 2;
 constexpr int kChunk = kThreads;  // sequences scanned at a time, one a thread
 constexpr int kWarps = kThreads / 32;
 
@@ -67,7 +68,7 @@ __device__ __forceinline__ void store4(int32_t* map, long long j0, const int (&v
     if (j0 + e >= lo && j0 + e < hi) map[j0 + e] = v[e];
 }
 
-__global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) batch_plan_kernel(const PlanArgs a) {
   __shared__ Chunk c;
   __shared__ Sums warp_sums[kWarps + 1];
   __shared__ int warp_granted[kWarps];
@@ -128,14 +129,14 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) 
     if (lane == 31) warp_sums[warp] = incl;
     __syncthreads();
     if (warp == 0) {
-      const Sums w = warp_sums[lane];
+      const Sums w = lane < kWarps ? warp_sums[lane] : Sums{0, 0, 0, 0};
       Sums s = w;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const Sums o = shfl_up(s, d);
         if (lane >= d) s = s + o;
       }
-      warp_sums[lane] = {s.rows - w.rows, s.seq - w.seq, s.take - w.take, s.give - w.give};
+      if (lane < kWarps) warp_sums[lane] = {s.rows - w.rows, s.seq - w.seq, s.take - w.take, s.give - w.give};
       if (lane == 31) warp_sums[kWarps] = s;
     }
     __syncthreads();
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) 
     const Sums total = carry + warp_sums[kWarps];
     const int nb = min(kChunk, a.batch - b0);
 
-    // the ids handed out, and those given back: CTA c has every n_cta-th stretch of 1024 of this chunk's
+    // the ids handed out, and those given back: CTA c has every n_cta-th stretch of kThreads of this chunk's
     const long long take_end = min(total.take, static_cast<long long>(count));
     for (long long i = carry.take + first; i < take_end; i += stride) {
       const int k = last_not_above(c.take0, nb, i);
@@ -188,23 +189,33 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) 
     for (long long j0 = carry.rows / 4 * 4 + 4 * first; j0 < row_end; j0 += 4 * stride) {
       int k = last_not_above(c.row0, nb, max(j0, carry.rows));
       int slot[4], seq[4], pos[4];
+      int at = -1, base = -1;  // the last page looked up (sequence k's page at): its first slot
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const long long j = j0 + e;
         slot[e] = seq[e] = pos[e] = -1;
         if (j < carry.rows || j >= row_end) continue;
-        while (k + 1 < nb && c.row0[k + 1] <= j) ++k;
+        while (k + 1 < nb && c.row0[k + 1] <= j) {
+          ++k;
+          at = -1;
+        }
         const int p = c.start[k] + static_cast<int>(j - c.row0[k]), pg = p / kPage;
         seq[e] = b0 + k;
         pos[e] = p;
-        if (pg < c.now[k] && a.row_slot != nullptr) {
-          const int id = pg < c.held[k] ? a.table[static_cast<size_t>(b0 + k) * a.max_pages + pg]
-                                        : ring_id(c.take0[k] + pg - c.held[k]);
-          if (id >= 0 && id < a.num_pages)
-            slot[e] = id * kPage + p % kPage;
-          else
-            err |= kErrBadPage;
+        if (a.row_slot == nullptr) continue;
+        if (pg != at) {
+          at = pg;
+          base = -1;
+          if (pg < c.now[k]) {
+            const int id = pg < c.held[k] ? a.table[static_cast<size_t>(b0 + k) * a.max_pages + pg]
+                                          : ring_id(c.take0[k] + pg - c.held[k]);
+            if (id >= 0 && id < a.num_pages)
+              base = id * kPage;
+            else
+              err |= kErrBadPage;
+          }
         }
+        slot[e] = base < 0 ? -1 : base + p % kPage;
       }
       store4(a.row_slot, j0, slot, carry.rows, row_end);
       store4(a.row_seq, j0, seq, carry.rows, row_end);
@@ -238,11 +249,11 @@ __global__ void __launch_bounds__(kThreads) batch_plan_kernel(const PlanArgs a) 
 }  // namespace
 
 cudaError_t launch_batch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream) {
-  // One CTA for each 4096 rows or pages that may have to be written, at most one an SM: each CTA repeats
+  // One CTA for each 4096 rows or pages that may have to be written, at most two an SM: each CTA repeats
   // the scan, so more of them only pay where there is enough to write.
   const long long pages = static_cast<long long>(a.batch) * a.max_pages;
   const long long most = std::max<long long>(a.cap_rows, std::min<long long>(pages, a.num_pages));
-  const int grid = static_cast<int>(std::max(1ll, std::min(static_cast<long long>(num_sms), most / 4096)));
+  const int grid = static_cast<int>(std::max(1ll, std::min(static_cast<long long>(kCtasPerSm * num_sms), most / 4096)));
   return attn::launch_pdl(batch_plan_kernel, dim3(grid), kThreads, 0, 0, stream, a);
 }
 
