@@ -640,6 +640,8 @@ dllm_status dllm_kv8_attention_workspace_size(const dllm_layer_desc* desc, const
   DLLM_TRY(check_batch(batch));
   DLLM_TRY(check_kv8(kv8, desc));
   if (bytes == nullptr) return DLLM_ERR_INVALID_ARGUMENT;
+  // rows that share a key head, and units of a sequence, are counted in 32 bits
+  if (static_cast<int64_t>(batch->max_block_len) * desc->n_heads > kMaxRows) return DLLM_ERR_UNSUPPORTED;
   *bytes = batch->batch > 0 && batch->total_block_rows > 0
                ? kv8_attention_workspace_bytes(batch->max_block_len, desc->n_heads, kv8->n_kv_heads, desc->head_dim,
                                                device_sms())

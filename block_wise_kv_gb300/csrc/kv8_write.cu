@@ -185,8 +185,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv8_write_kernel(const K
   __syncthreads();
   const int* cub = in_smem ? cu : bt.cu_block;
   const int total = min(cub[bt.batch], bt.total_block_rows);
+  if (row0 == 0 && t == 0 && (cub[bt.batch] < 0 || cub[bt.batch] > bt.total_block_rows)) err |= kErrBadShape;
   if (row0 >= total) {
-    if (row0 == 0 && t == 0 && cub[bt.batch] < 0) report_error(bt.err, kErrBadShape);
+    if (err) report_error(bt.err, err);
     return;
   }
   if (t < slice && row0 + t < total) {

@@ -328,7 +328,7 @@ def test_write_scale_at_powers_of_two():
 
 @pytest.mark.parametrize("change,bit", [
     (dict(table=[[99, 99], [2, 3]]), 2), (dict(table=[[-1, -1], [2, 3]]), 2), (dict(n=[1 << 20, 100]), 4),
-    (dict(start=[-1, 90]), 4), (dict(start=[95, 90]), 4), (dict(rows=[9, 10]), 4)])
+    (dict(start=[-1, 90]), 4), (dict(start=[95, 90]), 4), (dict(rows=[9, 10]), 4), (dict(cub=[0, 10, 21]), 4)])
 def test_write_skips_what_contradicts_the_bounds(change, bit):
     b = Batch([100, 100], [80, 90], [10, 10])
     b.t["table"].copy_(ints([[0, 1], [2, 3]]))
@@ -342,7 +342,7 @@ def test_write_skips_what_contradicts_the_bounds(change, bit):
     assert b.bits() == bit
     after = kv8.k.view(torch.uint8)
     assert torch.equal(after[[4, 5]], before[[4, 5]])
-    if "rows" not in change:
+    if "rows" not in change and "cub" not in change:
         assert torch.equal(after[:2], before[:2])
         assert not torch.equal(after[3], before[3])  # the other sequence is written
 
@@ -499,6 +499,74 @@ def test_attention_scale_and_strided_queries():
     desc = dllm.layer_desc(512, 4, 128, 1e4, softmax_scale=0.03125)
     dllm.dllm_kv8_attention(desc, b.view.c, q, kv8.c, o, lse, _ws(b, 4, 128, kv8))
     assert_attention(b, q, kv8, o, lse, scale=0.03125)
+
+
+@pytest.mark.parametrize("batch,longest,H,kv,d", [(129, 300, 2, 1, 128), (300, 700, 4, 4, 64), (700, 200, 16, 2, 64), (1500, 400, 2, 2, 64)])
+def test_attention_large_batches(batch, longest, H, kv, d):
+    """More sequences than one warp sums up, places without a request among them."""
+    r = random.Random(batch)
+    n = [r.choice([0, 1, r.randint(1, longest), r.randint(1, longest)]) for _ in range(batch)]
+    rows = [min(x, r.choice([0, 1, 1, 4])) for x in n]
+    start = [r.randint(0, x - k) for x, k in zip(n, rows)]
+    b = Batch(n, start, rows, seed=batch, max_block=4, max_seq=longest)
+    kv8 = random_pools(b.num_pages, kv, d, batch)
+    _poison_tails(b, kv8)
+    q = _q(b.M, H, d, 9)
+    o, lse = _attend(b, q, kv8)
+    assert b.bits() == 0
+    assert_attention(b, q, kv8, o, lse)
+
+
+@pytest.mark.parametrize("longest", [512, 513])
+def test_attention_with_and_without_cuts(longest):
+    """Sequences of up to 512 tokens are attended to whole, longer ones in pieces: the same inputs under either bound."""
+    n = [512, 300, 1, 129, 64, 512]
+    b = Batch(n, [480, 0, 0, 100, 0, 0], [32, 32, 1, 29, 1, 8], seed=1, max_seq=longest, max_pages=9)
+    kv8 = random_pools(b.num_pages, 4, 128, 5)
+    _poison_tails(b, kv8)
+    q = _q(b.M, 8, 128, 6)
+    o, lse = _attend(b, q, kv8)
+    assert b.bits() == 0
+    assert_attention(b, q, kv8, o, lse)
+
+
+def test_attention_one_head_over_the_whole_gpu():
+    """A single unit: every CTA has a piece of it, and the join more than it takes at a time."""
+    b = Batch([60000], [59999], [1], seed=1)
+    kv8 = random_pools(b.num_pages, 1, 128, 5, spread=1.0)
+    q = _q(1, 5, 128, 6)
+    o, lse = _attend(b, q, kv8)
+    assert b.bits() == 0
+    assert_attention(b, q, kv8, o, lse)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("n", [200, 3000])
+def test_attention_not_a_number_in_a_query_stays_in_its_row(value, n):
+    b = Batch([n, 77], [100, 0], [8, 8], seed=3)
+    kv8 = random_pools(b.num_pages, 2, 128, 5)
+    q = _q(b.M, 4, 128, 6)
+    ref = attention(b, q, kv8)
+    bad = q.clone()
+    bad[3, 1, 17] = value
+    o, lse = _attend(b, bad, kv8)
+    assert torch.isnan(o[3, 1]).all() and torch.isnan(lse[3, 1])
+    o[3, 1], lse[3, 1] = ref[0][3, 1].to(torch.bfloat16), ref[1][3, 1].float()
+    assert_attention(b, q, kv8, o, lse, ref=ref)
+
+
+def test_attention_zero_and_tiny_queries():
+    """A query of zeros weighs all keys alike; one far smaller than the others of its unit still has its own scores."""
+    b = Batch([300], [100], [4], seed=3)
+    kv8 = random_pools(b.num_pages, 1, 128, 5)
+    q = _q(4, 2, 128, 6)
+    q[0] = 0
+    q[1] *= 2.0 ** -9
+    o, lse = _attend(b, q, kv8)
+    assert_attention(b, q, kv8, o, lse)
+    assert (lse[0] - np.log(300)).abs().max() < 1e-5
+    o, lse = _attend(b, torch.zeros_like(q), kv8)
+    assert_attention(b, torch.zeros_like(q), kv8, o, lse)
 
 
 def test_attention_not_a_number_stays_in_its_head():

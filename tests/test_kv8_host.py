@@ -93,6 +93,12 @@ def test_plan_buffers_are_checked():
                    None) == dllm.DLLM_ERR_UNSUPPORTED
 
 
+def test_attention_refuses_more_rows_to_a_head_than_it_counts():
+    wide = _desc(n_heads=40000, head_dim=64, d_model=64)
+    b = _batch(batch=1, max_pages=1024, M=65536, R=65536, max_block=65536, max_seq=65536)
+    assert _status("dllm_kv8_attention", wide, b, A, 1 << 22, _kv8(heads=1), A, 0, None, A, 1 << 40, None) == dllm.DLLM_ERR_UNSUPPORTED
+
+
 def test_an_empty_batch_launches_nothing():
     b = _batch(batch=0, M=0, R=0)
     assert _status("dllm_kv8_write", _desc(), b, None, 0, 0, None, 0, 0, _kv8(), None) == 0
