@@ -231,10 +231,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-  // Let the next kernel (the step's attention) start on the SMs this grid leaves
-  // free: it streams what this kernel does not write while the weights stream.
-  griddep_launch_dependents();
-
   if (warp == 0) {
     // ---- TMA producer.  Weight tiles of the first stages go out before the
     // dependency wait (weights are constants); x^ tiles only once every row
@@ -250,6 +246,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                          wpol);
       }
       griddep_wait();
+      // Let the next kernel (the step's attention) start on the SMs this grid leaves
+      // free: it streams what this kernel does not write while the weights stream.  Not
+      // before this kernel's own wait: what lies before it (a boundary that writes the
+      // pools, a plan that writes the block table) has to have finished too.
+      griddep_launch_dependents();
       const uint64_t t0 = global_timer_ns();  // bounded wait for the x^ rows
       while (ld_acquire_gpu(a.norm_ctr + 1) < a.n_tok) {
         if (global_timer_ns() - t0 > kWaitLimitNs) {

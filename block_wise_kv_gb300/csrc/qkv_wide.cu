@@ -246,7 +246,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-  griddep_launch_dependents();
 
   if (warp < kFirstAccWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
@@ -265,6 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         (w.wt * kbp + 2 * w.ch + hb) * kTM);
           }
         griddep_wait();
+        // the next kernel may start: it reads what the kernels before this one wrote, so not earlier
+        griddep_launch_dependents();
         const uint64_t t0 = global_timer_ns();  // bounded wait for the x^ rows
         while (ld_acquire_gpu(a.norm_ctr + 1) < a.n_tok) {
           if (global_timer_ns() - t0 > kWaitLimitNs) {
