@@ -283,26 +283,37 @@ def dllm_block_ffn(desc, batch, d_ff, o_full, x_block, w_o, ffn_gain, w_gate_up,
         _nbytes(ws), _stream(stream)))
 
 
+# The calls of the 8-bit cache are made for small batches too, where the host's part is most of their time: they take
+# tensors only and do no more than their arguments need.
 def dllm_batch_plan(batch, pages_held, pages_held_out, block_table, cu_block, cu_seq, ring, row_slot=None,
                     row_seq=None, row_pos=None, stream=None):
-    _check("dllm_batch_plan", load().dllm_batch_plan(
-        ctypes.byref(batch), _ptr(pages_held), _ptr(pages_held_out), _ptr(block_table), _ptr(cu_block), _ptr(cu_seq),
-        ctypes.byref(ring), _ptr(row_slot), _ptr(row_seq), _ptr(row_pos), _stream(stream)))
+    status = (_lib or load()).dllm_batch_plan(
+        ctypes.byref(batch), pages_held.data_ptr(), pages_held_out.data_ptr(), block_table.data_ptr(),
+        cu_block.data_ptr(), cu_seq.data_ptr(), ctypes.byref(ring), None if row_slot is None else row_slot.data_ptr(),
+        None if row_seq is None else row_seq.data_ptr(), None if row_pos is None else row_pos.data_ptr(),
+        _stream(stream))
+    if status:
+        raise DllmError("dllm_batch_plan", status)
 
 
 def dllm_kv8_write(desc, batch, k_rows: torch.Tensor, v_rows: torch.Tensor, kv8, stream=None):
     """k_rows, v_rows: bf16 [M][n_kv_heads][head_dim], the last dimension
     contiguous (views of a wider projection output are fine)."""
-    if k_rows.stride(-1) != 1 or v_rows.stride(-1) != 1:
+    ks, vs = k_rows.stride(), v_rows.stride()
+    if len(ks) != 3 or len(vs) != 3 or ks[2] != 1 or vs[2] != 1:
         raise DllmError("dllm_kv8_write", DLLM_ERR_INVALID_ARGUMENT)
-    _check("dllm_kv8_write", load().dllm_kv8_write(
-        ctypes.byref(desc), ctypes.byref(batch), _ptr(k_rows), k_rows.stride(0), k_rows.stride(1), _ptr(v_rows),
-        v_rows.stride(0), v_rows.stride(1), ctypes.byref(kv8), _stream(stream)))
+    status = (_lib or load()).dllm_kv8_write(
+        ctypes.byref(desc), ctypes.byref(batch), k_rows.data_ptr(), ks[0], ks[1], v_rows.data_ptr(), vs[0], vs[1],
+        ctypes.byref(kv8), _stream(stream))
+    if status:
+        raise DllmError("dllm_kv8_write", status)
 
 
 def dllm_kv8_write_pool(desc, batch, cache, kv8, stream=None):
-    _check("dllm_kv8_write_pool", load().dllm_kv8_write_pool(
-        ctypes.byref(desc), ctypes.byref(batch), ctypes.byref(cache), ctypes.byref(kv8), _stream(stream)))
+    status = (_lib or load()).dllm_kv8_write_pool(ctypes.byref(desc), ctypes.byref(batch), ctypes.byref(cache),
+                                                  ctypes.byref(kv8), _stream(stream))
+    if status:
+        raise DllmError("dllm_kv8_write_pool", status)
 
 
 def dllm_kv8_attention_workspace_size(desc, batch, kv8) -> int:
@@ -313,12 +324,16 @@ def dllm_kv8_attention_workspace_size(desc, batch, kv8) -> int:
 
 
 def dllm_kv8_attention(desc, batch, q: torch.Tensor, kv8, o, lse, ws, o_rows: int = DLLM_ROWS_BLOCK, stream=None):
-    """q: bf16 [M][n_heads][head_dim], rows contiguous, any row stride."""
-    if q.stride(-1) != 1 or q.stride(1) != q.shape[2]:
+    """q: bf16 [M][n_heads][head_dim], rows contiguous, any row stride.  lse
+    may be None; ws: a uint8 tensor of dllm_kv8_attention_workspace_size bytes."""
+    qs = q.stride()
+    if len(qs) != 3 or qs[2] != 1 or qs[1] != q.shape[2]:
         raise DllmError("dllm_kv8_attention", DLLM_ERR_INVALID_ARGUMENT)
-    _check("dllm_kv8_attention", load().dllm_kv8_attention(
-        ctypes.byref(desc), ctypes.byref(batch), _ptr(q), q.stride(0), ctypes.byref(kv8), _ptr(o), int(o_rows),
-        _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+    status = (_lib or load()).dllm_kv8_attention(
+        ctypes.byref(desc), ctypes.byref(batch), q.data_ptr(), qs[0], ctypes.byref(kv8), o.data_ptr(), o_rows,
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes, _stream(stream))
+    if status:
+        raise DllmError("dllm_kv8_attention", status)
 
 
 # ---------------------------------------------------- memory / structs ----
