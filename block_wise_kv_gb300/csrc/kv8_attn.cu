@@ -236,7 +236,7 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
 struct Seq {
   int n, s, rows, cub, cus;
   int npages, tiles, nqt;  // tiles = 0: nothing to do
-  bool bad;
+  int bad;                 // (all of them ints: a Seq goes from lane to lane)
 };
 template <int NQ>
 __device__ __forceinline__ Seq load_seq(const Kv8AttnArgs& a, int b) {
@@ -248,12 +248,12 @@ __device__ __forceinline__ Seq load_seq(const Kv8AttnArgs& a, int b) {
   q.cub = __ldg(bt.cu_block + b);
   q.cus = __ldg(bt.cu_seq + b);
   q.tiles = q.nqt = q.npages = 0;
-  q.bad = false;
+  q.bad = 0;
   if (q.rows == 0 || q.n == 0) return q;
   if (q.n < 0 || q.n > bt.max_seq_len || q.rows < 0 || q.rows > bt.max_block_len || q.s < 0 || q.rows > q.n - q.s ||
       q.cub < 0 || q.rows > bt.total_block_rows - q.cub || (q.n + kPage - 1) / kPage > bt.max_pages ||
       (a.full_rows && (q.cus < 0 || q.n > bt.total_seq_rows - q.cus))) {
-    q.bad = true;
+    q.bad = 1;
     return q;
   }
   q.npages = (q.n + kPage - 1) / kPage;
@@ -366,6 +366,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     tma_prefetch_desc(&tm_v);
   }
   if (warp == C::kMmaWarp) tmem_alloc(&tmem_sh, C::kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_sh;
+  // what lies above needs nothing from the kernel before this one; the roles go apart from here, but for large batches
   griddep_wait();
   griddep_launch_dependents();
 
@@ -373,6 +378,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
   const int cta = blockIdx.x;
   long long T = 0, len = 1, lo = 0, start_base = 0;
   int start_b = 0;
+  Seq start_q = {};
   auto cut = [&]() {  // into pieces of len
     len = quotient(T + gridDim.x - 1, gridDim.x);
     lo = min(cta * len, T);
@@ -381,15 +387,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     if (warp == C::kProducerWarp) {  // up to four sequences a lane
       constexpr int kEach = kScan / 32;
       const int per = (bt.batch + 31) / 32;
+      Seq q[kEach];
       long long w[kEach], sum = 0;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         w[i] = 0;
         const int b = lane * per + i;
+        q[i] = Seq{};
         if (i >= per || b >= bt.batch) continue;
-        const Seq q = load_seq<NQ>(a, b);
-        if (q.bad && cta == 0) report_error(bt.err, kErrBadShape);
-        w[i] = seq_work<NQ>(a, q);
+        q[i] = load_seq<NQ>(a, b);
+        if (q[i].bad && cta == 0) report_error(bt.err, kErrBadShape);
+        w[i] = seq_work<NQ>(a, q[i]);
         sum += w[i];
       }
       long long incl = sum;
@@ -403,6 +411,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       long long at = incl - sum;
       int b = lane * per;
       const unsigned mine = __ballot_sync(0xffffffffu, at <= lo && lo < incl);
+      Seq here = q[0];
       bool passing = true;  // the lane's sequences that end at or before lo
 #pragma unroll
       for (int i = 0; i < kEach - 1; ++i) {
@@ -410,11 +419,16 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
         if (passing) {
           at += w[i];
           ++b;
+          here = q[i + 1];
         }
       }
       const int src = mine != 0 ? __ffs(mine) - 1 : 0;
       start_b = __shfl_sync(0xffffffffu, b, src);
       start_base = __shfl_sync(0xffffffffu, at, src);
+      int* const to = reinterpret_cast<int*>(&start_q);
+      const int* const from = reinterpret_cast<const int*>(&here);
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(Seq) / sizeof(int)); ++i) to[i] = __shfl_sync(0xffffffffu, from[i], src);
     }
   } else {
     const int per = (bt.batch + kScan - 1) / kScan;
@@ -458,12 +472,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
       const int src = mine != 0 ? __ffs(mine) - 1 : 0;
       start_b = __shfl_sync(0xffffffffu, b, src);
       start_base = __shfl_sync(0xffffffffu, at, src);
+      if (lo < T) start_q = load_seq<NQ>(a, start_b);
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_sh;
   // the ring's order: K of the next tile before V of this one, which is needed later (the last tile's V leaves the place
   // of the K that does not follow empty)
   auto k_index = [](int n) { return n == 0 ? 0 : 2 * n - 1; };
@@ -475,7 +486,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     // The copies of a tile are issued by lanes of one instruction each (K or V: a page a lane; the four pieces of scales):
     // a single thread that issued them one after the other was the slowest part of the CTA.
     const long long hi = min(lo + len, T);
-    Walk<NQ> walk(a, start_b, lo < hi ? load_seq<NQ>(a, start_b) : Seq{}, start_base, lo, hi);
+    Walk<NQ> walk(a, start_b, start_q, start_base, lo, hi);
     int slot = 0, phase = 0, issued = 0, nt = 0, n_parts = 0;
     bool ok = true;
     auto hand_over = [&](bool any) {  // the walk's part, or that there is no more
@@ -522,8 +533,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
     int y_last = 0, pages_last = 0;  // the last tile, whose V is still to be asked for
     uint64_t policy_last = again;
     bool have = walk.next();
-    hand_over(have);
     int ids_next = have ? page_ids(bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages, 2 * walk.t0, walk.q.npages) : 0;
+    hand_over(have);
     while (have && ok) {
       // this part's values: the walk goes on to the next before its end, whose page ids and rows of q are asked for ahead
       const int32_t* const row = bt.block_table + static_cast<size_t>(walk.b) * bt.max_pages;
