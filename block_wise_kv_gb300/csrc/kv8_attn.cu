@@ -983,31 +983,24 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const Kv8Attn
   const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31, cta = blockIdx.x;
   griddep_wait();
   griddep_launch_dependents();
-  const int2 record = __ldcg(static_cast<const int2*>(a.ws) + cta);
-  if (r >= record.y) return;
   const float* const parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + kRecordBytes);
   const float* const first = parts + (static_cast<size_t>(cta) * 2 + 1) * C::kPartFloats;
   auto part = [&](int i) { return i == 0 ? first : parts + static_cast<size_t>(cta + i) * 2 * C::kPartFloats; };
+  const int2 record = __ldcg(static_cast<const int2*>(a.ws) + cta);
+  if (r >= record.y) return;
   const long long row = __ldcg(reinterpret_cast<const long long*>(first + NQ * (D + 2)) + r);
   float top = attn::neg_inf(), o[kE], total = 0.f;
 #pragma unroll
   for (int e = 0; e < kE; ++e) o[e] = 0.f;
-  for (int i0 = 0; i0 < record.x; i0 += 32) {  // a piece a lane for R and l, then the pieces' rows, kFlight under way at a time
+  for (int i0 = 0; i0 < record.x; i0 += 32) {  // a piece a lane for R and l, the pieces' rows kFlight at a time
     const int n = min(32, record.x - i0);
     const float* const mine = part(i0 + min(lane, n - 1)) + NQ * D + r;
-    const float ref = lane < n ? __ldcg(mine) : attn::neg_inf(), sum = lane < n ? __ldcg(mine + NQ) : 0.f;
-    float now = ref;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
-    now = fmaxf(now, top);
-    const float keep = exp2f(top - now), w = exp2f(ref - now);
-    top = now;
-    float add = w * sum;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
-    total = fmaf(total, keep, add);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] *= keep;
+    float ref = attn::neg_inf(), sum = 0.f;
+    if (lane < n) {
+      ref = __ldcg(mine);
+      sum = __ldcg(mine + NQ);
+    }
+    float w = 0.f;
     for (int j0 = 0; j0 < n; j0 += kFlight) {
       float v[kFlight][kE];
 #pragma unroll
@@ -1018,6 +1011,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const Kv8Attn
           *reinterpret_cast<float4*>(v[j]) = __ldcg(reinterpret_cast<const float4*>(src));
         else
           *reinterpret_cast<float2*>(v[j]) = __ldcg(reinterpret_cast<const float2*>(src));
+      }
+      if (j0 == 0) {  // the weights, while the first rows are on their way
+        float now = ref;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+        now = fmaxf(now, top);
+        const float keep = exp2f(top - now);
+        w = exp2f(ref - now);
+        top = now;
+        float add = w * sum;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) add += __shfl_xor_sync(0xffffffffu, add, d);
+        total = fmaf(total, keep, add);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) o[e] *= keep;
       }
 #pragma unroll
       for (int j = 0; j < kFlight; ++j) {
