@@ -46,6 +46,7 @@ DLLM_ROWS_BLOCK = 0
 DLLM_ROWS_FULL = 1
 
 PAGE = 64
+_BF16, _INT32 = torch.bfloat16, torch.int32
 KV8_GROUP = 16  # token positions that share a scale of the 8-bit cache
 
 # Every symbol include/dllm.h declares.
@@ -287,6 +288,9 @@ def dllm_block_ffn(desc, batch, d_ff, o_full, x_block, w_o, ffn_gain, w_gate_up,
 # tensors only and do no more than their arguments need.
 def dllm_batch_plan(batch, pages_held, pages_held_out, block_table, cu_block, cu_seq, ring, row_slot=None,
                     row_seq=None, row_pos=None, stream=None):
+    for t in (pages_held, pages_held_out, block_table, cu_block, cu_seq, row_slot, row_seq, row_pos):
+        if t is not None and t.dtype is not _INT32:
+            raise DllmError("dllm_batch_plan", DLLM_ERR_INVALID_ARGUMENT)
     status = (_lib or load()).dllm_batch_plan(
         ctypes.byref(batch), pages_held.data_ptr(), pages_held_out.data_ptr(), block_table.data_ptr(),
         cu_block.data_ptr(), cu_seq.data_ptr(), ctypes.byref(ring), None if row_slot is None else row_slot.data_ptr(),
@@ -299,8 +303,9 @@ def dllm_batch_plan(batch, pages_held, pages_held_out, block_table, cu_block, cu
 def dllm_kv8_write(desc, batch, k_rows: torch.Tensor, v_rows: torch.Tensor, kv8, stream=None):
     """k_rows, v_rows: bf16 [M][n_kv_heads][head_dim], the last dimension
     contiguous (views of a wider projection output are fine)."""
-    ks, vs = k_rows.stride(), v_rows.stride()
-    if len(ks) != 3 or len(vs) != 3 or ks[2] != 1 or vs[2] != 1:
+    ks, vs, shape = k_rows.stride(), v_rows.stride(), k_rows.shape
+    if (len(ks) != 3 or shape != v_rows.shape or ks[2] != 1 or vs[2] != 1 or shape[1] != kv8.n_kv_heads
+            or shape[2] != desc.head_dim or k_rows.dtype is not _BF16 or v_rows.dtype is not _BF16):
         raise DllmError("dllm_kv8_write", DLLM_ERR_INVALID_ARGUMENT)
     status = (_lib or load()).dllm_kv8_write(
         ctypes.byref(desc), ctypes.byref(batch), k_rows.data_ptr(), ks[0], ks[1], v_rows.data_ptr(), vs[0], vs[1],
@@ -326,8 +331,9 @@ def dllm_kv8_attention_workspace_size(desc, batch, kv8) -> int:
 def dllm_kv8_attention(desc, batch, q: torch.Tensor, kv8, o, lse, ws, o_rows: int = DLLM_ROWS_BLOCK, stream=None):
     """q: bf16 [M][n_heads][head_dim], rows contiguous, any row stride.  lse
     may be None; ws: a uint8 tensor of dllm_kv8_attention_workspace_size bytes."""
-    qs = q.stride()
-    if len(qs) != 3 or qs[2] != 1 or qs[1] != q.shape[2]:
+    qs, shape = q.stride(), q.shape
+    if (len(qs) != 3 or qs[2] != 1 or qs[1] != shape[2] or shape[1] != desc.n_heads or shape[2] != desc.head_dim
+            or q.dtype is not _BF16 or o.dtype is not _BF16):
         raise DllmError("dllm_kv8_attention", DLLM_ERR_INVALID_ARGUMENT)
     status = (_lib or load()).dllm_kv8_attention(
         ctypes.byref(desc), ctypes.byref(batch), q.data_ptr(), qs[0], ctypes.byref(kv8), o.data_ptr(), o_rows,

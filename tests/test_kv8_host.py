@@ -130,3 +130,39 @@ def test_binding_checks_layouts():
         dllm.PageRing(i, i[::2], i)
     r = dllm.PageRing(i, i[:2], torch.ones(2, dtype=torch.int32))
     assert r.swapped().state is r.state_out and r.swapped().state_out is r.state and r.c.num_pages == 4
+
+
+def _refused():
+    return pytest.raises(dllm.DllmError, match="invalid argument")
+
+
+@pytest.mark.parametrize("k,v", [((64, 8, 64), (64, 8, 64)), ((64, 4, 128), (64, 4, 128)), ((64, 8, 128), (64, 4, 128)),
+                                 ((8, 64, 128), (8, 64, 128)), ((64, 1024), (64, 1024))])
+def test_binding_checks_the_rows_shapes(k, v):
+    with _refused():
+        dllm.dllm_kv8_write(_desc(), _batch(), torch.zeros(k, dtype=torch.bfloat16), torch.zeros(v, dtype=torch.bfloat16),
+                            _kv8())
+    q = torch.zeros(k, dtype=torch.bfloat16)
+    with _refused():
+        dllm.dllm_kv8_attention(_desc(), _batch(), q, _kv8(), q, None, torch.zeros(4096, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.float32, torch.float8_e4m3fn])
+def test_binding_checks_the_rows_types(dtype):
+    good, bad = torch.zeros(64, 8, 128, dtype=torch.bfloat16), torch.zeros(64, 8, 128).to(dtype)
+    for k, v in ((good, bad), (bad, good)):
+        with _refused():
+            dllm.dllm_kv8_write(_desc(), _batch(), k, v, _kv8())
+    good, bad = torch.zeros(64, 32, 128, dtype=torch.bfloat16), torch.zeros(64, 32, 128).to(dtype)
+    for q, o in ((good, bad), (bad, good)):
+        with _refused():
+            dllm.dllm_kv8_attention(_desc(), _batch(), q, _kv8(), o, None, torch.zeros(4096, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("which", range(8))
+def test_binding_checks_the_plans_types(which):
+    t = [torch.zeros(8, dtype=torch.int32) for _ in range(8)]
+    t[which] = t[which].long()
+    ring = dllm.PageRing(torch.zeros(4, dtype=torch.int32), *torch.zeros(2, 2, dtype=torch.int32))
+    with _refused():
+        dllm.dllm_batch_plan(_batch(), *t[:5], ring.c, *t[5:])
