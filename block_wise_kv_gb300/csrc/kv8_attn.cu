@@ -28,7 +28,7 @@
 // Roles of a CTA's warps: groups of four softmax warps (TMEM lane = key, then = column of
 // O^T; 16 rows to a group), one TMA producer, one MMA issuer.  K and V tiles share one ring of 16 KB slots (8 KB for
 // d = 64).  The tensor core has the next tile's S done, from the moment the scores are in
-// registers, while the softmax works.  Two CTAs an SM cover each other's serial parts.
+// registers, while the softmax works.  Two or three CTAs an SM cover each other's serial parts.
 //
 // Split: the tiles of all units form one line, cut into as many equal pieces as CTAs
 // (or fewer, where there are few tiles): a ragged batch or one long sequence loads all
@@ -48,7 +48,6 @@ namespace dllm {
 namespace {
 
 constexpr int kTile = 128;  // keys per tile: two pages
-constexpr int kCtasPerSm = 2;
 constexpr int kScaleSlots = 8;       // tiles whose scales are in shared memory
 constexpr int kMaxCtas = 1024;       // of a launch (records of the workspace)
 constexpr size_t kRecordBytes = kMaxCtas * sizeof(int2);
@@ -64,10 +63,17 @@ constexpr float kLimit = 32768.f;  // what a weight x value scale may reach befo
 // What a unit's beginning and end cost, in tiles (see the split above; 4.2, 1.7 and 1.9 by a fit to the CTAs' times).
 __host__ __device__ constexpr int unit_tiles(int nq) { return nq == 64 ? 4 : 2; }
 
+// CTAs an SM (of a unit's width): with 16 rows, memory's latency is what more of them cover, 96 registers a thread still
+// do, and three slots of the ring hold a tile and the next key tile (64 sequences of up to 16384 keys: 156.7 us with two,
+// 151.7 with three, 199 with four, whose rings of two slots run dry; 131072 keys: 84.8, 81.6, 84.5).  Wider units' softmax
+// needs the registers: 32 rows took 45.0 us with two CTAs of 16 rows a thread, 49.0 with three of 32 rows a thread.
+constexpr int ctas_per_sm(int nq) { return nq == 16 ? 3 : 2; }
+
 // NQ rows to a unit, handled by NQ / kCols groups of four softmax warps (a thread: one key, kCols rows).
 template <int D, int NQ>
 struct Cfg {
   static constexpr int kCols = NQ == 64 ? 32 : 16;
+  static constexpr int kCtas = ctas_per_sm(NQ);
   static constexpr int kGroups = NQ / kCols;
   static constexpr int kSoft = 128 * kGroups;  // softmax threads
   static constexpr uint32_t kTmemCols = 4 * NQ;  // S^T, O^T of the three parts
@@ -80,11 +86,11 @@ struct Cfg {
   static constexpr int kPRow = NQ == 32 ? 128 : 64;
   static constexpr int kPBytes = kTile * kPRow * (kPlanes ? 3 : 1);
   static constexpr int kStatic = NQ == 64 ? 5632 : NQ == 32 ? 4352 : 3456;  // static shared memory, at most
-  static constexpr int kBudget = 113 * 1024 - 1024 - kStatic;  // two CTAs an SM; 1 KB to align
+  static constexpr int kBudget = 227 * 1024 / kCtas - 2048 - kStatic;  // 1 KB to align, 1 KB of the system's a CTA
   static constexpr int kSlots0 = (kBudget - kQBytes - kPBytes) / kSlotBytes;
   static constexpr int kSlots = kSlots0 > 10 ? 10 : kSlots0;
   static constexpr int kDynSmem = kSlots * kSlotBytes + kQBytes + kPBytes + 1024;
-  static_assert(kSlots >= 4, "a tile's K and V, and the next tile's");
+  static_assert(kSlots >= 2, "a tile's V needs a slot beside the next tile's K");
   static_assert(kSlots / 2 + 2 < kScaleSlots, "scales stay until the softmax has read them");
   static constexpr size_t kPartFloats = static_cast<size_t>(NQ) * (D + 4);  // O, R, l, rows
 };
@@ -324,7 +330,7 @@ struct Walk {
 
 // ------------------------------------------------------------ the kernel
 template <int D, int NQ>
-__global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
     kv8_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const Kv8AttnArgs a) {
   using C = Cfg<D, NQ>;
@@ -1062,7 +1068,7 @@ cudaError_t encode_codes(CUtensorMap* map, const void* ptr, uint64_t rows) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-int grid_of(int num_sms) { return std::min(kCtasPerSm * num_sms, kMaxCtas); }
+int grid_of(int nq, int num_sms) { return std::min(ctas_per_sm(nq) * num_sms, kMaxCtas); }
 
 template <int D, int NQ>
 cudaError_t launch(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
@@ -1073,7 +1079,7 @@ cudaError_t launch(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
   if (e == cudaSuccess) e = encode_codes<D>(&tv, a.kv.v, rows);
   if (e == cudaSuccess) e = attn::set_smem(kv8_attn_kernel<D, NQ>, C::kDynSmem);
   if (e != cudaSuccess) return e;
-  const int grid = grid_of(num_sms);
+  const int grid = grid_of(NQ, num_sms);
   e = attn::launch_pdl(kv8_attn_kernel<D, NQ>, dim3(grid), C::kThreads, C::kDynSmem, 0, stream, tk, tv, a);
   if (e != cudaSuccess || a.whole_units) return e;
   const int64_t most = static_cast<int64_t>(a.bt.max_block_len) * (a.n_heads / a.kv.n_kv_heads);
@@ -1094,7 +1100,7 @@ int unit_rows(int max_block_len, int n_heads, int n_kv_heads) {
 
 size_t kv8_attention_workspace_bytes(int max_block_len, int n_heads, int n_kv_heads, int head_dim, int num_sms) {
   const size_t nq = unit_rows(max_block_len, n_heads, n_kv_heads);
-  return kRecordBytes + static_cast<size_t>(grid_of(num_sms)) * 2 * nq * (head_dim + 4) * sizeof(float);
+  return kRecordBytes + static_cast<size_t>(grid_of(static_cast<int>(nq), num_sms)) * 2 * nq * (head_dim + 4) * sizeof(float);
 }
 
 cudaError_t launch_kv8_attention(const Kv8AttnArgs& args, int num_sms, cudaStream_t stream) {
