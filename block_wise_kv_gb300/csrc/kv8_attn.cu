@@ -16,8 +16,9 @@
 // A weight is rounded to fp16 (11 bits) and split into three e5m2 parts, which is
 // exact (3 bits each, rounded to nearest) but for an absolute 2^-17, half of the
 // smallest e5m2 step, where a row's largest is 2^10 or more: a softmax with one large
-// weight and a long flat tail that together weighs as much keeps its tail.  The value scale of a key multiplies
-// its weight before the split; the sum l takes the weight without it.
+// weight and a long flat tail that together weighs as much keeps its tail.  The value
+// scale of a key multiplies its weight before the split; the sum l takes the weight
+// without it.
 //
 // The thread that holds a key's scores has its scales as two scalars; a row's
 // reference R is the same for all 128 keys.  R is set from a unit's first tile (so
@@ -25,20 +26,31 @@
 // a vote per tile, and otherwise no reduction over keys at all until the unit's end,
 // where the 128 partial sums of each row are added.
 //
-// Roles of a CTA's warps: groups of four softmax warps (TMEM lane = key, then = column of
-// O^T; 16 rows to a group), one TMA producer, one MMA issuer.  K and V tiles share one ring of 16 KB slots (8 KB for
-// d = 64).  The tensor core has the next tile's S done, from the moment the scores are in
-// registers, while the softmax works.  Two or three CTAs an SM cover each other's serial parts.
+// Roles of a CTA's warps: groups of four softmax warps (TMEM lane = key, then = column
+// of O^T; 16 rows to a group, 32 in units of 64), one TMA producer, one MMA issuer.  K
+// and V tiles share one ring of 16 KB slots (8 KB for d = 64).  The tensor core has the
+// next tile's S done, from the moment the scores are in registers, while the softmax
+// works.  Two or three CTAs an SM cover each other's serial parts.
 //
 // Split: the tiles of all units form one line, cut into as many equal pieces as CTAs
 // (or fewer, where there are few tiles): a ragged batch or one long sequence loads all
 // SMs alike.  Each unit stands there with two to four more than it has: what q, the first
 // reference and the output cost.  (Without them the CTAs that got the many short units of
-// a ragged batch took 1.6 times the mean.)  A unit cut by a border leaves its pieces' (O, R, l) in the workspace, and a
-// second, small kernel joins them in the order of the keys, a warp for each row (not
-// launched, and no unit cut, where no sequence has more than kWholeTiles tiles): with the
-// ring full, every dependent trip to memory (fence, counter, reads) costs the attention's
-// warps several microseconds, which a join inside the kernel had to wait for.
+// a ragged batch took 1.6 times the mean.)  A unit cut by a border leaves its pieces'
+// (O, R, l) in the workspace, and a second, small kernel joins them in the order of the
+// keys, a warp for each row (not launched, and no unit cut, where no sequence has more
+// than kWholeTiles tiles): with the ring full, every dependent trip to memory (fence,
+// counter, reads) costs the attention's warps several microseconds, which a join inside
+// the kernel had to wait for.
+//
+// Bound and measured (d = 128): single tokens and long contexts by HBM (64 sequences of up
+// to 16384 keys, 8 key heads: 152 to 159 us, 6.3 to 6.5 TB/s; two of 131072: 82 us, 6.0
+// TB/s with the join).  Wider units by the softmax of a tile, 2.0 us a tile and CTA for 64
+// rows, 1.35 for 32, with 16 softmax warps an SM (what the registers hold) and the issue
+// slots half busy: 32 ragged sequences of up to 4608 keys, blocks of 16 to 64: 136 us, 4.3
+// TB/s; eight sequences with 128 rows to a key head: 43 us.  16 sequences of 1536 with
+// blocks of 32: 45 us, 4.7 TB/s (42 without any traffic).  One sequence of 768: 12 us, of
+// which the two launches take 3.4, the line 1.1 and the join 3.7.
 #include <algorithm>
 
 #include "attn_common.cuh"
@@ -52,9 +64,11 @@ constexpr int kScaleSlots = 8;       // tiles whose scales are in shared memory
 constexpr int kMaxCtas = 1024;       // of a launch (records of the workspace)
 constexpr size_t kRecordBytes = kMaxCtas * sizeof(int2);
 // Sequences of up to this many tiles are not cut: three more tiles in a row take about what the second launch does
-// (320 tokens of 4 heads: 10.4 us cut and joined, 9.8 whole, and a launch less).
+// (320 tokens of 4 heads: 9.5 us cut and joined, 9.2 whole, and 1.7 us less on the host).
 constexpr int kWholeTiles = 4;
-constexpr int kScan = 128;           // threads that sum up a large batch's work
+// Up to this many sequences are summed up by the producer warp alone, four a lane; beyond, by as many threads through
+// shared memory, behind a barrier of the CTA (with that way for 16 sequences: 46.0 us for 44.9, one sequence 12.8 for 11.9).
+constexpr int kScan = 128;
 constexpr int kParts = 16;           // parts of units in shared memory: the producer is fewer than 8 tiles ahead
 constexpr float kTop = 10.f;    // log2 of a row's largest weight x value scale when R is set
 constexpr float kLimitLog2 = 15.f;
@@ -734,8 +748,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
           row_sh[par][tid] = a.full_rows ? part.cus + part.s + i : part.cub + i;
           nref_sh[par][tid] = 0.f;
         }
-      }
-      if (have) {
         soft_sync();
         // q in two e4m3 parts
         float amax = amax_sh[0];
@@ -782,7 +794,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
         const int cols = done.cols, was = par ^ 1;
         {
           float v[kCols];
-  #pragma unroll
+#pragma unroll
           for (int c = 0; c < kCols / 2; ++c) {
             const float2 p = unpack2(l[c]);
             v[2 * c] = p.x;
@@ -1089,8 +1101,11 @@ cudaError_t launch(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
 }
 
 // Rows that share a key head, at most: the smallest of 16, 32 and 64 that holds them, and units of 64 beyond.  A tile
-// costs the softmax its NQ columns whether they are rows or not, so the narrow units are what keeps single tokens and
-// blocks of 32 bound by memory; a unit wider than 64 rows would read the keys fewer times, but does not fit twice on an SM.
+// costs the softmax its NQ columns whether they are rows or not: 16 sequences with blocks of 32 take 45 us in units of
+// 32, 57 in units of 64, one sequence 11.9 and 14.4.  Four rows to a key head are bound by memory either way, and 16
+// leave it a little more of the SM: two contexts of 131072 keys 82.5 us in units of 16, 83.7 in units of 32 (64 single
+// tokens 153.7 and 154.1).  128 rows in two units of 64 read the keys twice, 43 us where the bytes take 10; one unit of
+// 128 would have the same softmax to do and fill the TMEM of an SM alone.
 int unit_rows(int max_block_len, int n_heads, int n_kv_heads) {
   const int64_t rows = static_cast<int64_t>(max_block_len) * (n_heads / n_kv_heads);
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
