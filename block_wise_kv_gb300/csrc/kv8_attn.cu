@@ -934,15 +934,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free);  // the scores are in registers
-        if (nt > 0) wait(&pv_done, nt - 1);  // P's buffer is free
-        if (valid < kTile) {                  // what lies behind the end must not meet a weight, not even 0
-          const int vi = v_index(nt);
-          wait(&full_bar[vi % C::kSlots], vi / C::kSlots);
-          if (tid >= valid && tid < kTile) {
-#pragma unroll 1
-            for (int i = 0; i < D / 16; ++i) st_shared_v4(ring + (vi % C::kSlots) * C::kSlotBytes + tid * D + i * 16, 0, 0, 0, 0);
-          }
-        }
         const uint64_t sv2 = pack2(sv, sv);
 #pragma unroll
         for (int c0 = 0; c0 < kCols; c0 += 16) {
@@ -971,12 +962,21 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
 #pragma unroll
             for (int z = 0; z < 3; ++z) part[z][j] = __byte_perm(w[z][0], w[z][1], 0x7531);
           }
+          if (c0 == 0 && nt > 0) wait(&pv_done, nt - 1);  // P's buffer is free
           const int chunk = (col0 + c0) / 16;
 #pragma unroll
           for (int z = 0; z < 3; ++z) {
             const uint32_t at = C::kPlanes ? p_base + z * kTile * C::kPRow + swz<C::kPRow>(key, chunk)
                                            : p_base + swz<C::kPRow>(key, z * (NQ / 16) + chunk);
             st_shared_v4(at, part[z][0], part[z][1], part[z][2], part[z][3]);
+          }
+        }
+        if (valid < kTile) {                  // what lies behind the end must not meet a weight, not even 0
+          const int vi = v_index(nt);
+          wait(&full_bar[vi % C::kSlots], vi / C::kSlots);
+          if (tid >= valid && tid < kTile) {
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) st_shared_v4(ring + (vi % C::kSlots) * C::kSlotBytes + tid * D + i * 16, 0, 0, 0, 0);
           }
         }
         tc_fence_before();
