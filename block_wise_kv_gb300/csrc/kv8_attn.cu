@@ -44,7 +44,7 @@
 // the kernel had to wait for.
 //
 // Bound and measured (d = 128): single tokens and long contexts by HBM (64 sequences of up
-// to 16384 keys, 8 key heads: 152 to 159 us, 6.3 to 6.5 TB/s; two of 131072: 82 us, 6.0
+// to 16384 keys, 8 key heads: 152 us, 6.6 TB/s; two of 131072: 83 us, 6.0
 // TB/s with the join).  Wider units by the softmax of a tile, 2.0 us a tile and CTA for 64
 // rows, 1.35 for 32, with 16 softmax warps an SM (what the registers hold) and the issue
 // slots half busy: 32 ragged sequences of up to 4608 keys, blocks of 16 to 64: 136 us, 4.3
@@ -79,7 +79,7 @@ __host__ __device__ constexpr int unit_tiles(int nq) { return nq == 64 ? 4 : 2; 
 
 // CTAs an SM (of a unit's width): with 16 rows, memory's latency is what more of them cover, 96 registers a thread still
 // do, and three slots of the ring hold a tile and the next key tile (64 sequences of up to 16384 keys: 156.7 us with two,
-// 151.7 with three, 199 with four, whose rings of two slots run dry; 131072 keys: 84.8, 81.6, 84.5).  Wider units' softmax
+// 151 with three, 199 with four, whose rings of two slots run dry; two of 131072 keys: 84.8, 83, 84.5).  Wider units' softmax
 // needs the registers: 32 rows took 45.0 us with two CTAs of 16 rows a thread, 49.0 with three of 32 rows a thread.
 constexpr int ctas_per_sm(int nq) { return nq == 16 ? 3 : 2; }
 
@@ -1000,7 +1000,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const Kv8Attn
   constexpr int kE = D / 32, kFlight = 4;
   const int r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31, cta = blockIdx.x;
   griddep_wait();
-  griddep_launch_dependents();
+  // Three CTAs leave little of an SM's shared memory: where the next attention starts beside this kernel's blocks, which
+  // hold a piece each, some SMs are left with gaps that fit two, and the last CTAs begin when the first end (about every
+  // third call took 200 us for 150).  So there the next kernel starts when this one is done.
+  if (C::kCtas < 3) griddep_launch_dependents();
   const float* const parts = reinterpret_cast<const float*>(static_cast<const uint8_t*>(a.ws) + kRecordBytes);
   const float* const first = parts + (static_cast<size_t>(cta) * 2 + 1) * C::kPartFloats;
   auto part = [&](int i) { return i == 0 ? first : parts + static_cast<size_t>(cta + i) * 2 * C::kPartFloats; };
