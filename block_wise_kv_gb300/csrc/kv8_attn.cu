@@ -240,6 +240,13 @@ __device__ __forceinline__ void tmem_load3(uint32_t taddr, uint32_t step, float 
   for (int c = 0; c < 16; ++c) v[c] = (__uint_as_float(r[0][c]) + __uint_as_float(r[1][c])) + __uint_as_float(r[2][c]);
 }
 
+// One lane of the warp, which is converged.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // Wait for the phase with the given parity, at most 2^18 tries of up to 20 us each (seconds), in few instructions: the
 // kernel's roles share the instruction cache.  False where it gave up.
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
@@ -617,45 +624,44 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
     }
   } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = idesc_f8(kTile, NQ, false, false);
-      constexpr uint32_t kIdescO = idesc_f8(kTile, 3 * NQ, true, true);
-      const uint32_t tm_o = tmem + NQ;
-      const uint64_t q_desc = desc_rows<D>(q_base), p_desc = desc_rows<C::kPRow>(p_base, C::kPlanes ? kTile * C::kPRow : 0);
-      int nt = 0, unit = 0;
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, int parity) {
-        if (ok && !wait_phase(bar, parity & 1)) {
-          report_error(bt.err, kErrTimeout);
-          ok = false;
-        }
-        return ok;
-      };
-      bool pending = false, fresh = false;  // a tile whose P V is still to be issued; the first of its unit
-      auto issue_pv = [&](int n) {          // tile number n of this CTA
-        const int i = v_index(n), s = i % C::kSlots;
-        if (!wait(&p_ready, n) || !wait(&full_bar[s], i / C::kSlots)) return;
-        tc_fence_after();
-        const uint64_t v = desc_rows<D>(ring + s * C::kSlotBytes);  // (a step of n bytes adds n / 16 to the address field)
+    // All of the warp goes through the loop, and its conditions are the same for every lane by votes: descriptors and
+    // counters can stay in the warp's uniform registers, which is where a product takes them from.  (One lane alone: 16
+    // sequences of 1536 keys 44.9 us for 44.5, 128 rows to a key head 43.4 for 43.0.)
+    constexpr uint32_t kIdescS = idesc_f8(kTile, NQ, false, false);
+    constexpr uint32_t kIdescO = idesc_f8(kTile, 3 * NQ, true, true);
+    const uint32_t tm_o = tmem + NQ;
+    const uint64_t q_desc = desc_rows<D>(q_base), p_desc = desc_rows<C::kPRow>(p_base, C::kPlanes ? kTile * C::kPRow : 0);
+    int nt = 0, unit = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int parity) {
+      if (ok) ok = __all_sync(0xffffffffu, wait_phase(bar, parity & 1));
+      return ok;
+    };
+    auto issue_pv = [&](int n, bool fresh) {  // tile number n of this CTA; the first of its part
+      const int i = v_index(n), s = i % C::kSlots;
+      if (!wait(&p_ready, n) || !wait(&full_bar[s], i / C::kSlots)) return;
+      tc_fence_after();
+      const uint64_t v = desc_rows<D>(ring + s * C::kSlotBytes);  // (a step of n bytes adds n / 16 to the address field)
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kTile / 32; ++k) umma_e4m3(tm_o, v + k * 2 * D, p_desc + k * 2 * C::kPRow, kIdescO, !fresh || k > 0);
         umma_commit(&empty_bar[s]);
         umma_commit(&pv_done);
-      };
-      for (;; ++unit) {
-        if (pending) {
-          issue_pv(nt - 1);
-          pending = false;
-        }
-        if (!wait(&part_bar[unit % kParts], unit / kParts)) break;
-        const int t0 = part_sh[unit % kParts].t0, t1 = part_sh[unit % kParts].t1;
-        if (t1 == 0 || !wait(&q_ready, unit)) break;
-        for (int t = t0; t < t1 && ok; ++t, ++nt) {
-          const int i = k_index(nt), s = i % C::kSlots;
-          if (!wait(&full_bar[s], i / C::kSlots)) break;
-          if (nt > 0 && !wait(&s_free, nt - 1)) break;
-          tc_fence_after();
-          const uint64_t k8 = desc_rows<D>(ring + s * C::kSlotBytes);
+      }
+      __syncwarp();
+    };
+    for (;; ++unit) {
+      if (!wait(&part_bar[unit % kParts], unit / kParts)) break;
+      const Part& part = part_sh[unit % kParts];
+      const int tiles = __reduce_max_sync(0xffffffffu, part.t1 == 0 ? 0 : part.t1 - part.t0);
+      if (tiles == 0 || !wait(&q_ready, unit)) break;
+      for (int t = 0; t < tiles && ok; ++t, ++nt) {
+        const int i = k_index(nt), s = i % C::kSlots;
+        if (!wait(&full_bar[s], i / C::kSlots)) break;
+        if (nt > 0 && !wait(&s_free, nt - 1)) break;
+        tc_fence_after();
+        const uint64_t k8 = desc_rows<D>(ring + s * C::kSlotBytes);
+        if (elect_one()) {
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -663,17 +669,19 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
               umma_e4m3(tmem, k8 + k * 2, q_desc + (part * NQ * D + k * 32) / 16, kIdescS, part > 0 || k > 0);
           umma_commit(&empty_bar[s]);
           umma_commit(&s_full);
-          if (pending) issue_pv(nt - 1);
-          pending = true;
-          fresh = t == t0;
         }
+        __syncwarp();
+        if (t > 0) issue_pv(nt - 1, t == 1);
       }
-      // the softmax warps wait for the last S and P V, the producer for the releases; where a wait gave up, the
-      // products that were issued end before the CTA does
-      if (!ok) {
-        umma_commit(&drain_bar);
-        if (!wait_phase(&drain_bar, 0)) report_error(bt.err, kErrTimeout);
-      }
+      if (ok) issue_pv(nt - 1, tiles == 1);
+    }
+    // the softmax warps wait for the last S and P V, the producer for the releases; where a wait gave up, the
+    // products that were issued end before the CTA does
+    if (!ok) {
+      if (lane == 0) report_error(bt.err, kErrTimeout);
+      if (elect_one()) umma_commit(&drain_bar);
+      __syncwarp();
+      if (!wait_phase(&drain_bar, 0) && lane == 0) report_error(bt.err, kErrTimeout);
     }
   } else {
     // ------------------------------------------------------------ softmax
@@ -1107,7 +1115,7 @@ cudaError_t launch(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
 // costs the softmax its NQ columns whether they are rows or not: 16 sequences with blocks of 32 take 45 us in units of
 // 32, 57 in units of 64, one sequence 11.9 and 14.4.  Four rows to a key head are bound by memory either way, and 16
 // leave it a little more of the SM: two contexts of 131072 keys 82.5 us in units of 16, 83.7 in units of 32 (64 single
-// tokens 153.7 and 154.1).  128 rows in two units of 64 read the keys twice, 43 us where the bytes take 10; one unit of
+// tokens 151 and 154).  128 rows in two units of 64 read the keys twice, 43 us where the bytes take 10; one unit of
 // 128 would have the same softmax to do and fill the TMEM of an SM alone.
 int unit_rows(int max_block_len, int n_heads, int n_kv_heads) {
   const int64_t rows = static_cast<int64_t>(max_block_len) * (n_heads / n_kv_heads);
