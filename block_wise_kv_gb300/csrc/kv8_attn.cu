@@ -99,7 +99,7 @@ struct Cfg {
   static constexpr bool kPlanes = NQ == 64;
   static constexpr int kPRow = NQ == 32 ? 128 : 64;
   static constexpr int kPBytes = kTile * kPRow * (kPlanes ? 3 : 1);
-  static constexpr int kStatic = NQ == 64 ? 5632 : NQ == 32 ? 4352 : 3456;  // static shared memory, at most
+  static constexpr int kStatic = NQ == 64 ? 6144 : NQ == 32 ? 4608 : 3584;  // static shared memory, at most
   static constexpr int kBudget = 227 * 1024 / kCtas - 2048 - kStatic;  // 1 KB to align, 1 KB of the system's a CTA
   static constexpr int kSlots0 = (kBudget - kQBytes - kPBytes) / kSlotBytes;
   static constexpr int kSlots = kSlots0 > 10 ? 10 : kSlots0;
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
   // (two of what the end of a unit still reads when the next has begun)
   __shared__ __align__(16) float nref_sh[2][NQ], alpha_sh[NQ], l_sh[NQ], inv_sh[NQ];
   __shared__ float red_sh[4][NQ];
-  __shared__ int row_sh[2][NQ];  // row of the output
+  __shared__ long long row_sh[2][NQ];  // row and head of the output, as one index
   __shared__ float amax_sh[4 * C::kGroups];
   __shared__ long long seg_sh[kScan + 1];
 
@@ -752,8 +752,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
         }
         if (lane == 0) amax_sh[warp] = __uint_as_float(m << 16);
         if (tid < NQ) {
-          const int i = (part.r0 + tid) / G;
-          row_sh[par][tid] = a.full_rows ? part.cus + part.s + i : part.cub + i;
+          const int r = part.r0 + tid, i = r / G;
+          row_sh[par][tid] = static_cast<long long>(a.full_rows ? part.cus + part.s + i : part.cub + i) * a.n_heads + part.h * G +
+                             (r - i * G);
           nref_sh[par][tid] = 0.f;
         }
         soft_sync();
@@ -821,7 +822,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
         soft_sync();
         tc_fence_after();
         const bool began = done.t0 == 0, whole = began && done.t1 == done.tiles;
-        const int head = done.h * G, r0 = done.r0;
         float* const mine = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + kRecordBytes) +
                             (static_cast<size_t>(cta) * 2 + (began ? 1 : 0)) * C::kPartFloats;
 #pragma unroll 1
@@ -831,13 +831,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
           if (key >= D) continue;
           if (whole) {
             __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.o) + key;
-            int j = (r0 + c0) % G;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              if (c0 + c < cols)
-                out[(static_cast<size_t>(row_sh[was][c0 + c]) * a.n_heads + head + j) * D] = __float2bfloat16(o[c] * inv_sh[c0 + c]);
-              if (++j == G) j = 0;
-            }
+            for (int c = 0; c < 16; ++c)
+              if (c0 + c < cols) out[row_sh[was][c0 + c] * D] = __float2bfloat16(o[c] * inv_sh[c0 + c]);
           } else {
 #pragma unroll
             for (int c = 0; c < 16; ++c)
@@ -846,15 +842,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
         }
         if (whole) {
           if (a.lse != nullptr && tid < cols)
-            a.lse[static_cast<size_t>(row_sh[was][tid]) * a.n_heads + head + (r0 + tid) % G] =
-                (log2f(l_sh[tid]) - nref_sh[was][tid]) * attn::kLn2;
+            a.lse[row_sh[was][tid]] = (log2f(l_sh[tid]) - nref_sh[was][tid]) * attn::kLn2;
         } else {
           if (tid < cols) {
             mine[NQ * D + tid] = -nref_sh[was][tid];
             mine[NQ * (D + 1) + tid] = l_sh[tid];
-            if (began)
-              reinterpret_cast<long long*>(mine + NQ * (D + 2))[tid] =
-                  static_cast<long long>(row_sh[was][tid]) * a.n_heads + head + (r0 + tid) % G;
+            if (began) reinterpret_cast<long long*>(mine + NQ * (D + 2))[tid] = row_sh[was][tid];
           }
           if (began) record = make_int2(done.c_last - cta + 1, cols);
         }
