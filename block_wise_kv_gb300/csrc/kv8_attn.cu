@@ -34,7 +34,7 @@
 //
 // Split: the tiles of all units form one line, cut into as many equal pieces as CTAs
 // (or fewer, where there are few tiles): a ragged batch or one long sequence loads all
-// SMs alike.  Each unit stands there with two to four more than it has: what q, the first
+// SMs alike.  Each unit stands there with two or three more than it has: what q, the first
 // reference and the output cost.  (Without them the CTAs that got the many short units of
 // a ragged batch took 1.6 times the mean.)  A unit cut by a border leaves its pieces'
 // (O, R, l) in the workspace, and a second, small kernel joins them in the order of the
@@ -44,13 +44,13 @@
 // the kernel had to wait for.
 //
 // Bound and measured (d = 128): single tokens and long contexts by HBM (64 sequences of up
-// to 16384 keys, 8 key heads: 152 us, 6.6 TB/s; two of 131072: 83 us, 6.0
-// TB/s with the join).  Wider units by the softmax of a tile, 2.0 us a tile and CTA for 64
-// rows, 1.35 for 32, with 16 softmax warps an SM (what the registers hold) and the issue
-// slots half busy: 32 ragged sequences of up to 4608 keys, blocks of 16 to 64: 136 us, 4.3
-// TB/s; eight sequences with 128 rows to a key head: 43 us.  16 sequences of 1536 with
-// blocks of 32: 45 us, 4.7 TB/s (42 without any traffic).  One sequence of 768: 12 us, of
-// which the two launches take 3.4, the line 1.1 and the join 3.7.
+// to 16384 keys, 8 key heads: 151 us, 6.6 TB/s; two of 131072: 83 us, 6.0 TB/s with the
+// join).  Wider units by the chain of a tile (scores, vote, weights, products), 1.9 us a
+// tile and CTA for 64 rows, 1.4 for 32, with 16 softmax warps an SM (what the registers
+// hold) and the issue slots half busy: 32 ragged sequences of up to 4608 keys, blocks of
+// 16 to 64: 131 us, 4.5 TB/s; eight sequences with 128 rows to a key head: 42 us.  16
+// sequences of 1536 with blocks of 32: 44 us, 4.8 TB/s.  One sequence of 768: 12 us, of
+// which the two launches take 3.4, the line 1.1, the join 3.7.
 #include <algorithm>
 
 #include "attn_common.cuh"
@@ -74,8 +74,10 @@ constexpr float kTop = 10.f;    // log2 of a row's largest weight x value scale 
 constexpr float kLimitLog2 = 15.f;
 constexpr float kLimit = 32768.f;  // what a weight x value scale may reach before R is raised
 
-// What a unit's beginning and end cost, in tiles (see the split above; 4.2, 1.7 and 1.9 by a fit to the CTAs' times).
-__host__ __device__ constexpr int unit_tiles(int nq) { return nq == 64 ? 4 : 2; }
+// What a unit's beginning and end cost, in tiles (see the split above): 32 ragged sequences in units of 64 take 139 us
+// with 2, 131 with 3, 132 with 4; 16 of 1536 in units of 32 44.3 with 1, 44.0 with 2; 64 of single tokens in units of 16
+// 151 with 1 or 2, 158 with 3.
+__host__ __device__ constexpr int unit_tiles(int nq) { return nq == 64 ? 3 : 2; }
 
 // CTAs an SM (of a unit's width): with 16 rows, memory's latency is what more of them cover, 96 registers a thread still
 // do, and three slots of the ring hold a tile and the next key tile (64 sequences of up to 16384 keys: 156.7 us with two,
@@ -1105,10 +1107,10 @@ cudaError_t launch(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
 }
 
 // Rows that share a key head, at most: the smallest of 16, 32 and 64 that holds them, and units of 64 beyond.  A tile
-// costs the softmax its NQ columns whether they are rows or not: 16 sequences with blocks of 32 take 45 us in units of
+// costs the softmax its NQ columns whether they are rows or not: 16 sequences with blocks of 32 take 44 us in units of
 // 32, 57 in units of 64, one sequence 11.9 and 14.4.  Four rows to a key head are bound by memory either way, and 16
 // leave it a little more of the SM: two contexts of 131072 keys 82.5 us in units of 16, 83.7 in units of 32 (64 single
-// tokens 151 and 154).  128 rows in two units of 64 read the keys twice, 43 us where the bytes take 10; one unit of
+// tokens 151 and 154).  128 rows in two units of 64 read the keys twice, 42 us where the bytes take 10; one unit of
 // 128 would have the same softmax to do and fill the TMEM of an SM alone.
 int unit_rows(int max_block_len, int n_heads, int n_kv_heads) {
   const int64_t rows = static_cast<int64_t>(max_block_len) * (n_heads / n_kv_heads);
