@@ -187,10 +187,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv8_write_kernel(const K
   griddep_wait();
   griddep_launch_dependents();
   if (t == 0) n_groups = 0;
+  // One CTA compares all blocks with the sums: one that they leave no rows is met by no search below.
+  const bool looks = blockIdx.x == 0 && blockIdx.y == 0;
+  const int len_t = looks && t < bt.batch ? __ldg(bt.block_len + t) : 0;
   if (in_smem)
     for (int i = t; i <= bt.batch; i += kThreads) cu[i] = __ldg(bt.cu_block + i);
   __syncthreads();
   const int* cub = in_smem ? cu : bt.cu_block;
+  for (int b = t; looks && b < bt.batch; b += kThreads)
+    if (cub[b + 1] - cub[b] != (b == t ? len_t : __ldg(bt.block_len + b))) err |= kErrBadShape;
   const int total = min(cub[bt.batch], bt.total_block_rows);
   if (row0 == 0 && t == 0 && (cub[bt.batch] < 0 || cub[bt.batch] > bt.total_block_rows)) err |= kErrBadShape;
   if (row0 >= total) {
@@ -207,11 +212,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv8_write_kernel(const K
       else
         hi = mid;
     }
-    const int b = lo, i = j - cub[b];
+    const int b = lo, first_row = cub[b], next_row = cub[b + 1], i = j - first_row;
     const int n = __ldg(bt.seq_len + b), s = __ldg(bt.block_start + b), len = __ldg(bt.block_len + b);
     const int pos = s + i;
-    if (n < 0 || n > bt.max_seq_len || s < 0 || len < 0 || len > n - s || i < 0 || i >= len ||
-        pos / kPage >= bt.max_pages) {
+    // The whole block lies in its own packed rows and within the bound: a group below reads up to 16 of them from row j on.
+    if (first_row < 0 || next_row < first_row || len > min(next_row, bt.total_block_rows) - first_row || n < 0 ||
+        n > bt.max_seq_len || s < 0 || len < 0 || len > n - s || i < 0 || i >= len || pos / kPage >= bt.max_pages) {
       err |= kErrBadShape;
     } else if (i == 0 || pos % kKv8Group == 0) {
       const int pg = __ldg(bt.block_table + static_cast<size_t>(b) * bt.max_pages + pos / kPage);

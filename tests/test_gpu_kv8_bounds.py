@@ -1,0 +1,109 @@
+"""The 8-bit paged cache's calls on batches that contradict their bounds, or that the plan could not serve: what is
+refused is refused whole, its error bit is set, and no other sequence sees any of it."""
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+from block_wise_kv_gb300 import dllm
+from kv8_util import PAGE, Batch, cu, ints, random_pools, write
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from block_wise_kv_gb300 import build
+
+    build.build()
+    dllm.load()
+    torch.cuda.init()
+
+
+def _desc(H, d):
+    return dllm.layer_desc(max(64, H * d), H, d, 1e4)
+
+
+def _decoded(codes):
+    return codes.view(torch.uint8).view(torch.float8_e4m3fn).float().double().cpu()
+
+
+def _rows(M, heads, d, seed):
+    g = torch.Generator("cuda").manual_seed(seed)
+    return torch.randn(M, heads, d, device="cuda", generator=g).to(torch.bfloat16)
+
+
+def _written(kv8, n, start, rows, table, cub, served, k, v):
+    """The pools after a write in which only the sequences `served` take part."""
+    b = SimpleNamespace(n=n, start=start, rows=[r if i in served else 0 for i, r in enumerate(rows)], table=table)
+    at = [j for i, r in enumerate(rows) if i in served for j in range(cub[i], cub[i] + r)]
+    out = []
+    for codes, scale, new in ((kv8.k, kv8.k_scale, k), (kv8.v, kv8.v_scale, v)):
+        vals, sc = _decoded(codes), scale.double().cpu()
+        write(b, vals, sc, new[at].double().cpu())
+        out.append((vals, sc))
+    return out
+
+
+def _assert_pools(kv8, want):
+    for (codes, scale), (vals, sc) in zip(((kv8.k, kv8.k_scale), (kv8.v, kv8.v_scale)), want):
+        assert torch.equal(scale.double().cpu(), sc)
+        assert torch.equal(_decoded(codes), vals)
+
+
+@pytest.mark.parametrize("start,rows,cub,bound,served", [
+    ([80, 89], [10, 11], [0, 10, 21], 20, [0]),                   # more rows than the bound holds
+    ([80, 87], [10, 13], [0, 10, 20], 20, [0]),                   # a last block longer than its rows
+    ([80, 87, 60], [10, 13, 10], [0, 10, 20, 30], 30, [0, 2]),    # one in the middle: the next one's rows are not its own
+    ([80, 80, 60], [10, 30, 10], [0, 10, 10, 20], 20, [0, 2]),    # one that the sums count as none
+    ([0, 0], [90, 100], [0, 90, 190], 150, [0]),                  # a prompt that the bound cuts
+    ([80, 80], [10, 10], [0, 20, 10], 20, [0]),                   # sums that fall
+])
+@pytest.mark.parametrize("d", [64, 128])
+def test_write_reads_no_row_that_is_not_the_blocks_own(start, rows, cub, bound, served, d):
+    """The rows are the front of a larger tensor; what lies behind them is far larger, so that it would show in a scale."""
+    b = Batch([100] * len(rows), start, rows, seed=1, cap_rows=bound)
+    b.t["cub"].copy_(ints(cub))
+    kv8 = random_pools(b.num_pages, 2, d, 3)
+    wide = [_rows(max(bound, sum(rows), max(cub)) + 64, 2, d, s) for s in (4, 5)]
+    for x in wide:
+        x[bound:] = 3000.0
+    want = _written(kv8, b.n, start, rows, b.table, cub, served, *wide)
+    dllm.dllm_kv8_write(_desc(2, d), b.view.c, wide[0][:bound], wide[1][:bound], kv8.c)
+    assert b.bits() == dllm.DLLM_DEVERR_BAD_SHAPE
+    _assert_pools(kv8, want)
+
+
+def test_write_of_a_large_batch_ends_at_the_bound():
+    """More sequences than are searched in shared memory, the bound in the middle of one of the last."""
+    rows = [3] * 1100
+    bound = sum(rows) - 4
+    b = Batch([20] * 1100, [14] * 1100, rows, seed=2, cap_rows=bound)
+    kv8 = random_pools(b.num_pages, 1, 128, 3)
+    wide = [_rows(sum(rows) + 64, 1, 128, s) for s in (4, 5)]
+    for x in wide:
+        x[bound:] = 3000.0
+    want = _written(kv8, b.n, b.start, rows, b.table, cu(rows), range(1098), *wide)
+    dllm.dllm_kv8_write(_desc(1, 128), b.view.c, wide[0][:bound], wide[1][:bound], kv8.c)
+    assert b.bits() == dllm.DLLM_DEVERR_BAD_SHAPE
+    _assert_pools(kv8, want)
+
+
+def test_write_behind_a_plan_of_more_rows_than_its_bound():
+    """The plan flags the batch and leaves its sums whole; the write on the same stream serves what lies within."""
+    n, bound, d = [100, 200], 250, 64
+    t = dict(n=ints(n), start=ints([0, 0]), rows=ints(n), table=ints([[-1] * 4] * 2), cub=ints([0] * 3), cus=ints([0] * 3),
+             held=ints([0, 0]), held_out=ints([0, 0]), err=ints([0]))
+    view = dllm.BatchView(t["table"], t["n"], t["start"], t["rows"], t["cub"], t["cus"], bound, 300, 200, 200, t["err"])
+    ring = dllm.PageRing.full(8)
+    kv8 = random_pools(8, 2, d, 3)
+    wide = [_rows(320, 2, d, s) for s in (4, 5)]
+    for x in wide:
+        x[bound:] = 3000.0
+    table = [[0, 1], [2, 3, 4, 5]]
+    want = _written(kv8, n, [0, 0], n, table, [0, 100, 300], [0], *wide)
+    dllm.dllm_batch_plan(view.c, t["held"], t["held_out"], t["table"], t["cub"], t["cus"], ring.c)
+    dllm.dllm_kv8_write(_desc(2, d), view.c, wide[0][:bound], wide[1][:bound], kv8.c)
+    assert view.error_bits() == dllm.DLLM_DEVERR_BAD_SHAPE
+    assert t["table"].tolist() == [[0, 1, -1, -1], [2, 3, 4, 5]] and PAGE * 6 >= 200
+    _assert_pools(kv8, want)
