@@ -276,11 +276,12 @@ __device__ __forceinline__ Seq load_seq(const Kv8AttnArgs& a, int b) {
   q.rows = __ldg(bt.block_len + b);
   q.cub = __ldg(bt.cu_block + b);
   q.cus = __ldg(bt.cu_seq + b);
+  const int next = __ldg(bt.cu_block + b + 1);  // the block's rows are its own: a plan may have counted none of them
   q.tiles = q.nqt = q.npages = 0;
   q.bad = 0;
   if (q.rows == 0 || q.n == 0) return q;
   if (q.n < 0 || q.n > bt.max_seq_len || q.rows < 0 || q.rows > bt.max_block_len || q.s < 0 || q.rows > q.n - q.s ||
-      q.cub < 0 || q.rows > bt.total_block_rows - q.cub || (q.n + kPage - 1) / kPage > bt.max_pages ||
+      q.cub < 0 || next < q.cub || q.rows > min(next, bt.total_block_rows) - q.cub || (q.n + kPage - 1) / kPage > bt.max_pages ||
       (a.full_rows && (q.cus < 0 || q.n > bt.total_seq_rows - q.cus))) {
     q.bad = 1;
     return q;

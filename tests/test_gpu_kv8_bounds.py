@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from block_wise_kv_gb300 import dllm
-from kv8_util import PAGE, Batch, cu, ints, random_pools, write
+from kv8_util import PAGE, Batch, assert_attention, cu, ints, random_pools, write
 
 pytestmark = pytest.mark.gpu
 
@@ -107,3 +107,61 @@ def test_write_behind_a_plan_of_more_rows_than_its_bound():
     assert view.error_bits() == dllm.DLLM_DEVERR_BAD_SHAPE
     assert t["table"].tolist() == [[0, 1, -1, -1], [2, 3, 4, 5]] and PAGE * 6 >= 200
     _assert_pools(kv8, want)
+
+
+# ------------------------------------------------------------------ the attention
+def _attend(view, q, kv8, rows, layout, H, d):
+    o = torch.full((rows, H, d), 7.5, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((rows, H), 7.5, device="cuda")
+    ws = dllm.workspace(dllm.dllm_kv8_attention_workspace_size(_desc(H, d), view.c, kv8.c))
+    dllm.dllm_kv8_attention(_desc(H, d), view.c, q, kv8.c, o, lse, ws, layout)
+    return o, lse
+
+
+@pytest.mark.parametrize("layout", [dllm.DLLM_ROWS_BLOCK, dllm.DLLM_ROWS_FULL])
+@pytest.mark.parametrize("bad", [0, 1, 2])
+def test_attention_behind_a_plan_that_counted_a_sequence_as_none(bad, layout):
+    """A pages_held that cannot be makes the plan leave its sequence no rows: the attention leaves it out too, and so
+    the rows of the next sequence (or, behind the last, of none) are not written twice."""
+    n, start, rows, H, kv, d = [150, 100, 300], [100, 20, 290], [10, 30, 7], 4, 2, 64
+    b = Batch(n, start, rows, seed=3)
+    kv8 = random_pools(b.num_pages, kv, d, 4)
+    q = _rows(b.M, H, d, 5)
+    held = [(x + PAGE - 1) // PAGE for x in n]
+    held[bad] = -3
+    t = b.t
+    ring = dllm.PageRing(ints([0] * b.num_pages), ints([0, 0]), ints([0, 0]))
+    dllm.dllm_batch_plan(b.view.c, ints(held), ints([0] * 3), t["table"], t["cub"], t["cus"], ring.c)
+    assert b.bits() == dllm.DLLM_DEVERR_BAD_SHAPE
+    left = [r if i != bad else 0 for i, r in enumerate(rows)]
+    assert t["cub"].tolist() == cu(left) and t["rows"].tolist() == rows
+    b.error.zero_()
+    # the packed queries of those that are left
+    kept = [j for i, r in enumerate(rows) if i != bad for j in range(cu(rows)[i], cu(rows)[i] + r)]
+    qk = q.clone()
+    qk[:len(kept)] = q[kept]
+    full = layout == dllm.DLLM_ROWS_FULL
+    o, lse = _attend(b.view, qk, kv8, b.R if full else b.M, layout, H, d)
+    assert b.bits() == dllm.DLLM_DEVERR_BAD_SHAPE
+    cus = t["cus"].tolist()
+    at = [cus[i] + start[i] + j for i, r in enumerate(left) for j in range(r)] if full else list(range(len(kept)))
+    those = SimpleNamespace(n=n, rows=left, table=b.table, M=b.M)
+    assert_attention(those, qk, kv8, o[at], lse[at])
+    rest = torch.ones(o.shape[0], dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert (o[rest] == 7.5).all() and (lse[rest] == 7.5).all()
+
+
+@pytest.mark.parametrize("cub", [[0, 9, 20], [0, 10, 19], [10, 9, 20], [0, 10, -2147483648]])
+def test_attention_refuses_a_block_longer_than_its_rows(cub):
+    b = Batch([100, 100], [80, 90], [10, 10], seed=1)
+    kv8 = random_pools(b.num_pages, 2, 64, 3)
+    q = _rows(b.M, 4, 64, 1)
+    b.t["cub"].copy_(ints(cub))
+    o, _ = _attend(b.view, q, kv8, b.M, dllm.DLLM_ROWS_BLOCK, 4, 64)
+    assert b.bits() == dllm.DLLM_DEVERR_BAD_SHAPE
+    for i in (0, 1):
+        if cub[i + 1] - cub[i] < 10:
+            mine = range(cub[i], cub[i] + 10)
+            others = range(cub[1 - i], cub[1 - i] + 10) if cub[2 - i] - cub[1 - i] >= 10 else []
+            assert (o[[j for j in mine if j not in others and 0 <= j < 20]] == 7.5).all()
