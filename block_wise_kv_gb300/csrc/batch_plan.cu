@@ -9,8 +9,9 @@
 // rows and moved pages: no CTA waits for another and there is no second launch.
 // That works in place because what is read is never written: pages are taken
 // from the ring's head and given back behind its tail, table entries below
-// held_b are only read and those from held_b on only written, and a row in a
-// page that this call hands out takes the id from the ring, not from the table.
+// held_b are only read and those from held_b on only written (or, where there was no
+// page for them, looked at by the one thread that clears them), and a row in a page that
+// this call hands out takes the id from the ring, not from the table.
 //
 // Bound: a step's plan is latency (a chain of two dependent loads and one block
 // scan: 64 sequences 5.9 us); a plan of many prompts is the 12 bytes a row of the
@@ -166,12 +167,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) batch_plan_kernel(const 
     const int nb = min(kChunk, a.batch - b0);
 
     // the ids handed out, and those given back: CTA c has every n_cta-th stretch of kThreads of this chunk's
-    const long long take_end = min(total.take, static_cast<long long>(count));
-    for (long long i = carry.take + first; i < take_end; i += stride) {
+    for (long long i = carry.take + first; i < total.take; i += stride) {
       const int k = last_not_above(c.take0, nb, i);
-      if (c.now[k] <= c.held[k]) continue;  // asked for more than was free
-      const int id = ring_id(i);
-      a.table[static_cast<size_t>(b0 + k) * a.max_pages + c.held[k] + (i - c.take0[k])] = id;
+      int32_t* const entry = a.table + static_cast<size_t>(b0 + k) * a.max_pages + c.held[k] + (i - c.take0[k]);
+      if (c.now[k] > c.held[k])
+        *entry = ring_id(i);
+      else if (*entry >= 0 && *entry < a.num_pages)  // asked for more than was free: a page named here may be another's by now
+        *entry = -1;
     }
     for (long long i = carry.give + first; i < total.give; i += stride) {
       const int k = last_not_above(c.give0, nb, i);

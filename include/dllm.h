@@ -419,7 +419,11 @@ typedef struct dllm_page_ring {
  *   - need_b > pages_held[b]: block_table[b][pages_held[b] .. need_b) get ids
  *     from the ring's head on, sequences in order.  A sequence gets its pages
  *     iff the pages asked for up to and including it were free when the call
- *     began; otherwise it keeps what it holds, and DLLM_DEVERR_NO_PAGES is set.
+ *     began; otherwise it keeps what it holds, DLLM_DEVERR_NO_PAGES is set, and
+ *     those of its entries in [pages_held[b], need_b) that name a page become -1
+ *     (the page may be another sequence's by now): the calls that follow set
+ *     DLLM_DEVERR_BAD_PAGE for such a sequence, write none of its positions
+ *     there, and leave its own outputs, and no others, undefined.
  *   - need_b < pages_held[b]: the ids in block_table[b][need_b .. pages_held[b])
  *     go to the ring's tail, sequences in order (free for the next call); the
  *     entries stay as they are.

@@ -165,3 +165,71 @@ def test_attention_refuses_a_block_longer_than_its_rows(cub):
             mine = range(cub[i], cub[i] + 10)
             others = range(cub[1 - i], cub[1 - i] + 10) if cub[2 - i] - cub[1 - i] >= 10 else []
             assert (o[[j for j in mine if j not in others and 0 <= j < 20]] == 7.5).all()
+
+
+# ------------------------------------------------------------------ a plan that runs short
+def test_a_plan_that_runs_short_leaves_no_page_of_another_sequence():
+    """The place of a request that has ended is taken by a longer one when no page is free.  Its entries still name the
+    pages that went back to the ring and that others hold by now: neither the write nor the attention may follow them."""
+    H, kv, d, P = 4, 2, 64, 9
+    t = dict(n=ints([250, 60, 190]), start=ints([0, 0, 0]), rows=ints([250, 60, 190]), table=ints([[-1] * 4] * 3),
+             cub=ints([0] * 4), cus=ints([0] * 4), err=ints([0]))
+    held, held_out, ring = ints([0] * 3), ints([0] * 3), dllm.PageRing.full(P)
+    view = dllm.BatchView(t["table"], t["n"], t["start"], t["rows"], t["cub"], t["cus"], 500, 600, 256, 256, t["err"])
+    kv8 = random_pools(P, kv, d, 3)
+
+    def step(n, start, rows, seed):
+        nonlocal held, held_out, ring
+        for key, val in (("n", n), ("start", start), ("rows", rows)):
+            t[key].copy_(ints(val))
+        before = [x.clone() for x in (kv8.k.view(torch.uint8), kv8.v.view(torch.uint8), kv8.k_scale, kv8.v_scale)]
+        k, v, q = _rows(500, kv, d, seed), _rows(500, kv, d, seed + 1), _rows(500, H, d, seed + 2)
+        dllm.dllm_batch_plan(view.c, held, held_out, t["table"], t["cub"], t["cus"], ring.c)
+        dllm.dllm_kv8_write(_desc(H, d), view.c, k, v, kv8.c)
+        o, lse = _attend(view, q, kv8, 500, dllm.DLLM_ROWS_BLOCK, H, d)
+        torch.cuda.synchronize()
+        held, held_out, ring = held_out, held, ring.swapped()
+        return before, k, v, q, o, lse
+
+    step([250, 60, 190], [0, 0, 0], [250, 60, 190], 10)  # four pages, one, three; one left
+    assert view.error_bits() == 0
+    assert t["table"].tolist() == [[0, 1, 2, 3], [4, -1, -1, -1], [5, 6, 7, -1]]
+    step([10, 60, 190], [0, 0, 0], [10, 0, 0], 20)       # the first ends, a short one takes its place: three pages back
+    step([10, 256, 190], [10, 60, 190], [0, 196, 0], 30)  # the second grows into them
+    assert view.error_bits() == 0
+    assert t["table"].tolist() == [[0, 1, 2, 3], [4, 8, 1, 2], [5, 6, 7, -1]]
+    # the first wants three pages more and one is free; its entries 1 and 2 name pages of the second
+    n, start, rows = [200, 256, 190], [10, 250, 180], [190, 6, 10]
+    before, k, v, q, o, lse = step(n, start, rows, 40)
+    assert view.error_bits() & dllm.DLLM_DEVERR_NO_PAGES
+    assert t["table"].tolist() == [[0, -1, -1, -1], [4, 8, 1, 2], [5, 6, 7, -1]]
+    assert held.tolist() == [1, 4, 3]
+    table = t["table"].tolist()
+    old = dllm.Kv8Cache.of(before[0].view(torch.float8_e4m3fn), before[1].view(torch.float8_e4m3fn), *before[2:])
+    want = _written(old, n, start, rows, table, cu(rows), [1, 2], k, v)
+    others = [4, 8, 1, 2, 5, 6, 7]
+    for (codes, scale), (vals, sc) in zip(((kv8.k, kv8.k_scale), (kv8.v, kv8.v_scale)), want):
+        assert torch.equal(scale.double().cpu()[others], sc[others]) and torch.equal(_decoded(codes)[others], vals[others])
+    those = SimpleNamespace(n=n[1:], rows=rows[1:], table=table[1:], M=16)
+    assert_attention(those, q[190:206], kv8, o[190:206], lse[190:206])
+    assert (o[206:] == 7.5).all() and (lse[206:] == 7.5).all()
+
+
+def test_a_short_plan_called_again_gives_the_same_and_pages_that_come_later_are_taken():
+    P = 7
+    t = dict(n=ints([100, 256, 64]), rows=ints([1, 1, 1]), start=ints([0, 0, 0]), table=ints([[6, 0, 5, 2], [0, 1, 4, 99], [3, -5, 6, 0]]),
+             cub=ints([0] * 4), cus=ints([0] * 4), err=ints([0]))
+    ring = dllm.PageRing(ints([5, 2, 0, 0, 0, 0, 3]), ints([6, 3]), ints([0, 0]))  # 3, 5 and 2 are free
+    view = dllm.BatchView(t["table"], t["n"], t["start"], t["rows"], t["cub"], t["cus"], 3, 500, 1, 256, t["err"])
+    held, out = ints([1, 0, 0]), ints([0] * 3)
+    for _ in range(2):
+        dllm.dllm_batch_plan(view.c, held, out, t["table"], t["cub"], t["cus"], ring.c)
+        # the first has its page; the second is four short, and the third then too; what names no page stays
+        assert view.error_bits() == dllm.DLLM_DEVERR_NO_PAGES
+        assert t["table"].tolist() == [[6, 3, 5, 2], [-1, -1, -1, 99], [-1, -5, 6, 0]]
+        assert out.tolist() == [2, 0, 0] and ring.state_out.tolist() == [0, 2]
+    t["n"].copy_(ints([100, 0, 64]))
+    t["rows"].copy_(ints([1, 0, 1]))
+    ring = ring.swapped()
+    dllm.dllm_batch_plan(view.c, out, held, t["table"], t["cub"], t["cus"], ring.c)
+    assert held.tolist() == [2, 0, 1] and t["table"].tolist()[2] == [5, -5, 6, 0]
