@@ -6,13 +6,17 @@
 // 128 keys fill the tensor core's M and the few rows are its N:
 //
 //   S^T[key][row] = K8 (Q_hi + Q_lo)^T         e4m3 x e4m3, two products into one accumulator
-//   P^T[key][row] = 2^(x),  x = f_key S - R_row  (f_key = key scale x q scale x softmax scale x log2 e)
+//   P^T[key][row] = 2^(x),  x = f_key g_row S - R_row  (key scale; q scale x softmax scale x log2 e)
 //   O^T[col][row] += V8^T (P_hi + P_mid + P_lo)^T  e4m3 x e5m2
 //
 // The pages are used as they lie: no key or value is ever converted.  What makes that
-// exact enough is the other operand.  A row's q is scaled by a power of two so that
-// the unit's largest is in (224, 448] and split into two e4m3 parts: 4 + 4 bits hold
-// bf16's 8 exactly down to 2^-11 of the largest, and below that to 2^-19 of it.
+// exact enough is the other operand.  A row's q is scaled by a power of two of its own so
+// that its largest is in (224, 448], and split into two e4m3 parts.  4 + 4 bits hold
+// bf16's 8 exactly where the scaled value is 2^-2 or more (at least down to 2^-9.8 of the
+// row's largest); smaller ones are off by up to 2^-10, half of e4m3's smallest step (at
+// most 2^-17.8 of the row's largest).  With one scale for a whole unit a row lost what it
+// was smaller than its neighbours by, and was all zeros at 2^-19 of them; a row's own costs
+// a product for each pair of scores (32 ragged sequences 136 us for 131).
 // A weight is rounded to fp16 (11 bits) and split into three e5m2 parts, which is
 // exact (3 bits each, rounded to nearest) but for an absolute 2^-17, half of the
 // smallest e5m2 step, where a row's largest is 2^10 or more: a softmax with one large
@@ -20,8 +24,8 @@
 // scale of a key multiplies its weight before the split; the sum l takes the weight
 // without it.
 //
-// The thread that holds a key's scores has its scales as two scalars; a row's
-// reference R is the same for all 128 keys.  R is set from a unit's first tile (so
+// The thread that holds a key's scores has its scales as two scalars; a row's g and
+// reference R are the same for all 128 keys.  R is set from a unit's first tile (so
 // that the largest weight x value scale is 2^10) and raised only when one passes 2^15:
 // a vote per tile, and otherwise no reduction over keys at all until the unit's end,
 // where the 128 partial sums of each row are added.
@@ -371,9 +375,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
   // of each row: -R; what the sums so far are multiplied by where R is raised; the sum l and 1 / l
   // (two of what the end of a unit still reads when the next has begun)
   __shared__ __align__(16) float nref_sh[2][NQ], alpha_sh[NQ], l_sh[NQ], inv_sh[NQ];
+  __shared__ __align__(16) float fq_sh[NQ];  // a row's q scale x softmax scale x log2 e
   __shared__ float red_sh[4][NQ];
   __shared__ long long row_sh[2][NQ];  // row and head of the output, as one index
-  __shared__ float amax_sh[4 * C::kGroups];
   __shared__ long long seg_sh[kScan + 1];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x;
@@ -704,7 +708,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
       }
     };
     int2 record = make_int2(0, 0);
-    float f_q = 0.f;
 
     // The rows of q of part u: asked for while the last tile of the part before is still to be done (in narrow units, where
     // there are registers for it).
@@ -733,13 +736,19 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
       if (!kAhead || u == 0) ask_q(u);
       const bool have = !barrier_any<C::kSoft>(1, dead || part.t1 == 0);  // (the same for all, whoever gave up)
       if (have) {
+        // the row's largest: its kPer lanes are neighbours
+        auto row_max = [](uint32_t v) {
+#pragma unroll
+          for (int o = 1; o < kPer; o <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+          return v;
+        };
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
           m = max_u16x2(m, max_u16x2(max_u16x2(qv[i].x & 0x7fff7fffu, qv[i].y & 0x7fff7fffu),
                                      max_u16x2(qv[i].z & 0x7fff7fffu, qv[i].w & 0x7fff7fffu)));
-        m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-        if (m >= 0x7f80u) {  // values that are not finite take no part, and make their row, and no other, not a number
+        m = row_max(max(m & 0xffffu, m >> 16));
+        if (__any_sync(0xffffffffu, m >= 0x7f80u)) {  // values that are not finite take no part, and make their row not a number
           m = 0;
 #pragma unroll
           for (int i = 0; i < kVec; ++i) {
@@ -751,26 +760,19 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
               w[k] |= (lo < 0x7f80u ? 0u : 0x7fu) | (hi < 0x7f80u ? 0u : 0x7f0000u);
             }
           }
-          m = __reduce_max_sync(0xffffffffu, m);
+          m = row_max(m);
         }
-        if (lane == 0) amax_sh[warp] = __uint_as_float(m << 16);
         if (tid < NQ) {
           const int r = part.r0 + tid, i = r / G;
           row_sh[par][tid] = static_cast<long long>(a.full_rows ? part.cus + part.s + i : part.cub + i) * a.n_heads + part.h * G +
                              (r - i * G);
           nref_sh[par][tid] = 0.f;
         }
-        soft_sync();
-        // q in two e4m3 parts
-        float amax = amax_sh[0];
-#pragma unroll
-        for (int i = 1; i < 4 * C::kGroups; ++i) amax = fmaxf(amax, amax_sh[i]);
-        // 2^e with amax 2^-e in (224, 448]; 448 = 1.75 2^8
-        const uint32_t bits = __float_as_uint(amax);
-        int e = static_cast<int>(bits >> 23) - 127 - ((bits & 0x7fffffu) <= 0x600000u ? 8 : 7);
+        // q in two e4m3 parts: 2^e with the row's largest x 2^-e in (224, 448]; 448 = 1.75 2^8
+        int e = static_cast<int>(m >> 7) - 127 - ((m & 127u) <= 96u ? 8 : 7);
         e = max(e, -118);
         const float down = __int_as_float((127 - e) << 23);
-        f_q = a.scale_log2 * __int_as_float((127 + e) << 23);
+        if (tid % kPer == 0) fq_sh[q_row] = a.scale_log2 * __int_as_float((127 + e) << 23);
         const uint64_t down2 = pack2(down, down);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
@@ -799,6 +801,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
         }
         fence_async_smem();
         mbar_arrive(&q_ready);
+        if (u == 0) soft_sync();  // the rows' values are there (later ones behind the barriers of the end below)
       }
       if (u > 0) {
         // ---- the end of the part before: l over all keys, then O / l, or (O, R, l) to the workspace
@@ -866,7 +869,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
         const int valid = n - t * kTile;  // keys of this tile that there are
         wait(&scale_bar[nt % kScaleSlots], nt / kScaleSlots);
         const float sv = key < valid ? scales[nt % kScaleSlots][1][key / kKv8Group] : 0.f;
-        const float f = key < valid ? scales[nt % kScaleSlots][0][key / kKv8Group] * f_q : 0.f;
+        const float f = key < valid ? scales[nt % kScaleSlots][0][key / kKv8Group] : 0.f;
         wait(&s_full, nt);
         tc_fence_after();
         uint64_t x[kCols / 2];
@@ -875,10 +878,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
           float s[kCols];
           tmem_load(tm_s, s);
 #pragma unroll
-          for (int c = 0; c < kCols; c += 4) {  // x = f S - R
+          for (int c = 0; c < kCols; c += 4) {  // x = f g S - R
             const ulonglong2 r = *reinterpret_cast<const ulonglong2*>(&nref_sh[par][col0 + c]);
-            x[c / 2] = fma2(pack2(s[c], s[c + 1]), f2, r.x);
-            x[c / 2 + 1] = fma2(pack2(s[c + 2], s[c + 3]), f2, r.y);
+            const ulonglong2 g = *reinterpret_cast<const ulonglong2*>(&fq_sh[col0 + c]);
+            x[c / 2] = fma2(pack2(s[c], s[c + 1]), mul2(f2, g.x), r.x);
+            x[c / 2 + 1] = fma2(pack2(s[c + 2], s[c + 3]), mul2(f2, g.y), r.y);
           }
           if (key >= valid) {
 #pragma unroll

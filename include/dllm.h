@@ -484,7 +484,14 @@ dllm_status dllm_kv8_write_pool(const dllm_layer_desc* desc, const dllm_batch* b
  *   O = sum_j softmax_j(scale * q_i . k_j) v_j,  L = log sum_j exp(scale * q_i . k_j)
  * with k_j, v_j the values the codes stand for.  Single-token decoding is
  * block_len = 1.  What lies at or behind N_b in a sequence's last page is not
- * used (it may hold anything).  The split of the keys over the GPU depends on
+ * used (it may hold anything).
+ *   Precision: scores, sums and accumulators are fp32.  A row's q is exact in its
+ * larger values and off by at most 2^-17 of its own largest in the others.  A
+ * weight times the value scale of its key is rounded to 11 bits and to an absolute
+ * 2^-27 of the row's largest such product; o is rounded to bf16 once.  A row whose
+ * q holds a value that is not finite, or a score beyond 2^25 in magnitude, may come
+ * out as not a number, it alone; one with a not-a-number key or value does.
+ *   The split of the keys over the GPU depends on
  * the batch alone, and partial results are joined in a fixed order: the same
  * call gives the same bits.
  *   q: device bf16, row j of the packed block rows at j * q_row_stride
