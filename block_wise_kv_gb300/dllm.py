@@ -46,7 +46,7 @@ DLLM_ROWS_BLOCK = 0
 DLLM_ROWS_FULL = 1
 
 PAGE = 64
-_BF16, _INT32 = torch.bfloat16, torch.int32
+_BF16, _FP32, _INT32 = torch.bfloat16, torch.float32, torch.int32
 KV8_GROUP = 16  # token positions that share a scale of the 8-bit cache
 
 # Every symbol include/dllm.h declares.
@@ -285,38 +285,63 @@ def dllm_block_ffn(desc, batch, d_ff, o_full, x_block, w_o, ffn_gain, w_gate_up,
 
 
 # The calls of the 8-bit cache are made for small batches too, where the host's part is most of their time: they take
-# tensors only and do no more than their arguments need.
+# tensors only, and check type, layout, length and device once each, in as few steps as that takes.
+def _on(device: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+
+
 def dllm_batch_plan(batch, pages_held, pages_held_out, block_table, cu_block, cu_seq, ring, row_slot=None,
                     row_seq=None, row_pos=None, stream=None):
-    for t in (pages_held, pages_held_out, block_table, cu_block, cu_seq, row_slot, row_seq, row_pos):
-        if t is not None and t.dtype is not _INT32:
-            raise DllmError("dllm_batch_plan", DLLM_ERR_INVALID_ARGUMENT)
+    """pages_held, pages_held_out: int32 [batch]; block_table [batch][max_pages_per_seq]; cu_block, cu_seq
+    [batch + 1]; the row maps [total_block_rows], each may be None.  All contiguous, longer ones are fine."""
+    i32, dev, n, rows = _INT32, pages_held.get_device(), 4 * batch.batch, 4 * batch.total_block_rows
+    table, cub, cus = block_table.data_ptr(), cu_block.data_ptr(), cu_seq.data_ptr()
+    # (written out: a helper for each tensor takes a microsecond more.  What the batch names itself is what it says.)
+    if (pages_held.dtype is not i32 or pages_held.nbytes < n or not pages_held.is_contiguous()
+            or pages_held_out.dtype is not i32 or pages_held_out.nbytes < n or not pages_held_out.is_contiguous()
+            or pages_held_out.get_device() != dev
+            or table != batch.block_table and (
+                block_table.dtype is not i32 or block_table.nbytes < n * batch.max_pages_per_seq
+                or not block_table.is_contiguous() or block_table.get_device() != dev)
+            or cub != batch.cu_block and (cu_block.dtype is not i32 or cu_block.nbytes <= n
+                                          or not cu_block.is_contiguous() or cu_block.get_device() != dev)
+            or cus != batch.cu_seq and (cu_seq.dtype is not i32 or cu_seq.nbytes <= n
+                                        or not cu_seq.is_contiguous() or cu_seq.get_device() != dev)
+            or row_slot is not None and (row_slot.dtype is not i32 or row_slot.nbytes < rows
+                                         or not row_slot.is_contiguous() or row_slot.get_device() != dev)
+            or row_seq is not None and (row_seq.dtype is not i32 or row_seq.nbytes < rows
+                                        or not row_seq.is_contiguous() or row_seq.get_device() != dev)
+            or row_pos is not None and (row_pos.dtype is not i32 or row_pos.nbytes < rows
+                                        or not row_pos.is_contiguous() or row_pos.get_device() != dev)
+            or dev != torch._C._cuda_getDevice()):
+        raise DllmError("dllm_batch_plan", DLLM_ERR_INVALID_ARGUMENT)
     status = (_lib or load()).dllm_batch_plan(
-        ctypes.byref(batch), pages_held.data_ptr(), pages_held_out.data_ptr(), block_table.data_ptr(),
-        cu_block.data_ptr(), cu_seq.data_ptr(), ctypes.byref(ring), None if row_slot is None else row_slot.data_ptr(),
-        None if row_seq is None else row_seq.data_ptr(), None if row_pos is None else row_pos.data_ptr(),
-        _stream(stream))
+        batch, pages_held.data_ptr(), pages_held_out.data_ptr(), table, cub, cus, ring,
+        None if row_slot is None else row_slot.data_ptr(), None if row_seq is None else row_seq.data_ptr(),
+        None if row_pos is None else row_pos.data_ptr(), _on(dev, stream))
     if status:
         raise DllmError("dllm_batch_plan", status)
 
 
 def dllm_kv8_write(desc, batch, k_rows: torch.Tensor, v_rows: torch.Tensor, kv8, stream=None):
-    """k_rows, v_rows: bf16 [M][n_kv_heads][head_dim], the last dimension
+    """k_rows, v_rows: bf16 [M][n_kv_heads][head_dim], M >= total_block_rows, the last dimension
     contiguous (views of a wider projection output are fine)."""
     ks, vs, shape = k_rows.stride(), v_rows.stride(), k_rows.shape
     if (len(ks) != 3 or shape != v_rows.shape or ks[2] != 1 or vs[2] != 1 or shape[1] != kv8.n_kv_heads
-            or shape[2] != desc.head_dim or k_rows.dtype is not _BF16 or v_rows.dtype is not _BF16):
+            or shape[2] != desc.head_dim or shape[0] < batch.total_block_rows or k_rows.dtype is not _BF16
+            or v_rows.dtype is not _BF16):
+        raise DllmError("dllm_kv8_write", DLLM_ERR_INVALID_ARGUMENT)
+    dev = k_rows.get_device()
+    if v_rows.get_device() != dev or dev != torch._C._cuda_getDevice():
         raise DllmError("dllm_kv8_write", DLLM_ERR_INVALID_ARGUMENT)
     status = (_lib or load()).dllm_kv8_write(
-        ctypes.byref(desc), ctypes.byref(batch), k_rows.data_ptr(), ks[0], ks[1], v_rows.data_ptr(), vs[0], vs[1],
-        ctypes.byref(kv8), _stream(stream))
+        desc, batch, k_rows.data_ptr(), ks[0], ks[1], v_rows.data_ptr(), vs[0], vs[1], kv8, _on(dev, stream))
     if status:
         raise DllmError("dllm_kv8_write", status)
 
 
 def dllm_kv8_write_pool(desc, batch, cache, kv8, stream=None):
-    status = (_lib or load()).dllm_kv8_write_pool(ctypes.byref(desc), ctypes.byref(batch), ctypes.byref(cache),
-                                                  ctypes.byref(kv8), _stream(stream))
+    status = (_lib or load()).dllm_kv8_write_pool(desc, batch, cache, kv8, _stream(stream))
     if status:
         raise DllmError("dllm_kv8_write_pool", status)
 
@@ -329,15 +354,24 @@ def dllm_kv8_attention_workspace_size(desc, batch, kv8) -> int:
 
 
 def dllm_kv8_attention(desc, batch, q: torch.Tensor, kv8, o, lse, ws, o_rows: int = DLLM_ROWS_BLOCK, stream=None):
-    """q: bf16 [M][n_heads][head_dim], rows contiguous, any row stride.  lse
-    may be None; ws: a uint8 tensor of dllm_kv8_attention_workspace_size bytes."""
-    qs, shape = q.stride(), q.shape
-    if (len(qs) != 3 or qs[2] != 1 or qs[1] != shape[2] or shape[1] != desc.n_heads or shape[2] != desc.head_dim
-            or q.dtype is not _BF16 or o.dtype is not _BF16):
+    """q: bf16 [M][n_heads][head_dim], M >= total_block_rows, rows contiguous, any row stride.  o: contiguous bf16 of
+    as many rows (DLLM_ROWS_FULL: of total_seq_rows rows), lse: contiguous float32 of as many rows of n_heads, or
+    None; ws: a uint8 tensor of dllm_kv8_attention_workspace_size bytes."""
+    qs, shape, n_heads, d, m = q.stride(), q.shape, desc.n_heads, desc.head_dim, batch.total_block_rows
+    if (len(qs) != 3 or qs[2] != 1 or shape[1] != n_heads or shape[2] != d or (qs[1] != d and n_heads > 1)
+            or shape[0] < m or q.dtype is not _BF16):
+        raise DllmError("dllm_kv8_attention", DLLM_ERR_INVALID_ARGUMENT)
+    dev = q.get_device()
+    values = (batch.total_seq_rows if o_rows == DLLM_ROWS_FULL else m) * n_heads
+    if (o.dtype is not _BF16 or o.nbytes < 2 * values * d or not o.is_contiguous() or o.get_device() != dev
+            or not ws.is_contiguous() or ws.get_device() != dev
+            or lse is not None and (lse.dtype is not _FP32 or lse.nbytes < 4 * values or not lse.is_contiguous()
+                                    or lse.get_device() != dev)
+            or dev != torch._C._cuda_getDevice()):
         raise DllmError("dllm_kv8_attention", DLLM_ERR_INVALID_ARGUMENT)
     status = (_lib or load()).dllm_kv8_attention(
-        ctypes.byref(desc), ctypes.byref(batch), q.data_ptr(), qs[0], ctypes.byref(kv8), o.data_ptr(), o_rows,
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.nbytes, _stream(stream))
+        desc, batch, q.data_ptr(), qs[0], kv8, o.data_ptr(), o_rows, None if lse is None else lse.data_ptr(),
+        ws.data_ptr(), ws.nbytes, _on(dev, stream))
     if status:
         raise DllmError("dllm_kv8_attention", status)
 
@@ -413,6 +447,14 @@ class BatchView:
         for t in self.tensors:
             if t is not None and (t.dtype != torch.int32 or not t.is_contiguous()):
                 raise ValueError("batch metadata are contiguous int32 tensors")
+            if t is not None and t.device != seq_len.device:
+                raise ValueError("batch metadata are tensors of one device")
+        n = seq_len.numel()
+        if (seq_len.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] < n or block_start.numel() < n
+                or block_len.numel() < n or cu_block.numel() <= n or cu_seq.numel() <= n
+                or error is not None and error.numel() < 1):
+            raise ValueError("batch metadata are seq_len, block_start, block_len [batch], block_table [batch][pages], "
+                             "cu_block and cu_seq [batch + 1], and one error word")
         self.c = BatchC(seq_len.shape[0], block_table.shape[1], total_block_rows, total_seq_rows, max_block_len,
                         max_seq_len, _ptr(block_table), _ptr(seq_len), _ptr(block_start), _ptr(block_len),
                         _ptr(cu_block), _ptr(cu_seq), _ptr(error))
@@ -429,6 +471,10 @@ class PageRing:
         for t in (pages, state, state_out):
             if t.dtype != torch.int32 or not t.is_contiguous():
                 raise ValueError("a page ring's tensors are contiguous int32")
+            if t.device != pages.device:
+                raise ValueError("a page ring's tensors are of one device")
+        if pages.dim() != 1 or state.numel() < 2 or state_out.numel() < 2:
+            raise ValueError("a page ring has pages [P], state [2] and state_out [2]")
         self.pages, self.state, self.state_out = pages, state, state_out
         self.c = PageRingC(_ptr(pages), _ptr(state), _ptr(state_out), pages.shape[0])
 
@@ -458,6 +504,8 @@ class Kv8Cache:
         for t, dtype in zip(tensors, (torch.float8_e4m3fn,) * 2 + (torch.float32,) * 2):
             if t.dtype != dtype or not t.is_contiguous():
                 raise ValueError("the pools are contiguous float8_e4m3fn tensors, the scales contiguous float32")
+            if t.device != self.k.device:
+                raise ValueError("the pools and their scales are of one device")
         shape = (num_pages, n_kv_heads, PAGE, head_dim)
         scales = (num_pages, n_kv_heads, PAGE // KV8_GROUP)
         if any(tuple(t.shape) != s for t, s in zip(tensors, (shape, shape, scales, scales))):
