@@ -105,7 +105,7 @@ struct Cfg {
   static constexpr bool kPlanes = NQ == 64;
   static constexpr int kPRow = NQ == 32 ? 128 : 64;
   static constexpr int kPBytes = kTile * kPRow * (kPlanes ? 3 : 1);
-  static constexpr int kStatic = NQ == 64 ? 6144 : NQ == 32 ? 4608 : 3584;  // static shared memory, at most
+  static constexpr int kStatic = NQ == 64 ? 6400 : NQ == 32 ? 4608 : 3584;  // static shared memory, at most
   static constexpr int kBudget = 227 * 1024 / kCtas - 2048 - kStatic;  // 1 KB to align, 1 KB of the system's a CTA
   static constexpr int kSlots0 = (kBudget - kQBytes - kPBytes) / kSlotBytes;
   static constexpr int kSlots = kSlots0 > 10 ? 10 : kSlots0;
