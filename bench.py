@@ -174,7 +174,7 @@ TRAFFIC = {
     # (workload, kernel): (DRAM bytes per launch, sources hash); profiles/attn_stream_stack.md,
     # profiles/qkv_wide_stack.md (the DRAM-only capture listed there)
     ("stack", "attention"): (969_189_632, "47432f11b3637cc5"),
-    ("stack", "qkv"): (135_171_584, "042ebfe49b5f9368"),
+    ("stack", "qkv"): (131_329_792, "71aba221426de0ff"),
 }
 
 
