@@ -14,7 +14,7 @@
 // this call hands out takes the id from the ring, not from the table.
 //
 // Bound: a step's plan is latency (a chain of two dependent loads and one block
-// scan: 64 sequences 5.9 us); a plan of many prompts is the 12 bytes a row of the
+// scan: 64 sequences 5.7 us); a plan of many prompts is the 12 bytes a row of the
 // three row maps behind that (512 prompts of 2.1 M rows 12.7 us; 392 with one row to a
 // thread, which searched the sums for each).
 #include <algorithm>
@@ -254,8 +254,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) batch_plan_kernel(const 
 
 cudaError_t launch_batch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream) {
   // One CTA for each 4096 rows or pages that may have to be written, at most two an SM: each CTA repeats
-  // the scan, so more of them only pay where there is enough to write (512 prompts of 2.1 M rows: 12.8 us, 1694 with one
-  // CTA; 64 sequences of 32 rows take one CTA, 5.9 us, as with one for each 512).
+  // the scan, so more of them only pay where there is enough to write (512 prompts of 2.1 M rows: 12.7 us, 1692 with one
+  // CTA; 64 sequences of 32 rows take one CTA, 5.7 us, as with one for each 512).
   const long long pages = static_cast<long long>(a.batch) * a.max_pages;
   const long long most = std::max<long long>(a.cap_rows, std::min<long long>(pages, a.num_pages));
   const int grid = static_cast<int>(std::max(1ll, std::min(static_cast<long long>(kCtasPerSm * num_sms), most / 4096)));

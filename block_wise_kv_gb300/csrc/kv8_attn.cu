@@ -52,9 +52,13 @@
 // join).  Wider units by the chain of a tile (scores, vote, weights, products), 1.9 us a
 // tile and CTA for 64 rows, 1.4 for 32, with 16 softmax warps an SM (what the registers
 // hold) and the issue slots half busy: 32 ragged sequences of up to 4608 keys, blocks of
-// 16 to 64: 131 us, 4.5 TB/s; eight sequences with 128 rows to a key head: 42 us.  16
-// sequences of 1536 with blocks of 32: 44 us, 4.8 TB/s.  One sequence of 768: 12 us, of
-// which the two launches take 3.4, the line 1.1, the join 3.7.
+// 16 to 64: 136 us, 4.3 TB/s; eight sequences with 128 rows to a key head: 43 us.  16
+// sequences of 1536 with blocks of 32: 44 us, 4.7 TB/s.  One sequence of 768: 12 us, of
+// which the two launches take 3.4, the line 1.1, the join 3.7.  Half the columns are half
+// the bytes of a tile and the same chain: the 16 sequences as 64 heads of 64 take 70 us.
+// All of these are with scores whose spread is about 1.3 (in natural units), where R is
+// hardly ever raised.  With queries 2, 4 and 8 times as large the 16 sequences take 48, 54
+// and 56 us, the ragged ones 168, 204 and 218.
 #include <algorithm>
 
 #include "attn_common.cuh"
@@ -68,25 +72,26 @@ constexpr int kScaleSlots = 8;       // tiles whose scales are in shared memory
 constexpr int kMaxCtas = 1024;       // of a launch (records of the workspace)
 constexpr size_t kRecordBytes = kMaxCtas * sizeof(int2);
 // Sequences of up to this many tiles are not cut: three more tiles in a row take about what the second launch does
-// (320 tokens of 4 heads: 9.5 us cut and joined, 9.2 whole, and 1.7 us less on the host).
+// (320 tokens of 4 heads: 9.4 us cut and joined, 8.5 whole, and 2 us less on the host).
 constexpr int kWholeTiles = 4;
 // Up to this many sequences are summed up by the producer warp alone, four a lane; beyond, by as many threads through
-// shared memory, behind a barrier of the CTA (with that way for 16 sequences: 46.0 us for 44.9, one sequence 12.8 for 11.9).
+// shared memory, behind a barrier of the CTA (with that way for 16 sequences: 45.5 us for 44.2, one sequence 12.7 for 11.9).
 constexpr int kScan = 128;
 constexpr int kParts = 16;           // parts of units in shared memory: the producer is fewer than 8 tiles ahead
 constexpr float kTop = 10.f;    // log2 of a row's largest weight x value scale when R is set
 constexpr float kLimitLog2 = 15.f;
 constexpr float kLimit = 32768.f;  // what a weight x value scale may reach before R is raised
 
-// What a unit's beginning and end cost, in tiles (see the split above): 32 ragged sequences in units of 64 take 139 us
-// with 2, 131 with 3, 132 with 4; 16 of 1536 in units of 32 44.3 with 1, 44.0 with 2; 64 of single tokens in units of 16
-// 151 with 1 or 2, 158 with 3.
+// What a unit's beginning and end cost, in tiles (see the split above): 32 ragged sequences in units of 64 take 145 us
+// with 2, 136 with 3, 138 with 4; 16 of 1536 in units of 32 44.9 with 1, 44.3 with 2, 44.7 with 3; 64 of single tokens in
+// units of 16 151 with 1 or 2, 153 with 3.
 __host__ __device__ constexpr int unit_tiles(int nq) { return nq == 64 ? 3 : 2; }
 
-// CTAs an SM (of a unit's width): with 16 rows, memory's latency is what more of them cover, 96 registers a thread still
-// do, and three slots of the ring hold a tile and the next key tile (64 sequences of up to 16384 keys: 156.7 us with two,
-// 151 with three, 199 with four, whose rings of two slots run dry; two of 131072 keys: 84.8, 83, 84.5).  Wider units' softmax
-// needs the registers: 32 rows took 45.0 us with two CTAs of 16 rows a thread, 49.0 with three of 32 rows a thread.
+// CTAs an SM (of a unit's width): with 16 rows, memory's latency is what more of them cover, 96 registers a thread nearly
+// do (40 bytes go to the stack and back), and three slots of the ring hold a tile and the next key tile (64 sequences of up
+// to 16384 keys: 157.7 us with two, 151.4 with three, 150.5 with four, whose rings have two slots; two of 131072 keys: 84.9,
+// 82.8, 84.5).  Wider units' softmax needs the registers: 32 rows took 45.0 us with two CTAs of 16 rows a thread, 49.0 with
+// three of 32 rows a thread.
 constexpr int ctas_per_sm(int nq) { return nq == 16 ? 3 : 2; }
 
 // NQ rows to a unit, handled by NQ / kCols groups of four softmax warps (a thread: one key, kCols rows).
@@ -632,8 +637,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::kThreads, Cfg<D, NQ>::kCtas)
   } else if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
     // All of the warp goes through the loop, and its conditions are the same for every lane by votes: descriptors and
-    // counters can stay in the warp's uniform registers, which is where a product takes them from.  (One lane alone: 16
-    // sequences of 1536 keys 44.9 us for 44.5, 128 rows to a key head 43.4 for 43.0.)
+    // counters can stay in the warp's uniform registers, which is where a product takes them from.  (One lane alone: 0.4 us
+    // more for 16 sequences of 1536 keys and for 128 rows to a key head.)
     constexpr uint32_t kIdescS = idesc_f8(kTile, NQ, false, false);
     constexpr uint32_t kIdescO = idesc_f8(kTile, 3 * NQ, true, true);
     const uint32_t tm_o = tmem + NQ;
@@ -1113,10 +1118,10 @@ cudaError_t launch(const Kv8AttnArgs& a, int num_sms, cudaStream_t stream) {
 
 // Rows that share a key head, at most: the smallest of 16, 32 and 64 that holds them, and units of 64 beyond.  A tile
 // costs the softmax its NQ columns whether they are rows or not: 16 sequences with blocks of 32 take 44 us in units of
-// 32, 57 in units of 64, one sequence 11.9 and 14.4.  Four rows to a key head are bound by memory either way, and 16
-// leave it a little more of the SM: two contexts of 131072 keys 82.5 us in units of 16, 83.7 in units of 32 (64 single
-// tokens 151 and 154).  128 rows in two units of 64 read the keys twice, 42 us where the bytes take 10; one unit of
-// 128 would have the same softmax to do and fill the TMEM of an SM alone.
+// 32, 58 in units of 64, one sequence 11.9 and 14.1.  Four rows to a key head are bound by memory either way, and 16
+// leave it a little more of the SM: two contexts of 131072 keys 82.8 us in units of 16, 83.6 in units of 32 (64 single
+// tokens 151 and 154).  128 rows in two units of 64 read and work on the keys twice, 43 us where the bytes take 10; a
+// unit of 128, which would need one CTA an SM, was not built.
 int unit_rows(int max_block_len, int n_heads, int n_kv_heads) {
   const int64_t rows = static_cast<int64_t>(max_block_len) * (n_heads / n_kv_heads);
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;

@@ -15,9 +15,9 @@
 // head) items to its warps.
 //
 // Measured (d = 128): four whole sequences of 5120 rows of 32 heads from the bf16 pools
-// 74.7 us, 6.7 TB/s, a copy's rate (118 us with fp32 maxima and products one by one and
-// the rare values in the same registers).  512 block rows of 32 heads 5.6 us, 128 single
-// tokens of 8 heads 4.3 us: a launch and the dependent trips cu_block -> lengths -> page
+// 74.8 us, 6.7 TB/s, a copy's rate (118 us with fp32 maxima and products one by one and
+// the rare values in the same registers), and out of packed rows 77.2 us, 6.5 TB/s.  512
+// block rows of 32 heads 5.7 us, 128 single tokens of 8 heads 4.4 us: a launch and the dependent trips cu_block -> lengths -> page
 // -> rows, scale.
 #include <algorithm>
 
@@ -275,8 +275,8 @@ cudaError_t launch_kv8_write(const Kv8WriteArgs& a, int num_sms, cudaStream_t st
   const int mean = std::min(kKv8Group, std::max(1, rows / a.bt.batch));
   const long long items = 2ll * heads * ((rows + mean - 1) / mean), resident = static_cast<long long>(kCtasPerSm) * num_sms;
   int slice, hc;
-  // Enough for every resident warp several times over: wide slices, whose search serves more items (whole sequences 74.9
-  // us; 75.4 with narrow ones).  Else latency: about an item to a warp (single tokens 4.2 us, blocks 5.6; 41.5 and 6.1
+  // Enough for every resident warp several times over: wide slices, whose search serves more items (whole sequences 74.8
+  // us; 75.6 with narrow ones).  Else latency: about an item to a warp (single tokens 4.4 us, blocks 5.7; 42.0 and 6.2
   // with the wide ones).
   if (items >= 4 * kWarps * resident) {
     slice = kMaxSlice;
