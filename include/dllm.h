@@ -390,7 +390,10 @@ dllm_status dllm_block_ffn(const dllm_layer_desc* desc, const dllm_batch* batch,
  * sequence has no rows, nothing is read or written for it.
  * total_block_rows, total_seq_rows, max_block_len and max_seq_len bound the
  * device arrays; the actual sums and lengths may be smaller from one replay of
- * a captured call to the next.  Every call waits for the preceding kernel of
+ * a captured call to the next.  A block longer than its packed rows
+ * (cu_block[b + 1] - cu_block[b]) or reaching beyond total_block_rows sets
+ * DLLM_DEVERR_BAD_SHAPE and is neither written nor attended to; the other
+ * sequences are.  Every call waits for the preceding kernel of
  * its stream before it reads or writes anything. */
 
 /* The 8-bit cache of one layer (device buffers, caller-owned).  The value of a
