@@ -189,13 +189,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv8_write_kernel(const K
   if (t == 0) n_groups = 0;
   // One CTA compares all blocks with the sums: one that they leave no rows is met by no search below.
   const bool looks = blockIdx.x == 0 && blockIdx.y == 0;
-  const int len_t = looks && t < bt.batch ? __ldg(bt.block_len + t) : 0;
+  auto rows_of = [&](int b) { return __ldg(bt.seq_len + b) == 0 ? 0 : __ldg(bt.block_len + b); };  // (a place without a request)
+  const int rows_t = looks && t < bt.batch ? rows_of(t) : 0;
   if (in_smem)
     for (int i = t; i <= bt.batch; i += kThreads) cu[i] = __ldg(bt.cu_block + i);
   __syncthreads();
   const int* cub = in_smem ? cu : bt.cu_block;
   for (int b = t; looks && b < bt.batch; b += kThreads)
-    if (cub[b + 1] - cub[b] != (b == t ? len_t : __ldg(bt.block_len + b))) err |= kErrBadShape;
+    if (cub[b + 1] - cub[b] != (b == t ? rows_t : rows_of(b))) err |= kErrBadShape;
   const int total = min(cub[bt.batch], bt.total_block_rows);
   if (row0 == 0 && t == 0 && (cub[bt.batch] < 0 || cub[bt.batch] > bt.total_block_rows)) err |= kErrBadShape;
   if (row0 >= total) {

@@ -1,5 +1,6 @@
 """The 8-bit paged cache's calls on batches that contradict their bounds, or that the plan could not serve: what is
 refused is refused whole, its error bit is set, and no other sequence sees any of it."""
+import random
 from types import SimpleNamespace
 
 import pytest
@@ -233,3 +234,30 @@ def test_a_short_plan_called_again_gives_the_same_and_pages_that_come_later_are_
     ring = ring.swapped()
     dllm.dllm_batch_plan(view.c, out, held, t["table"], t["cub"], t["cus"], ring.c)
     assert held.tolist() == [2, 0, 1] and t["table"].tolist()[2] == [5, -5, 6, 0]
+
+
+# ------------------------------------------------------------------ places without a request
+def _padded(batch=600):
+    """A batch of fixed places: those without a request have length 0 and keep a block length and start of before."""
+    r = random.Random(7)
+    n = [r.choice([0, 0, 40, 200, 333]) for _ in range(batch)]
+    rows = [8] * batch
+    start = [max(0, x - 8) if x else 77 for x in n]
+    return n, start, rows
+
+
+@pytest.mark.parametrize("batch", [5, 600])
+def test_write_and_attention_take_a_length_of_zero_beside_a_block_length(batch):
+    n, start, rows = _padded(batch)
+    there = [r if x else 0 for x, r in zip(n, rows)]
+    b = Batch(n, start, there, seed=1, max_block=8, max_seq=333, max_pages=6)
+    b.t["rows"].copy_(ints(rows))
+    kv8 = random_pools(b.num_pages, 2, 64, 3)
+    k, v, q = _rows(b.M, 2, 64, 4), _rows(b.M, 2, 64, 5), _rows(b.M, 4, 64, 6)
+    want = _written(kv8, n, start, there, b.table, cu(there), range(batch), k, v)
+    dllm.dllm_kv8_write(_desc(4, 64), b.view.c, k, v, kv8.c)
+    assert b.bits() == 0
+    _assert_pools(kv8, want)
+    o, lse = _attend(b.view, q, kv8, b.M, dllm.DLLM_ROWS_BLOCK, 4, 64)
+    assert b.bits() == 0
+    assert_attention(b, q, kv8, o, lse)
