@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) batch_plan_kernel(const 
       }
       need = (bad_held || bad_n) ? held : (n + kPage - 1) / kPage;
       if (rows < 0 || start < 0 || rows > n - start) {
-        if (rows != 0) err |= kErrBadShape;
+        if (rows < 0 || (rows > 0 && n > 0)) err |= kErrBadShape;  // (a length of 0 is a place without a request: no rows)
         rows = 0;
       }
       mine = {rows, n, bad_held || need < held ? 0 : need - held, bad_held || need > held ? 0 : held - need};

@@ -444,8 +444,8 @@ typedef struct dllm_page_ring {
  * dllm_block_attention, dllm_state_merge or dllm_step_attention).
  *   A seq_len outside [0, max_seq_len], a pages_held outside [0,
  *   max_pages_per_seq] (both: the sequence keeps its pages, its lengths count
- *   as 0) or a block outside its sequence (its rows count as 0) sets
- *   DLLM_DEVERR_BAD_SHAPE, as do sums beyond total_block_rows or
+ *   as 0) or a block outside a sequence that is not empty (its rows count as 0)
+ *   sets DLLM_DEVERR_BAD_SHAPE, as do sums beyond total_block_rows or
  *   total_seq_rows and a ring state outside the ring (taken as empty); an id
  *   outside the pages sets DLLM_DEVERR_BAD_PAGE and is written as -1.
  *   row_slot, row_seq, row_pos: device int32 [total_block_rows], 16-byte

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from block_wise_kv_gb300 import dllm
-from kv8_util import PAGE, Batch, assert_attention, cu, ints, random_pools, write
+from kv8_util import PAGE, Batch, assert_attention, cu, ints, plan, random_pools, write
 
 pytestmark = pytest.mark.gpu
 
@@ -261,3 +261,30 @@ def test_write_and_attention_take_a_length_of_zero_beside_a_block_length(batch):
     o, lse = _attend(b.view, q, kv8, b.M, dllm.DLLM_ROWS_BLOCK, 4, 64)
     assert b.bits() == 0
     assert_attention(b, q, kv8, o, lse)
+
+
+@pytest.mark.parametrize("batch", [5, 600])
+def test_a_plan_takes_a_length_of_zero_beside_a_block_length(batch):
+    """Such a place has no rows: nothing is flagged, the pages it held go back, the others are planned."""
+    n, start, rows = _padded(batch)
+    there = [r if x else 0 for x, r in zip(n, rows)]
+    held = [2 if x == 0 else 0 for x in n]
+    need = [(x + PAGE - 1) // PAGE for x in n]
+    P = sum(held) + sum(need)
+    table = [[-1] * 6 for _ in n]
+    at = 0
+    for b, h in enumerate(held):
+        table[b][:h] = range(at, at + h)
+        at += h
+    ring = list(range(at, P)) + [-1] * at
+    M = 8 * batch
+    t = dict(table=ints(table), n=ints(n), start=ints(start), rows=ints(rows), cub=ints([0] * (batch + 1)), cus=ints([0] * (batch + 1)),
+             err=ints([0]), held=ints(held), out=ints([0] * batch), slot=ints([0] * M), seq=ints([0] * M), pos=ints([0] * M))
+    view = dllm.BatchView(t["table"], t["n"], t["start"], t["rows"], t["cub"], t["cus"], M, sum(n), 8, 333, t["err"])
+    r = dllm.PageRing(ints(ring), ints([0, P - at]), ints([0, 0]))
+    dllm.dllm_batch_plan(view.c, t["held"], t["out"], t["table"], t["cub"], t["cus"], r.c, t["slot"], t["seq"], t["pos"])
+    assert view.error_bits() == 0
+    now, state, cub, cus, slot, seq, pos, short = plan(n, start, there, held, table, ring, (0, P - at), M)
+    assert not short and (t["out"].tolist(), t["cub"].tolist(), t["cus"].tolist()) == (now, cub, cus)
+    assert (t["slot"].tolist(), t["seq"].tolist(), t["pos"].tolist()) == (slot, seq, pos)
+    assert t["table"].tolist() == table and r.pages.tolist() == ring and r.state_out.tolist() == state
