@@ -7,6 +7,7 @@
 #include "dllm.h"
 #include "kernels.cuh"
 #include "kv8.cuh"
+#include "layer_ops.cuh"
 
 using namespace dllm;
 
@@ -676,6 +677,234 @@ dllm_status dllm_kv8_attention(const dllm_layer_desc* desc, const dllm_batch* ba
   a.scale_log2 = softmax_scale(desc) * 1.4426950408889634f;
   a.ws = ws;
   return cuda_status(launch_kv8_attention(a, device_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+// Elements that rows and heads take up: heads of `len` at rs and hs elements (bf16), from p on.
+struct Extent {
+  const void* p;
+  int64_t rows, rs, heads, hs, len;
+  int64_t width() const { return (heads - 1) * hs + len; }              // of a row
+  int64_t bytes() const { return ((rows - 1) * rs + width()) * 2; }
+};
+
+// Whether two sets of rows may share an element: no where their extents lie apart, where they are columns of
+// the same wider rows that lie apart, or heads side by side at the same strides; yes otherwise.
+bool may_overlap(const Extent& a, const Extent& b) {
+  if (a.rows == 0 || b.rows == 0 || a.heads == 0 || b.heads == 0) return false;
+  if (!overlap(a.p, a.bytes(), b.p, b.bytes())) return false;
+  const int64_t bytes = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p));
+  if (bytes % 2 != 0) return true;
+  // a's and b's pieces repeat every `step`: apart iff b's begins behind a's and ends before a's next
+  auto apart = [&](int64_t step, int64_t len_a, int64_t len_b) {
+    if (step <= 0) return false;
+    const int64_t d = ((bytes / 2) % step + step) % step;
+    return d >= len_a && d + len_b <= step;
+  };
+  if (a.rs == b.rs && apart(a.rs, a.width(), b.width())) return false;
+  if (a.hs == b.hs && a.rs == b.rs && a.heads > 1 && b.heads > 1 && a.hs > 0 && a.rs % a.hs == 0 &&
+      apart(a.hs, a.len, b.len))
+    return false;
+  return true;
+}
+
+dllm_status check_linear(const dllm_linear_layer* l, int32_t rows) {
+  if (l == nullptr || rows < 0) return DLLM_ERR_INVALID_ARGUMENT;
+  if (l->in_features < 1 || l->out_features < 1) return DLLM_ERR_INVALID_ARGUMENT;
+  if (l->act < DLLM_ACT_NONE || l->act > DLLM_ACT_GELU_TANH) return DLLM_ERR_INVALID_ARGUMENT;
+  if (l->gated != 0 && l->gated != 1) return DLLM_ERR_INVALID_ARGUMENT;
+  if (!(l->rms_eps >= 0.f) || !isfinite(l->rms_eps)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (l->in_features % 8 != 0) return DLLM_ERR_UNSUPPORTED;
+  // tiles of 128 x 16 and coordinates are counted in 32 bits
+  if (l->in_features > kMaxRows - 64 || l->out_features > (kMaxRows - 256) / 2 || rows > kMaxRows - 256)
+    return DLLM_ERR_UNSUPPORTED;
+  const int64_t wide = static_cast<int64_t>(l->out_features) * (l->gated ? 2 : 1);
+  if (((wide + 127) / 128) * ((rows + int64_t{15}) / 16) > kMaxRows / 2) return DLLM_ERR_UNSUPPORTED;
+  return DLLM_OK;
+}
+
+size_t linear_xhat_bytes(const dllm_linear_layer* l, int32_t rows) {
+  return (static_cast<size_t>(rows) * l->in_features * 2 + 255) & ~static_cast<size_t>(255);
+}
+}  // namespace
+
+dllm_status dllm_linear_workspace_size(const dllm_linear_layer* layer, int32_t rows, int32_t normed, size_t* bytes) {
+  DLLM_TRY(check_linear(layer, rows));
+  if (bytes == nullptr) return DLLM_ERR_INVALID_ARGUMENT;
+  *bytes = normed ? linear_xhat_bytes(layer, rows) : 0;
+  return DLLM_OK;
+}
+
+dllm_status dllm_linear(const dllm_linear_layer* layer, int32_t rows, const void* x, int64_t x_stride,
+                        const void* rms_gain, const void* w, const void* bias, const void* residual,
+                        int64_t residual_stride, void* y, int64_t y_stride, int32_t* error_flag, void* ws,
+                        size_t ws_bytes, void* stream) {
+  DLLM_TRY(check_linear(layer, rows));
+  if (rows == 0) return DLLM_OK;
+  const int64_t k = layer->in_features, n = layer->out_features, wide = layer->gated ? 2 * n : n;
+  if (!aligned(x, 16) || x_stride % 8 != 0 || x_stride < k || !aligned(w, 16)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (x_stride > (int64_t{1} << 38)) return DLLM_ERR_UNSUPPORTED;  // a tensor map's strides are below 2^40 bytes
+  if (rms_gain != nullptr && !aligned(rms_gain, 16)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (bias != nullptr && !aligned(bias, 2)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (residual != nullptr && (!aligned(residual, 2) || residual_stride < n)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (!aligned(y, 2) || y_stride < n) return DLLM_ERR_INVALID_ARGUMENT;
+  if (error_flag != nullptr && !aligned(error_flag, 4)) return DLLM_ERR_INVALID_ARGUMENT;
+  const Extent ye = {y, rows, y_stride, 1, 0, n};
+  if (may_overlap(ye, {x, rows, x_stride, 1, 0, k}) || may_overlap(ye, {w, 1, 0, 1, 0, wide * k}) ||
+      (rms_gain != nullptr && may_overlap(ye, {rms_gain, 1, 0, 1, 0, k})) ||
+      (bias != nullptr && may_overlap(ye, {bias, 1, 0, 1, 0, wide})))
+    return DLLM_ERR_INVALID_ARGUMENT;
+  if (residual != nullptr && !(residual == y && (residual_stride == y_stride || rows == 1)) &&
+      may_overlap(ye, {residual, rows, residual_stride, 1, 0, n}))
+    return DLLM_ERR_INVALID_ARGUMENT;
+  if (rms_gain != nullptr) {
+    const size_t need = linear_xhat_bytes(layer, rows);
+    if (ws_bytes < need) return DLLM_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned(ws, 256)) return DLLM_ERR_INVALID_ARGUMENT;
+    const Extent we = {ws, 1, 0, 1, 0, rows * k};
+    if (may_overlap(we, ye) || may_overlap(we, {x, rows, x_stride, 1, 0, k}) || may_overlap(we, {w, 1, 0, 1, 0, wide * k}))
+      return DLLM_ERR_INVALID_ARGUMENT;
+  }
+  LinearArgs a = {};
+  a.x = x;
+  a.x_stride = x_stride;
+  a.gain = rms_gain;
+  a.w = w;
+  a.bias = bias;
+  a.residual = residual;
+  a.r_stride = residual_stride;
+  a.y = y;
+  a.y_stride = y_stride;
+  a.xhat = ws;
+  a.err = error_flag;
+  a.rows = rows;
+  a.k = layer->in_features;
+  a.n = layer->out_features;
+  a.wide = static_cast<int32_t>(wide);
+  a.act = layer->act;
+  a.gated = layer->gated != 0;
+  a.rms_eps = layer->rms_eps;
+  return cuda_status(launch_linear(a, device_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+Extent in_extent(const dllm_head_rows* h, int32_t rows, int32_t d) {
+  return {h->in, rows, h->in_row_stride, h->n_heads, h->in_head_stride, d};
+}
+Extent out_extent(const dllm_head_rows* h, int32_t rows, int32_t d) {
+  return {h->out, rows, h->out_row_stride, h->n_heads, h->out_head_stride, d};
+}
+
+dllm_status check_head_rows(const dllm_head_rows* h, int32_t rows, int32_t d) {
+  if (h->n_heads < 1) return DLLM_ERR_INVALID_ARGUMENT;
+  if (!rows_ok(h->in, h->in_row_stride, h->in_head_stride) || !rows_ok(h->out, h->out_row_stride, h->out_head_stride))
+    return DLLM_ERR_INVALID_ARGUMENT;
+  if (h->gain != nullptr && !aligned(h->gain, 16)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (h->in_row_stride > (int64_t{1} << 31) || h->in_head_stride > (int64_t{1} << 31) ||
+      h->out_row_stride > (int64_t{1} << 31) || h->out_head_stride > (int64_t{1} << 31))
+    return DLLM_ERR_UNSUPPORTED;  // offsets in 64 bits
+  // the outputs' heads lie apart: heads within rows, or rows within heads
+  const int64_t rs = h->out_row_stride, hs = h->out_head_stride;
+  const bool heads_in_rows = (h->n_heads == 1 || hs >= d) && (rows <= 1 || rs >= (h->n_heads - 1) * hs + d);
+  const bool rows_in_heads = (rows <= 1 || rs >= d) && (h->n_heads == 1 || hs >= (rows - 1) * rs + d);
+  if (!heads_in_rows && !rows_in_heads) return DLLM_ERR_INVALID_ARGUMENT;
+  const bool same = h->in == h->out && (rows <= 1 || h->in_row_stride == rs) &&
+                    (h->n_heads == 1 || h->in_head_stride == hs);
+  if (!same && may_overlap(out_extent(h, rows, d), in_extent(h, rows, d))) return DLLM_ERR_INVALID_ARGUMENT;
+  return DLLM_OK;
+}
+
+HeadRows head_rows(const dllm_head_rows* h) {
+  HeadRows r;
+  r.in = h->in;
+  r.in_row = h->in_row_stride;
+  r.in_head = h->in_head_stride;
+  r.out = h->out;
+  r.out_row = h->out_row_stride;
+  r.out_head = h->out_head_stride;
+  r.gain = h->gain;
+  r.n_heads = h->n_heads;
+  return r;
+}
+}  // namespace
+
+dllm_status dllm_head_norm_rope(const dllm_layer_desc* desc, int32_t rows, const int32_t* row_pos,
+                                const dllm_head_rows* queries, const dllm_head_rows* keys, const float* rope_table,
+                                int32_t rope_max_pos, int32_t rotary_dim, int32_t pairs, int32_t* error_flag,
+                                void* stream) {
+  DLLM_TRY(check_desc(desc));
+  if (rows < 0 || queries == nullptr || rope_max_pos < 1) return DLLM_ERR_INVALID_ARGUMENT;
+  if (pairs != DLLM_ROPE_HALVES && pairs != DLLM_ROPE_NEIGHBOURS) return DLLM_ERR_INVALID_ARGUMENT;
+  if ((rotary_dim != 64 && rotary_dim != 128) || rotary_dim > desc->head_dim) return DLLM_ERR_UNSUPPORTED;
+  if (rows == 0) return DLLM_OK;
+  const int32_t d = desc->head_dim;
+  if (!aligned(row_pos, 4) || !aligned(rope_table, 16)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (error_flag != nullptr && !aligned(error_flag, 4)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (queries->n_heads != desc->n_heads) return DLLM_ERR_INVALID_ARGUMENT;
+  DLLM_TRY(check_head_rows(queries, rows, d));
+  const Extent pos = {row_pos, 1, 0, 1, 0, 2 * int64_t{rows}};
+  const Extent table = {rope_table, 1, 0, 1, 0, 2 * int64_t{rope_max_pos} * rotary_dim};
+  for (const dllm_head_rows* h : {queries, keys}) {
+    if (h == nullptr) continue;
+    if (h == keys) DLLM_TRY(check_head_rows(keys, rows, d));
+    const Extent out = out_extent(h, rows, d);
+    if (may_overlap(out, pos) || may_overlap(out, table)) return DLLM_ERR_INVALID_ARGUMENT;
+    for (const dllm_head_rows* g : {queries, keys})
+      if (g != nullptr && g->gain != nullptr && may_overlap(out, {g->gain, 1, 0, 1, 0, d}))
+        return DLLM_ERR_INVALID_ARGUMENT;
+  }
+  if (keys != nullptr) {
+    const Extent qi = in_extent(queries, rows, d), qo = out_extent(queries, rows, d);
+    const Extent ki = in_extent(keys, rows, d), ko = out_extent(keys, rows, d);
+    if (may_overlap(qo, ki) || may_overlap(qo, ko) || may_overlap(ko, qi)) return DLLM_ERR_INVALID_ARGUMENT;
+  }
+  HeadRopeArgs a = {};
+  a.q = head_rows(queries);
+  if (keys != nullptr) a.k = head_rows(keys);
+  a.row_pos = row_pos;
+  a.table = rope_table;
+  a.err = error_flag;
+  a.rows = rows;
+  a.head_dim = d;
+  a.max_pos = rope_max_pos;
+  a.rotary_dim = rotary_dim;
+  a.neighbours = pairs == DLLM_ROPE_NEIGHBOURS;
+  a.eps = desc->rms_eps;
+  return cuda_status(launch_head_rope(a, device_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+dllm_status dllm_token_scores(int32_t rows, int32_t vocab, const void* logits, int32_t logits_type, int64_t row_stride,
+                              float scale, const int32_t* tokens, float* logp, float* lse, float* entropy,
+                              int32_t top_k, int32_t* top_ids, float* top_logp, int32_t* error_flag, void* stream) {
+  if (rows < 0 || vocab < 1 || top_k < 0) return DLLM_ERR_INVALID_ARGUMENT;
+  if (logits_type != DLLM_TYPE_BF16 && logits_type != DLLM_TYPE_FP32) return DLLM_ERR_INVALID_ARGUMENT;
+  if (!(scale > 0.f) || !isfinite(scale)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (top_k > kMaxTop || vocab > (1 << 30)) return DLLM_ERR_UNSUPPORTED;
+  if (rows == 0) return DLLM_OK;
+  const int size = logits_type == DLLM_TYPE_BF16 ? 2 : 4;
+  if (!aligned(logits, size) || row_stride < vocab) return DLLM_ERR_INVALID_ARGUMENT;
+  if (row_stride > (int64_t{1} << 31)) return DLLM_ERR_UNSUPPORTED;  // offsets in 64 bits
+  if ((tokens == nullptr) != (logp == nullptr)) return DLLM_ERR_INVALID_ARGUMENT;
+  for (const void* p : {static_cast<const void*>(tokens), static_cast<const void*>(logp), static_cast<const void*>(lse),
+                        static_cast<const void*>(entropy), static_cast<const void*>(error_flag)})
+    if (p != nullptr && !aligned(p, 4)) return DLLM_ERR_INVALID_ARGUMENT;
+  if (top_k > 0 && (!aligned(top_ids, 4) || !aligned(top_logp, 4))) return DLLM_ERR_INVALID_ARGUMENT;
+  ScoreArgs a = {};
+  a.logits = logits;
+  a.stride = row_stride;
+  a.tokens = tokens;
+  a.logp = logp;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.top_ids = top_ids;
+  a.top_logp = top_logp;
+  a.err = error_flag;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.top = top_k;
+  a.scale = scale;
+  a.fp32 = logits_type == DLLM_TYPE_FP32;
+  return cuda_status(launch_token_scores(a, device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
 const char* dllm_status_string(dllm_status status) {

@@ -39,6 +39,22 @@ inline cudaError_t encode_2d_sw128(CUtensorMap* map, CUtensorMapDataType dtype, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// bf16 [rows][cols], rows `stride` elements apart (a multiple of 8), loaded in boxes of
+// box_cols x box_rows with 128-byte swizzling (box_cols 64).  What lies outside reads zero.
+inline cudaError_t encode_rows_sw128(CUtensorMap* map, const void* ptr, uint64_t cols, uint64_t rows, uint64_t stride,
+                                     uint32_t box_cols, uint32_t box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {stride * 2};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // Row-major [n2][n1][cols] tensor (cols innermost, all dense), loaded in
 // boxes of box_cols x 1 x box_n2 with 128-byte swizzling: box_n2 rows of
 // box_cols elements taken at a stride of n1 * cols (one fixed middle index).

@@ -45,6 +45,17 @@ DLLM_OP_CACHE_ADVANCE = 5
 DLLM_ROWS_BLOCK = 0
 DLLM_ROWS_FULL = 1
 
+DLLM_ACT_NONE = 0
+DLLM_ACT_SILU = 1
+DLLM_ACT_GELU = 2
+DLLM_ACT_GELU_TANH = 3
+
+DLLM_ROPE_HALVES = 0
+DLLM_ROPE_NEIGHBOURS = 1
+
+DLLM_TYPE_BF16 = 0
+DLLM_TYPE_FP32 = 1
+
 PAGE = 64
 _BF16, _FP32, _INT32 = torch.bfloat16, torch.float32, torch.int32
 KV8_GROUP = 16  # token positions that share a scale of the 8-bit cache
@@ -54,7 +65,9 @@ EXPORTS = ("dllm_workspace_size", "dllm_rope_table_build", "dllm_qkv_weight_pack
            "dllm_cache_build", "dllm_cache_advance", "dllm_block_qkv_rope_write", "dllm_block_qkv_rope_write_noalloc",
            "dllm_block_attention", "dllm_state_merge", "dllm_step_attention", "dllm_lm_head_workspace_size",
            "dllm_block_lm_head", "dllm_ffn_workspace_size", "dllm_block_ffn", "dllm_batch_plan", "dllm_kv8_write",
-           "dllm_kv8_write_pool", "dllm_kv8_attention_workspace_size", "dllm_kv8_attention", "dllm_status_string")
+           "dllm_kv8_write_pool", "dllm_kv8_attention_workspace_size", "dllm_kv8_attention",
+           "dllm_linear_workspace_size", "dllm_linear", "dllm_head_norm_rope", "dllm_token_scores",
+           "dllm_status_string")
 
 
 class DllmError(RuntimeError):
@@ -93,6 +106,17 @@ class Kv8CacheC(ctypes.Structure):
 class PageRingC(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_void_p), ("state", ctypes.c_void_p), ("state_out", ctypes.c_void_p),
                 ("num_pages", ctypes.c_int32)]
+
+
+class LinearLayerC(ctypes.Structure):
+    _fields_ = [("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("gated", ctypes.c_int32), ("rms_eps", ctypes.c_float)]
+
+
+class HeadRowsC(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("in_row_stride", ctypes.c_int64), ("in_head_stride", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("gain", ctypes.c_void_p), ("n_heads", ctypes.c_int32)]
 
 
 _lib = None
@@ -135,6 +159,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
                 "dllm_kv8_write_pool": [P(LayerDescC), P(BatchC), P(CacheC), P(Kv8CacheC), vp],
                 "dllm_kv8_attention_workspace_size": [P(LayerDescC), P(BatchC), P(Kv8CacheC), P(sz)],
                 "dllm_kv8_attention": [P(LayerDescC), P(BatchC), vp, i64, P(Kv8CacheC), vp, i32, vp, vp, sz, vp],
+                "dllm_linear_workspace_size": [P(LinearLayerC), i32, i32, P(sz)],
+                "dllm_linear": [P(LinearLayerC), i32, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, sz, vp],
+                "dllm_head_norm_rope": [P(LayerDescC), i32, vp, P(HeadRowsC), P(HeadRowsC), vp, i32, i32, i32, vp, vp],
+                "dllm_token_scores": [i32, i32, vp, i32, i64, ctypes.c_float, vp, vp, vp, vp, i32, vp, vp, vp, vp],
             }
             for name, argt in sig.items():
                 fn = getattr(lib, name)
@@ -376,10 +404,118 @@ def dllm_kv8_attention(desc, batch, q: torch.Tensor, kv8, o, lse, ws, o_rows: in
         raise DllmError("dllm_kv8_attention", status)
 
 
+def dllm_linear_workspace_size(layer, rows: int, normed: bool) -> int:
+    out = ctypes.c_size_t(0)
+    _check("dllm_linear_workspace_size", load().dllm_linear_workspace_size(
+        ctypes.byref(layer), int(rows), int(bool(normed)), ctypes.byref(out)))
+    return int(out.value)
+
+
+def _vector_ok(t, dtype, n: int, dev: int) -> bool:
+    """None, or a contiguous tensor of n values or more."""
+    return t is None or (t.dtype is dtype and t.numel() >= n and t.is_contiguous() and t.get_device() == dev)
+
+
+def dllm_linear(layer, x: torch.Tensor, w, y, rms_gain=None, bias=None, residual=None, ws=None, error=None,
+                stream=None):
+    """x: bf16 [M][in_features], w: contiguous bf16 [out_features (gated: twice that)][in_features], y and residual:
+    bf16 [M][out_features]; x, y and residual with any row stride; rms_gain, bias: bf16 vectors; ws: a uint8 tensor of
+    dllm_linear_workspace_size bytes (with a gain); error: an int32 word."""
+    k, n = layer.in_features, layer.out_features
+    wide = 2 * n if layer.gated else n
+    m, dev, xs, ys = x.shape[0], x.get_device(), x.stride(), y.stride()
+    rs = ys if residual is None else residual.stride()
+    if (x.dtype is not _BF16 or tuple(x.shape) != (m, k) or xs[1] != 1 and k > 1
+            or w.dtype is not _BF16 or tuple(w.shape) != (wide, k) or not w.is_contiguous() or w.get_device() != dev
+            or y.dtype is not _BF16 or tuple(y.shape) != (m, n) or ys[1] != 1 and n > 1 or y.get_device() != dev
+            or residual is not None and (
+                residual.dtype is not _BF16 or tuple(residual.shape) != (m, n) or rs[1] != 1 and n > 1
+                or residual.get_device() != dev)
+            or not _vector_ok(rms_gain, _BF16, k, dev) or not _vector_ok(bias, _BF16, wide, dev)
+            or not _vector_ok(error, _INT32, 1, dev)
+            or ws is not None and (not ws.is_contiguous() or ws.get_device() != dev)
+            or dev != torch._C._cuda_getDevice()):
+        raise DllmError("dllm_linear", DLLM_ERR_INVALID_ARGUMENT)
+    status = (_lib or load()).dllm_linear(
+        layer, m, x.data_ptr(), xs[0] if m > 1 else k, None if rms_gain is None else rms_gain.data_ptr(), w.data_ptr(),
+        None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
+        rs[0] if m > 1 else n, y.data_ptr(), ys[0] if m > 1 else n, None if error is None else error.data_ptr(),
+        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, _on(dev, stream))
+    if status:
+        raise DllmError("dllm_linear", status)
+
+
+def _head_rows(t, out, gain, m: int, d: int, dev: int):
+    """The dllm_head_rows of bf16 tensors [m][heads][d], or None where they do not fit."""
+    ts, os_, shape = t.stride(), out.stride(), t.shape
+    if (len(ts) != 3 or shape != out.shape or shape[0] != m or shape[2] != d or ts[2] != 1 or os_[2] != 1
+            or t.dtype is not _BF16 or out.dtype is not _BF16 or t.get_device() != dev or out.get_device() != dev
+            or not _vector_ok(gain, _BF16, d, dev)):
+        return None
+    h = shape[1]
+    return HeadRowsC(t.data_ptr(), ts[0] if m > 1 else h * d, ts[1] if h > 1 else d, out.data_ptr(),
+                     os_[0] if m > 1 else h * d, os_[1] if h > 1 else d, None if gain is None else gain.data_ptr(), h)
+
+
+def dllm_head_norm_rope(desc, q: torch.Tensor, q_out, k, k_out, row_pos, rope_table, q_gain=None, k_gain=None,
+                        pairs: int = DLLM_ROPE_HALVES, error=None, stream=None):
+    """q, q_out: bf16 [M][n_heads][head_dim], k, k_out: bf16 [M][any number of heads][head_dim] or None, the last
+    dimension contiguous, outputs the inputs themselves or apart from them; row_pos: contiguous int32 of M positions
+    (more are fine); rope_table: contiguous float32 [positions][rotary_dim / 2][2]; gains: bf16 [head_dim] or None."""
+    d, m, dev = desc.head_dim, q.shape[0], q.get_device()
+    queries = _head_rows(q, q_out, q_gain, m, d, dev)
+    keys = None if k is None else _head_rows(k, k_out, k_gain, m, d, dev)
+    ts = rope_table.shape
+    if (queries is None or k is not None and keys is None or not _vector_ok(row_pos, _INT32, m, dev) or row_pos is None
+            or rope_table.dtype is not _FP32 or len(ts) != 3 or ts[2] != 2 or not rope_table.is_contiguous()
+            or rope_table.get_device() != dev or not _vector_ok(error, _INT32, 1, dev)
+            or dev != torch._C._cuda_getDevice()):
+        raise DllmError("dllm_head_norm_rope", DLLM_ERR_INVALID_ARGUMENT)
+    status = (_lib or load()).dllm_head_norm_rope(
+        desc, m, row_pos.data_ptr(), queries, keys, rope_table.data_ptr(), ts[0], 2 * ts[1], pairs,
+        None if error is None else error.data_ptr(), _on(dev, stream))
+    if status:
+        raise DllmError("dllm_head_norm_rope", status)
+
+
+def dllm_token_scores(logits: torch.Tensor, tokens=None, logp=None, lse=None, entropy=None, top_ids=None,
+                      top_logp=None, scale: float = 1.0, error=None, stream=None):
+    """logits: bf16 or float32 [M][vocab], any row stride; tokens: int32 and logp: float32 of M values, or both None;
+    lse, entropy: float32 of M values or None; top_ids: contiguous int32 and top_logp: contiguous float32 [M][top_k], or
+    both None."""
+    dev, shape, ls = logits.get_device(), logits.shape, logits.stride()
+    if len(shape) != 2:
+        raise DllmError("dllm_token_scores", DLLM_ERR_INVALID_ARGUMENT)
+    m, vocab = shape
+    top = 0 if top_ids is None else top_ids.shape[-1]
+    if (logits.dtype is not _BF16 and logits.dtype is not _FP32 or ls[1] != 1 and vocab > 1
+            or (tokens is None) != (logp is None) or (top_ids is None) != (top_logp is None)
+            or top_ids is not None and (tuple(top_ids.shape) != (m, top) or tuple(top_logp.shape) != (m, top))
+            or not _vector_ok(tokens, _INT32, m, dev) or not _vector_ok(logp, _FP32, m, dev)
+            or not _vector_ok(lse, _FP32, m, dev) or not _vector_ok(entropy, _FP32, m, dev)
+            or not _vector_ok(top_ids, _INT32, m * top, dev) or not _vector_ok(top_logp, _FP32, m * top, dev)
+            or not _vector_ok(error, _INT32, 1, dev) or dev != torch._C._cuda_getDevice()):
+        raise DllmError("dllm_token_scores", DLLM_ERR_INVALID_ARGUMENT)
+    status = (_lib or load()).dllm_token_scores(
+        m, vocab, logits.data_ptr(), DLLM_TYPE_BF16 if logits.dtype is _BF16 else DLLM_TYPE_FP32,
+        ls[0] if m > 1 else vocab, scale, None if tokens is None else tokens.data_ptr(),
+        None if logp is None else logp.data_ptr(), None if lse is None else lse.data_ptr(),
+        None if entropy is None else entropy.data_ptr(), top, None if top_ids is None else top_ids.data_ptr(),
+        None if top_logp is None else top_logp.data_ptr(), None if error is None else error.data_ptr(),
+        _on(dev, stream))
+    if status:
+        raise DllmError("dllm_token_scores", status)
+
+
 # ---------------------------------------------------- memory / structs ----
 def layer_desc(d_model: int, n_heads: int, head_dim: int, rope_theta: float, rms_eps: float = 1e-5,
                softmax_scale: float = 0.0) -> LayerDescC:
     return LayerDescC(d_model, n_heads, head_dim, PAGE, rope_theta, rms_eps, softmax_scale)
+
+
+def linear_desc(in_features: int, out_features: int, act: int = DLLM_ACT_NONE, gated: bool = False,
+                rms_eps: float = 1e-5) -> LinearLayerC:
+    return LinearLayerC(in_features, out_features, act, int(gated), rms_eps)
 
 
 class BatchLayout:

@@ -511,6 +511,127 @@ dllm_status dllm_kv8_attention(const dllm_layer_desc* desc, const dllm_batch* ba
                                int64_t q_row_stride, const dllm_kv8_cache* kv8, void* o, int32_t o_rows, float* lse,
                                void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The rest of a layer of grouped heads, for programs that keep the 8-bit
+ * cache: products with a weight, the norm and rotation of the heads between
+ * projection and cache, and what a sampler reads off the logits.  An addition
+ * of this library.  A step of such a layer is dllm_batch_plan, dllm_linear
+ * (rms_gain, bias), dllm_head_norm_rope, dllm_kv8_write, dllm_kv8_attention,
+ * dllm_linear (residual), dllm_linear (rms_gain, gated), dllm_linear
+ * (residual); behind the last layer dllm_linear (or dllm_block_lm_head) and
+ * dllm_token_scores.  Every call waits for the preceding kernel of its stream
+ * before it reads or writes anything. */
+
+#define DLLM_ACT_NONE 0
+#define DLLM_ACT_SILU 1      /* t / (1 + e^-t) */
+#define DLLM_ACT_GELU 2      /* t (1 + erf(t / sqrt 2)) / 2 */
+#define DLLM_ACT_GELU_TANH 3 /* t (1 + tanh(sqrt(2 / pi) (t + 0.044715 t^3))) / 2 */
+
+/* A product with a weight. */
+typedef struct dllm_linear_layer {
+  int32_t in_features;  /* K: a multiple of 8 */
+  int32_t out_features; /* N: columns of y */
+  int32_t act;          /* DLLM_ACT_* */
+  int32_t gated;        /* 0, or 1: w has 2 N rows, row 2j gate j and row 2j + 1 up j (as w_gate_up) */
+  float rms_eps;        /* RMSNorm epsilon, where the call has a gain */
+} dllm_linear_layer;
+
+/* y = act(t) + r, or (gated) act(t_gate) * t_up + r, with t = x^ W^T + b and
+ *   x^ = x, or with a gain RMSNorm(x) (correctly rounded to bf16).
+ * Products are summed in fp32 by the tensor core over all of K (or over equal
+ * parts of K, whose sums are added in their order); bias, activation, gate and
+ * residual are fp32, and y is rounded to bf16 once.  The same call gives the
+ * same bits; how K is cut depends on the sizes and the number of SMs alone.
+ *   x:        device bf16 [rows][in_features], rows x_stride elements apart;
+ *             16-byte aligned, the stride a multiple of 8 and >= in_features.
+ *   rms_gain: device bf16 [in_features], 16-byte aligned, nullable (no norm).
+ *   w:        device bf16 [out_features, or 2 out_features][in_features], 16-byte aligned.
+ *   bias:     device bf16, one for each row of w; nullable.
+ *   residual: device bf16 [rows][out_features], rows residual_stride elements
+ *             apart; nullable.  It may be y itself (the same pointer and stride).
+ *   y:        device bf16 [rows][out_features], rows y_stride >= out_features
+ *             elements apart; it overlaps nothing else that the call reads.
+ *             (Rows on 16-byte boundaries, y's and the residual's, are the
+ *             faster ones.)
+ *   error_flag: device int32, nullable: DLLM_DEVERR_TIMEOUT is ORed in.
+ *   ws: dllm_linear_workspace_size bytes (the x^ rows; 0 without a gain),
+ *   256-byte aligned scratch.  Calls that may run at the same time need
+ *   workspaces of their own. */
+dllm_status dllm_linear_workspace_size(const dllm_linear_layer* layer, int32_t rows, int32_t normed, size_t* bytes);
+dllm_status dllm_linear(const dllm_linear_layer* layer, int32_t rows, const void* x, int64_t x_stride,
+                        const void* rms_gain, const void* w, const void* bias, const void* residual,
+                        int64_t residual_stride, void* y, int64_t y_stride, int32_t* error_flag, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* Which elements of a head turn together, of the rotary_dim first. */
+#define DLLM_ROPE_HALVES 0     /* i and i + rotary_dim / 2, as everywhere else in this library */
+#define DLLM_ROPE_NEIGHBOURS 1 /* 2i and 2i + 1 */
+
+/* Packed rows of heads: row j, head h at j * row_stride + h * head_stride
+ * elements, head_dim contiguous; 16-byte aligned, strides multiples of 8 and
+ * not negative.  `out` may be `in` itself (with the same strides) or overlaps
+ * nothing that the call reads; its heads do not overlap each other. */
+typedef struct dllm_head_rows {
+  const void* in;  /* device bf16 */
+  int64_t in_row_stride;
+  int64_t in_head_stride;
+  void* out;       /* device bf16 */
+  int64_t out_row_stride;
+  int64_t out_head_stride;
+  const void* gain; /* device bf16 [head_dim], 16-byte aligned; NULL: no norm */
+  int32_t n_heads;
+} dllm_head_rows;
+
+/* The norm of each head and the rotation by position, in one pass over packed
+ * rows of queries and keys:
+ *   u = x / sqrt(mean(x^2) + rms_eps) * gain   (u = x without a gain)
+ *   the pair (u_a, u_b) number i of the first rotary_dim elements becomes
+ *   (u_a cos - u_b sin, u_a sin + u_b cos), cos and sin those of the row's
+ *   position and i in rope_table; the elements behind rotary_dim stay u.
+ * All of it in fp32, rounded to bf16 once.  Row j has position row_pos[j] (as
+ * dllm_batch_plan writes it); rows with -1 are left as they are.  A position
+ * below -1 or not below rope_max_pos sets DLLM_DEVERR_BAD_SHAPE, and its row
+ * is left as it is.
+ *   queries: n_heads == desc->n_heads; keys: any number of heads, nullable
+ *   (no keys).  rotary_dim: 64 or 128, at most head_dim.
+ *   rope_table: device fp32 [rope_max_pos][rotary_dim / 2][2], 16-byte aligned
+ *   (dllm_rope_table_build of a layer whose head_dim is rotary_dim).
+ *   row_pos: device int32 [rows].  error_flag: device int32, nullable. */
+dllm_status dllm_head_norm_rope(const dllm_layer_desc* desc, int32_t rows, const int32_t* row_pos,
+                                const dllm_head_rows* queries, const dllm_head_rows* keys, const float* rope_table,
+                                int32_t rope_max_pos, int32_t rotary_dim, int32_t pairs, int32_t* error_flag,
+                                void* stream);
+
+#define DLLM_TYPE_BF16 0
+#define DLLM_TYPE_FP32 1
+
+/* What a sampler reads off each row of logits, in one pass: with
+ * p = softmax(scale * logits[j]) over the vocabulary,
+ *   lse[j]      = log sum_v exp(scale * logits[j][v]),
+ *   entropy[j]  = -sum_v p_v log p_v,
+ *   logp[j]     = log p of tokens[j]; 0 where tokens[j] is negative,
+ *   top_ids[j], top_logp[j] [top_k] = the tokens of the largest logits and
+ *   their log p, largest first, of equal logits the lowest token first.
+ * A logit of -inf is a token that cannot be: it is no alternative, and where
+ * fewer than top_k tokens remain the ids are -1 and the log p -inf.  A row in
+ * which none remains has lse -inf, entropy 0, logp -inf.  Any finite logit,
+ * the type's lowest included, counts as it is.  A row that holds a NaN or +inf
+ * has NaN in lse, entropy, logp (also without a given token) and top_logp and
+ * -1 in top_ids, and sets DLLM_DEVERR_RANGE; tokens[j] >= vocab sets
+ * DLLM_DEVERR_BAD_SHAPE and makes logp[j] NaN.
+ *   logits: device bf16 or fp32 (logits_type) [rows][vocab], rows row_stride
+ *   >= vocab elements apart, at any element's alignment.
+ *   scale: the inverse temperature, positive and finite.
+ *   tokens: device int32 [rows]; logp: device fp32 [rows]; both nullable together.
+ *   lse, entropy: device fp32 [rows], each nullable.
+ *   top_k: 0 to 32; top_ids: device int32 [rows][top_k], top_logp: device fp32
+ *   [rows][top_k] (not read or written for top_k 0).
+ * Sums and statistics are fp32, relative to the row's largest logit; the same
+ * call gives the same bits. */
+dllm_status dllm_token_scores(int32_t rows, int32_t vocab, const void* logits, int32_t logits_type, int64_t row_stride,
+                              float scale, const int32_t* tokens, float* logp, float* lse, float* entropy,
+                              int32_t top_k, int32_t* top_ids, float* top_logp, int32_t* error_flag, void* stream);
+
 /* Static description of a status code (never NULL). */
 const char* dllm_status_string(dllm_status status);
 

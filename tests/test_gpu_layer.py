@@ -1,0 +1,383 @@
+"""A layer's products, the norm and rotation of its heads, and token scores on the GPU, each against a plain 64-bit
+implementation (tests/layer_util.py), and a run of them together with the 8-bit cache."""
+import math
+
+import pytest
+import torch
+
+import layer_util as lu
+from block_wise_kv_gb300 import dllm
+from kv8_util import Batch, attention, ints, random_pools
+
+pytestmark = pytest.mark.gpu
+ACT = {"none": dllm.DLLM_ACT_NONE, "silu": dllm.DLLM_ACT_SILU, "gelu": dllm.DLLM_ACT_GELU,
+       "gelu_tanh": dllm.DLLM_ACT_GELU_TANH}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from block_wise_kv_gb300 import build
+
+    build.build()
+    dllm.load()
+    torch.cuda.init()
+
+
+# ------------------------------------------------------------------ products with a weight
+class Linear:
+    def __init__(self, m, k, n, name="none", gated=False, norm=False, bias=False, residual=False, pad=0, seed=0, size=1.0):
+        wide = 2 * n if gated else n
+        self.m, self.n, self.name, self.gated = m, n, name, gated
+        self.x = lu.randn((m, k + 8 * pad), seed, size)[:, :k]
+        self.w = lu.randn((wide, k), seed + 1, 1.0 / math.sqrt(k))
+        self.gain = (1 + lu.randn((k,), seed + 2, 0.2).float()).bfloat16() if norm else None
+        self.bias = lu.randn((wide,), seed + 3) if bias else None
+        self.residual = lu.randn((m, n + pad), seed + 4)[:, :n] if residual else None
+        self.whole = torch.full((m, n + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+        self.y = self.whole[:, :n]
+        self.desc = dllm.linear_desc(k, n, ACT[name], gated, 1e-5)
+        self.ws = dllm.workspace(dllm.dllm_linear_workspace_size(self.desc, m, norm)) if norm else None
+        self.error = ints([0])
+
+    def call(self, **kw):
+        dllm.dllm_linear(self.desc, self.x, self.w, self.y, **{**dict(
+            rms_gain=self.gain, bias=self.bias, residual=self.residual, ws=self.ws, error=self.error), **kw})
+
+    def check(self, y=None, residual=None):
+        y = self.y if y is None else y
+        want, off = lu.linear(self.x, self.w, self.gain, self.bias, self.residual if residual is None else residual,
+                              self.name, self.gated)
+        err = (y.double() - want).abs()
+        assert (err <= off).all(), (err.max().item(), (err / off).max().item())
+        assert self.error.item() == 0
+        assert (self.whole[:, self.n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("m", [1, 2, 15, 16, 17, 33, 64, 100, 128, 255, 256, 257, 513])
+@pytest.mark.parametrize("k,n", [(64, 128), (256, 768), (1000, 130)])
+def test_linear_rows(m, k, n):
+    c = Linear(m, k, n, residual=m % 2 == 0, bias=m % 3 == 0, seed=m)
+    c.call()
+    c.check()
+
+
+@pytest.mark.parametrize("k", [8, 16, 56, 72, 120, 136, 520, 4096, 12288])
+@pytest.mark.parametrize("n,m", [(1, 3), (127, 1), (129, 40), (200, 300)])
+def test_linear_sizes(k, n, m):
+    c = Linear(m, k, n, bias=True, residual=True, pad=1, seed=k + n)
+    c.call()
+    c.check()
+
+
+@pytest.mark.parametrize("name", lu.ACTS)
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("m,n", [(1, 64), (37, 100), (300, 333), (700, 1024)])
+def test_linear_epilogues(name, gated, m, n):
+    for bias, residual, norm in ((False, False, False), (True, True, False), (False, True, True), (True, False, True)):
+        c = Linear(m, 192, n, name, gated, norm, bias, residual, pad=3 if residual else 0, seed=n, size=2.0)
+        c.call()
+        c.check()
+
+
+def test_linear_large_arguments_of_the_activations():
+    for name in lu.ACTS:
+        c = Linear(70, 64, 96, name, seed=5, size=60.0)
+        c.call()
+        c.check()
+
+
+@pytest.mark.parametrize("m,k,n,gated", [(512, 1024, 3000, False), (2048, 512, 1536, True), (5000, 264, 520, False)])
+def test_linear_many_rows(m, k, n, gated):
+    c = Linear(m, k, n, "silu" if gated else "none", gated, norm=gated, residual=not gated, seed=m)
+    c.call()
+    c.check()
+
+
+def test_linear_values_that_are_not_finite_stay_in_their_row():
+    c = Linear(40, 128, 200, seed=3)
+    c.x[7, 5] = math.nan
+    c.x[9, 9] = math.inf
+    c.call()
+    assert torch.isnan(c.y[7]).all() and not torch.isfinite(c.y[9]).any()
+    keep = [i for i in range(40) if i not in (7, 9)]
+    want, off = lu.linear(c.x[keep], c.w)
+    assert ((c.y[keep].double() - want).abs() <= off).all()
+
+
+@pytest.mark.parametrize("m,n,pad", [(1, 640, 0), (96, 640, 8), (600, 640, 0), (600, 641, 2)])
+def test_linear_adds_to_the_residual_in_place(m, n, pad):
+    c = Linear(m, 256, n, residual=True, pad=pad, seed=m)
+    before = c.residual.clone()
+    whole = torch.full_like(c.whole, 7.0)
+    y = whole[:, :n]
+    y.copy_(before)
+    dllm.dllm_linear(c.desc, c.x, c.w, y, residual=y)
+    c.check(y, before)
+    assert (whole[:, n:] == 7.0).all()
+
+
+def test_linear_out_of_and_into_columns_of_one_buffer():
+    wide = lu.randn((50, 64 + 96 + 40), 1)
+    x, y = wide[:, :64], wide[:, 64:160]
+    w = lu.randn((96, 64), 2, 0.1)
+    want, off = lu.linear(x, w)
+    kept = wide[:, 160:].clone()
+    dllm.dllm_linear(dllm.linear_desc(64, 96), x, w, y)
+    assert ((y.double() - want).abs() <= off).all() and torch.equal(wide[:, 160:], kept)
+
+
+def test_linear_gives_the_same_bits_again_and_rows_do_not_see_each_other():
+    for m, k, n in ((3, 4096, 512), (64, 4096, 512), (300, 1024, 700), (1024, 2048, 512)):
+        c = Linear(m, k, n, "silu", norm=True, seed=m)
+        c.call()
+        first = c.y.clone()
+        c.x[m // 2 + 1:] = 0
+        c.call()
+        assert torch.equal(c.y[:m // 2 + 1], first[:m // 2 + 1])
+
+
+def test_linear_on_two_streams_and_captured():
+    cs = [Linear(48, 1024, 640, norm=True, residual=True, seed=s) for s in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, s in zip(cs, streams):
+            with torch.cuda.stream(s):
+                c.call()
+    torch.cuda.synchronize()
+    for c in cs:
+        c.check()
+    c = cs[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.call()
+    for seed in (11, 12):
+        c.x.copy_(lu.randn(c.x.shape, seed))
+        c.y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check()
+
+
+def test_linear_sees_what_the_kernel_before_it_wrote():
+    """Weights, rows and residual written by the kernel directly in front, and rows read by the one behind, over and over."""
+    c = Linear(64, 2048, 1024, residual=True, seed=1)
+    ws = [c.w.clone(), lu.randn(c.w.shape, 9, 0.02)]
+    xs = [c.x.clone(), lu.randn(c.x.shape, 8)]
+    want = []
+    for w, x in zip(ws, xs):
+        c.w.copy_(w)
+        c.x.copy_(x)
+        torch.cuda.synchronize()
+        c.call()
+        want.append(c.y.clone())
+    for i in range(40):
+        c.x.copy_(xs[i % 2])
+        c.w.copy_(ws[i % 2])
+        c.call()
+        got = c.y.clone()
+        assert torch.equal(got, want[i % 2])
+
+
+# ------------------------------------------------------------------ head norms and rotation
+def _heads(m, h, d, seed, layout):
+    if layout == "rows":
+        return lu.randn((m, h, d), seed)
+    if layout == "wide":  # heads out of a wider row
+        return lu.randn((m, h + 5, d), seed)[:, 2:2 + h]
+    return lu.randn((h, m, d), seed).transpose(0, 1)  # rows within heads
+
+
+@pytest.mark.parametrize("d,rotary", [(128, 128), (128, 64), (64, 64)])
+@pytest.mark.parametrize("neighbours", [False, True])
+@pytest.mark.parametrize("m,h,kv,layout", [(1, 2, 2, "rows"), (7, 8, 1, "wide"), (33, 6, 3, "heads"), (130, 32, 8, "wide"),
+                                           (1000, 4, 4, "rows")])
+def test_head_norm_rope(d, rotary, neighbours, m, h, kv, layout):
+    q, k = _heads(m, h, d, 1, layout), _heads(m, kv, d, 2, layout)
+    table = lu.rope_table(777, rotary)
+    pos = torch.randint(777, (m,), device="cuda", dtype=torch.int32, generator=torch.Generator("cuda").manual_seed(m))
+    desc = dllm.layer_desc(max(64, h * d), h, d, 1e4, 1e-6)
+    pairs = dllm.DLLM_ROPE_NEIGHBOURS if neighbours else dllm.DLLM_ROPE_HALVES
+    gains = [lu.randn((d,), 3, 0.5), lu.randn((d,), 4, 0.5)]
+    for qg, kg in ((gains[0], gains[1]), (None, None), (None, gains[1])):
+        error = ints([0])
+        qo, ko = torch.zeros_like(q), torch.zeros(m, kv, d, dtype=torch.bfloat16, device="cuda")
+        dllm.dllm_head_norm_rope(desc, q, qo, k, ko, pos, table, qg, kg, pairs, error)
+        for x, g, out in ((q, qg, qo), (k, kg, ko)):
+            want, off = lu.head_norm_rope(x, g, pos, table, rotary, neighbours, 1e-6)
+            err = (out.double() - want).abs()
+            assert (err <= off).all(), (err / off).max().item()
+        q2, k2 = q.clone(memory_format=torch.preserve_format), k.clone()
+        dllm.dllm_head_norm_rope(desc, q2, q2, k2, k2, pos, table, qg, kg, pairs, error)  # in place
+        assert torch.equal(q2, qo) and torch.equal(k2, ko) and error.item() == 0
+        qo2 = torch.zeros_like(q)
+        dllm.dllm_head_norm_rope(desc, q, qo2, None, None, pos, table, qg, None, pairs, error)  # queries alone
+        assert torch.equal(qo2, qo)
+
+
+def test_head_norm_rope_leaves_rows_without_a_position():
+    m, h, kv, d = 50, 4, 2, 128
+    q, k = lu.randn((m, h, d), 1), lu.randn((m, kv, d), 2)
+    table = lu.rope_table(64, d)
+    pos = [i % 64 if i % 3 else -1 for i in range(m)]
+    pos[10], pos[20], pos[40] = 64, -2, 1 << 30
+    desc = dllm.layer_desc(h * d, h, d, 1e4)
+    for bad in (True, False):
+        p = ints(pos if bad else [x if -1 <= x < 64 else -1 for x in pos])
+        error, qo, ko = ints([0]), torch.full_like(q, 3.0), torch.full_like(k, 3.0)
+        dllm.dllm_head_norm_rope(desc, q, qo, k, ko, p, table, error=error)
+        assert error.item() == (dllm.DLLM_DEVERR_BAD_SHAPE if bad else 0)
+        for i, x in enumerate(pos):
+            there = 0 <= x < 64
+            assert there or ((qo[i] == 3.0).all() and (ko[i] == 3.0).all())
+            assert not there or not (qo[i] == 3.0).all()
+
+
+def test_head_norm_rope_rows_of_zeros_large_and_not_finite_values():
+    d = 128
+    q = lu.randn((6, 2, d), 1)
+    q[0] = 0
+    q[1] *= 1e4
+    q[2] *= 1e-4
+    q[3, 0, 5] = math.nan
+    q[4, 1, 100] = math.inf
+    gain, table, pos = lu.randn((d,), 2), lu.rope_table(10, 64), ints([0, 1, 2, 3, 4, 5])
+    out = torch.zeros_like(q)
+    desc = dllm.layer_desc(2 * d, 2, d, 1e4, 1e-6)
+    dllm.dllm_head_norm_rope(desc, q, out, None, None, pos, table, gain)
+    want, off = lu.head_norm_rope(q, gain, pos, table, 64, False, 1e-6)
+    fine = [(0, 0), (0, 1), (1, 0), (1, 1), (2, 0), (2, 1), (3, 1), (4, 0), (5, 0), (5, 1)]
+    for i, h in fine:
+        assert ((out[i, h].double() - want[i, h]).abs() <= off[i, h]).all()
+    assert torch.isnan(out[3, 0]).all() and not torch.isfinite(out[4, 1]).all()
+    dllm.dllm_head_norm_rope(desc, q, out, None, None, pos, table)  # without a norm: elements behind the rotation as they are
+    assert torch.equal(out[4, :, 64:], q[4, :, 64:]) and torch.equal(out[0], q[0])
+
+
+# ------------------------------------------------------------------ token scores
+def _scores(x, tokens, top, scale, some=True):
+    m = x.shape[0]
+    error = ints([0])
+    f = lambda *s: torch.full(s, 9.0, device="cuda")  # noqa: E731
+    lse, entropy, logp = f(m), f(m), f(m)
+    ids = torch.full((m, top), -9, dtype=torch.int32, device="cuda") if top else None
+    best = f(m, top) if top else None
+    dllm.dllm_token_scores(x, tokens, logp, lse, entropy, ids, best, scale, error)
+    return (lse, entropy, logp, ids, best), error.item()
+
+
+def _tokens(m, v, seed=0):
+    return torch.randint(-1, v, (m,), device="cuda", dtype=torch.int32, generator=torch.Generator("cuda").manual_seed(seed))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,v,pad", [(1, 1, 0), (3, 2, 1), (5, 7, 0), (4, 64, 3), (17, 1000, 1), (2, 4099, 0), (400, 515, 2),
+                                     (1, 126464, 0), (2, 126464, 8), (9, 50001, 7), (40, 126464, 0), (700, 8200, 5)])
+def test_token_scores(dtype, m, v, pad):
+    x = lu.randn((m, v + pad), m + v, 3.0, dtype)[:, :v]
+    for top in (0, 1, 2, 20, 32):
+        tokens = _tokens(m, v, top)
+        got, bits = _scores(x, tokens, top, 1.0)
+        assert bits == 0
+        lu.assert_scores(got, x, tokens, top, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale", [0.25, 1.5, 40.0])
+def test_token_scores_at_a_temperature(dtype, scale):
+    x = lu.randn((20, 3001), 1, 4.0, dtype)
+    tokens = _tokens(20, 3001)
+    got, bits = _scores(x, tokens, 5, scale)
+    assert bits == 0
+    lu.assert_scores(got, x, tokens, 5, scale)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("v", [130, 9000, 126464])
+def test_token_scores_under_masks(dtype, v):
+    """-inf, the type's lowest value, next to nothing left, nothing left, and rows of one value."""
+    lowest = torch.finfo(dtype).min
+    x = lu.randn((13, v), v, 3.0, dtype)
+    u = torch.rand(x.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    x[0].masked_fill_(u[0] < 0.9, -math.inf)
+    x[1].masked_fill_(u[1] < 0.9, lowest)
+    x[2] = -math.inf
+    x[3] = lowest
+    x[4] = -math.inf
+    x[4, v - 1] = 2.0
+    x[5] = -math.inf
+    x[5, [0, 7, v // 2]] = lowest
+    x[6] = lowest
+    x[6, v // 3] = -5.0
+    x[7] = 0.0
+    x[8] = -0.0
+    x[8, ::2] = 0.0
+    x[9] = -1e30
+    x[10] = torch.linspace(-20, 20, v, device="cuda")
+    x[11] = torch.linspace(20, -20, v, device="cuda")
+    tokens = _tokens(13, v)
+    tokens[6] = v // 3
+    for top in (1, 20, 32):
+        got, bits = _scores(x, tokens, top, 1.0)
+        assert bits == 0
+        lu.assert_scores(got, x, tokens, top, 1.0)
+
+
+@pytest.mark.parametrize("dtype,step", [(torch.bfloat16, 1), (torch.float32, 1), (torch.bfloat16, 8), (torch.float32, 4)])
+def test_token_scores_with_the_largest_anywhere(dtype, step):
+    """The largest values side by side, in every n-th place for many n (all of them one thread's, for some), and equal."""
+    v = 40000
+    places = [1, 8, 64, 128, 256, 512, 1024, 2048, 4096, 8192, 16384]
+    x = lu.randn((2 * len(places), v), 3, 1.0, dtype)
+    for i, n in enumerate(places):
+        at = (torch.arange(40000 // max(n, 100), device="cuda") * n + 3 * step) % v
+        x[2 * i, at] = 30.0 + (torch.arange(at.numel(), device="cuda") % 50).to(dtype)
+        x[2 * i + 1, at] = 30.0
+    tokens = _tokens(x.shape[0], v)
+    for top in (1, 5, 32):
+        got, bits = _scores(x, tokens, top, 1.0)
+        assert bits == 0
+        lu.assert_scores(got, x, tokens, top, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,v", [(6, 1003), (6, 126464), (900, 2000)])
+def test_token_scores_of_rows_that_are_not_numbers(dtype, m, v):
+    x = lu.randn((m, v), 1, 3.0, dtype)
+    x[1, v // 2] = math.nan
+    x[2, v - 1] = math.inf
+    x[3, 0] = math.nan
+    x[3, 1:] = -math.inf
+    tokens = _tokens(m, v)
+    tokens[1] = -1
+    tokens[4] = v
+    tokens[5] = v - 1
+    (lse, entropy, logp, ids, best), bits = _scores(x, tokens, 4, 1.0)
+    assert bits == dllm.DLLM_DEVERR_RANGE | dllm.DLLM_DEVERR_BAD_SHAPE
+    for t in (lse, entropy, logp, best):
+        assert torch.isnan(t[1:4]).all()
+    assert (ids[1:4] == -1).all() and torch.isnan(logp[4]) and torch.isfinite(lse[4])
+    keep = [0] + list(range(5, m))
+    lu.assert_scores([t[keep] for t in (lse, entropy, logp, ids, best)], x[keep], tokens[keep], 4, 1.0)
+
+
+def test_token_scores_some_outputs_alone():
+    x, tokens = lu.randn((8, 5000), 1, 3.0), _tokens(8, 5000)
+    (lse, entropy, logp, ids, best), _ = _scores(x, tokens, 3, 1.0)
+    a, b, c, i, t = (torch.zeros_like(y) for y in (lse, entropy, logp, ids, best))
+    dllm.dllm_token_scores(x, lse=a)
+    dllm.dllm_token_scores(x, entropy=b)
+    dllm.dllm_token_scores(x, tokens, c)
+    dllm.dllm_token_scores(x, top_ids=i, top_logp=t)
+    for got, want in ((a, lse), (b, entropy), (c, logp), (i, ids), (t, best)):
+        assert torch.equal(got, want)
+
+
+def test_token_scores_rows_beyond_32_bits_of_elements():
+    v, m = 126464, 17200  # 2.18 G elements
+    x = torch.zeros(m, v, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = lu.randn((3, v), 1, 3.0)
+    tokens = _tokens(m, v)
+    got, bits = _scores(x, tokens, 3, 1.0)
+    assert bits == 0
+    lu.assert_scores([t[-5:] for t in got], x[-5:], tokens[-5:], 3, 1.0)
