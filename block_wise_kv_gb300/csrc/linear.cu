@@ -58,8 +58,8 @@ __global__ void __launch_bounds__(kNormThreads) linear_norm_kernel(const LinearA
   __shared__ float2 part[kNormThreads / 32];
   __shared__ float2 scale;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nvec = a.k / 8;
+  griddep_launch_dependents();  // the product behind reads nothing before its own wait
   griddep_wait();
-  griddep_launch_dependents();
   const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + blockIdx.x * a.x_stride);
   uint4* out = static_cast<uint4*>(a.xhat) + static_cast<size_t>(blockIdx.x) * nvec;
   const uint4* g = static_cast<const uint4*>(a.gain);
@@ -98,7 +98,7 @@ __device__ __forceinline__ float bf16_at(const void* p, int64_t i) {
 }
 
 // ------------------------------------------------------------ few rows
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kBK = 64;
 constexpr int kTW = 128;                 // rows of W to a tile (tcgen05 M)
 constexpr int kABytes = kTW * kBK * 2;
@@ -110,46 +110,143 @@ struct RowsPlan {
   int split;      // CTAs that share a tile's K
   int stages;     // of the ring
   int boxes;      // of K
+  int norm;       // the normed x of this CTA's part of K is made here: where in shared memory, or 0
   int per_rank;   // groups of 4 rows of x that each CTA of a cluster finishes
+  int join;       // where in shared memory the parts of a tile meet: behind the ring, or 0, in the ring when that is done with
+  int smem;       // dynamic shared memory
   uint32_t cols;  // TMEM columns
   int xt;         // tiles of x
 };
 
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
-  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x),
-               "r"(y)
-               : "memory");
+// A bounded wait without the timer that mbar_wait reads: each try sleeps for up to 20 us, two seconds in all at most.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 100000; ++i)
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+  return false;
 }
 
-// y of four rows of x (x0 + c ...) under this thread's row of W, whose sums are v.
-template <int ACT, bool GATED>
-__device__ __forceinline__ void finish4(const LinearArgs& a, const float (&v)[4], float b, int wr, int row, int lane) {
-  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y);
-  if (GATED) {
-    // the even lane has the gate of four rows, the odd one the up: each makes y of two of them
-    const bool up = lane & 1;
-    const int n = wr >> 1;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float mine = (up ? v[2 + i] : v[i]) + b, give = (up ? v[i] : v[2 + i]) + b;
-      const float other = __shfl_xor_sync(0xffffffffu, give, 1);
-      const float g = up ? other : mine, u = up ? mine : other;
-      const int64_t r = row + (up ? 2 : 0) + i;
-      if (wr < a.wide && r < a.rows) {
-        float o = activate<ACT>(g) * u;
-        if (a.residual != nullptr) o += bf16_at(a.residual, r * a.r_stride + n);
-        y[r * a.y_stride + n] = __float2bfloat16_rn(o);
-      }
+// A place in a ring and the parity of its present use, stepped without divisions: a division by the number of stages costs
+// the one thread that issues the loads about as much as the load (an SM's loads then came at 51 GB/s, not at 100).
+struct Ring {
+  int s = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      parity ^= 1;
     }
-  } else {
+  }
+};
+
+// 16 bytes to a place in the shared memory of a CTA of the cluster, counted by the barrier there.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, float x, float y, float z, float w, uint32_t bar) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr), "f"(x),
+      "f"(y), "f"(z), "f"(w), "r"(bar)
+      : "memory");
+}
+
+// Sixteen rows of x (row, row + 1, ...) under this thread's row of W: what is added to y, asked for ahead, and y from
+// the sums v.  Gated, the even lane has the gate of the sixteen and the odd one the up: each makes y of eight.
+template <bool GATED>
+struct Finish {
+  static constexpr int kOut = GATED ? 8 : 16;
+  __nv_bfloat16 r[kOut];
+
+  static __device__ __forceinline__ int64_t row_of(int row, int i, int lane) { return row + (GATED ? (lane & 1) * 8 : 0) + i; }
+
+  __device__ __forceinline__ void ask(const LinearArgs& a, int wr, int row, int lane) {
+    const int n = GATED ? wr >> 1 : wr;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = row + i;
-      if (wr < a.wide && r < a.rows) {
-        float o = activate<ACT>(v[i] + b);
-        if (a.residual != nullptr) o += bf16_at(a.residual, r * a.r_stride + wr);
-        y[r * a.y_stride + wr] = __float2bfloat16_rn(o);
+    for (int i = 0; i < kOut; ++i) {
+      const int64_t j = row_of(row, i, lane);
+      r[i] = __float2bfloat16_rn(0.f);
+      if (a.residual != nullptr && wr < a.wide && j < a.rows)
+        r[i] = static_cast<const __nv_bfloat16*>(a.residual)[j * a.r_stride + n];
+    }
+  }
+
+  template <int ACT>
+  __device__ __forceinline__ void make(const LinearArgs& a, const float (&v)[16], float b, int wr, int row, int lane,
+                                       int end = 0x7fffffff) {
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y);
+    const bool up = lane & 1;
+    const int n = GATED ? wr >> 1 : wr;
+#pragma unroll
+    for (int i = 0; i < kOut; ++i) {
+      float o;
+      if (GATED) {
+        const float mine = (up ? v[8 + i] : v[i]) + b, give = (up ? v[i] : v[8 + i]) + b;
+        const float other = __shfl_xor_sync(0xffffffffu, give, 1);
+        o = activate<ACT>(up ? other : mine) * (up ? mine : other);
+      } else {
+        o = activate<ACT>(v[i] + b);
       }
+      const int64_t j = row_of(row, i, lane);
+      if (wr < a.wide && j < a.rows && j < end) y[j * a.y_stride + n] = __float2bfloat16_rn(o + __bfloat162float(r[i]));
+    }
+  }
+};
+
+// Threads that norm a row inside the product: four pieces of 8 elements each (fewer: a piece's eight exact squares are a
+// chain of eight sums).
+constexpr int kNormPieces = 4;
+__host__ __device__ inline int norm_lanes(int k) {
+  int t = 8;
+  while (t * kNormPieces * 8 < k) t *= 2;
+  return t;
+}
+constexpr int kNormMaxLanes = 128;
+
+// Four warps (tid: 0 to 127): columns [64 kb0, 64 (kb0 + nb)) of RMSNorm(x) of the rows from x0 on, as the boxes that the
+// MMAs take (rows of 128 bytes, swizzled).  `boxes` is zero where no row or column is.
+__device__ __forceinline__ void norm_rows(const LinearArgs& a, uint8_t* boxes, float2* part, int x0, int bn, int kb0, int nb,
+                                          int tid) {
+  const int nvec = a.k / 8, lanes = norm_lanes(a.k), sub = tid / lanes, l = tid % lanes;
+  const uint4* g = static_cast<const uint4*>(a.gain);
+  const int rows = min(bn, a.rows - x0);
+  for (int r0 = 0; r0 < rows; r0 += kNormMaxLanes / lanes) {
+    const int row = r0 + sub;
+    const bool there = row < rows;
+    const uint4* x =
+        reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (x0 + (there ? row : 0)) * a.x_stride);
+    uint4 u[kNormPieces], w[kNormPieces];
+#pragma unroll
+    for (int i = 0; i < kNormPieces; ++i) {
+      const int v = l + i * lanes;
+      u[i] = w[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (v < nvec) u[i] = __ldg(x + v);
+      if (v >= kb0 * 8 && v < (kb0 + nb) * 8 && v < nvec) w[i] = __ldg(g + v);
+    }
+    float hi = 0.f, lo = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNormPieces; ++i) sumsq_pair_add(u[i], hi, lo);
+    for (int o = 1; o < lanes && o < 32; o <<= 1) {
+      const float oh = __shfl_xor_sync(0xffffffffu, hi, o), ol = __shfl_xor_sync(0xffffffffu, lo, o);
+      // (the same order in both lanes: the pair sum is not commutative in its last bits)
+      float h = (tid & o) ? oh : hi, s = (tid & o) ? ol : lo;
+      pair_add(h, s, (tid & o) ? hi : oh, (tid & o) ? lo : ol);
+      hi = h;
+      lo = s;
+    }
+    if (lanes > 32) {
+      if ((tid & 31) == 0) part[tid >> 5] = make_float2(hi, lo);
+      named_barrier(1, 128);
+      const int w0 = sub * (lanes / 32);
+      hi = part[w0].x;
+      lo = part[w0].y;
+      for (int i = 1; i < lanes / 32; ++i) pair_add(hi, lo, part[w0 + i].x, part[w0 + i].y);
+      named_barrier(1, 128);
+    }
+    two_sum(hi, lo, hi, lo);
+    float s_hi, s_lo;
+    rsqrt_pair(hi, lo, a.k, a.rms_eps, s_hi, s_lo);
+#pragma unroll
+    for (int i = 0; i < kNormPieces; ++i) {
+      const int v = l + i * lanes, c = v - kb0 * 8;
+      if (there && c >= 0 && c < nb * 8 && v < nvec)
+        *reinterpret_cast<uint4*>(boxes + (c >> 3) * bn * 128 + sw128_offset(row, c & 7)) = normed8(u[i], w[i], s_hi, s_lo);
     }
   }
 }
@@ -161,14 +258,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
-  __shared__ uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar;
+  __shared__ uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar, join_bar, norm_bar;
   __shared__ uint32_t tmem_base_sh;
+  __shared__ float2 norm_part[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int stage_bytes = kABytes + t.bn * kBK * 2;
+  const int x_box = t.bn * kBK * 2, stage_bytes = kABytes + (t.norm ? 0 : x_box);
   const int rank = static_cast<int>(blockIdx.x) % t.split, tile = static_cast<int>(blockIdx.x) / t.split;
   const int w0 = tile / t.xt * kTW, x0 = tile % t.xt * t.bn;  // tiles that share rows of W side by side
   const int kb0 = static_cast<int>(static_cast<int64_t>(t.boxes) * rank / t.split);
   const int nb = static_cast<int>(static_cast<int64_t>(t.boxes) * (rank + 1) / t.split) - kb0;
+  const int groups = t.split > 1 ? min(t.per_rank, t.bn / 4 - rank * t.per_rank) : 0;  // that this CTA finishes, of 4 rows of x
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < t.stages; ++s) {
@@ -176,7 +275,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&empty_bar[s], 1);
     }
     mbar_init(&done_bar, 1);
+    mbar_init(&join_bar, 1);
+    mbar_init(&norm_bar, 4);
     fence_barrier_init();
+    if (groups > 0) mbar_arrive_expect_tx(&join_bar, t.split * groups * kTW * 16);
     tma_prefetch_desc(&tm_w);
     tma_prefetch_desc(&tm_x);
   }
@@ -184,120 +286,135 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (t.split > 1 && t.join > 0) cluster_arrive_release();  // this CTA's barrier and buffer are there
   const uint32_t tmem = tmem_base_sh;
   const int quad = warp & 3;
   const int wr = w0 + quad * 32 + lane;  // warps 2-5: this thread's row of W
   float b = 0.f;
+  Finish<GATED> fin;
+  const int first = t.split > 1 ? rank * t.per_rank * 4 : 0;  // the first row of x that this CTA finishes
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp == 0 || warp == 6) {
+    // Warp 0 loads W, warp 6 x: a thread is done with a load only after about 100 ns.
+    if (lane == 0 && (warp == 0 || t.norm == 0)) {
+      const bool is_w = warp == 0;
+      const CUtensorMap* map = is_w ? &tm_w : &tm_x;
+      const int y0 = is_w ? w0 : x0;
+      uint8_t* dst = smem + (is_w ? 0 : kABytes);
       bool ok = true;
-      const int early = nb < t.stages ? nb : t.stages;
-      // What stands in front may still be writing W, but where that is the norm kernel, which starts this one only
-      // behind its own wait.  Elsewhere the first boxes of W go as far as L2.
-      if (a.gain != nullptr) {
-        for (int i = 0; i < early; ++i) {
-          mbar_arrive_expect_tx(&full_bar[i], stage_bytes);
-          tma_load_2d(smem + i * stage_bytes, &tm_w, &full_bar[i], (kb0 + i) * kBK, w0);
-        }
-      } else {
-        for (int i = 0; i < early; ++i) tma_prefetch_2d(&tm_w, (kb0 + i) * kBK, w0);
-      }
       griddep_wait();
       griddep_launch_dependents();
+      Ring r;
       int i = 0;
-      for (; i < nb && ok; ++i) {
-        const int s = i % t.stages;
-        uint8_t* st = smem + s * stage_bytes;
-        if (i >= t.stages && !mbar_wait(&empty_bar[s], (i / t.stages - 1) & 1)) {
+      for (; i < nb; ++i, r.next(t.stages)) {
+        if (i >= t.stages && !wait_phase(&empty_bar[r.s], r.parity ^ 1)) {
           ok = false;
           break;
         }
-        if (i >= early || a.gain == nullptr) {
-          mbar_arrive_expect_tx(&full_bar[s], stage_bytes);
-          tma_load_2d(st, &tm_w, &full_bar[s], (kb0 + i) * kBK, w0);  // rows past W's, and x's, read 0
-        }
-        tma_load_2d(st + kABytes, &tm_x, &full_bar[s], (kb0 + i) * kBK, x0);
+        if (is_w) mbar_arrive_expect_tx(&full_bar[r.s], stage_bytes);
+        tma_load_2d(dst + r.s * stage_bytes, map, &full_bar[r.s], (kb0 + i) * kBK, y0);  // rows past the last read 0
       }
-      for (int j = i > t.stages ? i - t.stages : 0; j < i; ++j)  // every load has landed before the ring ends
-        ok = mbar_wait(&full_bar[j % t.stages], (j / t.stages) & 1) && ok;
+      // every load has landed before the ring ends: each place's last one
+      for (int j = 0; j < t.stages && j < i; ++j, r.next(t.stages))
+        ok = wait_phase(&full_bar[i < t.stages ? j : r.s], i < t.stages ? 0 : r.parity ^ 1) && ok;
       if (!ok) report_error(a.err, kErrTimeout);
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = umma_idesc_bf16(kTW, t.bn);
-      bool ok = true;
-      for (int i = 0; i < nb; ++i) {
-        const int s = i % t.stages;
-        ok = mbar_wait(&full_bar[s], (i / t.stages) & 1);
+      bool ok = t.norm == 0 || wait_phase(&norm_bar, 0);
+      Ring r;
+      for (int i = 0; i < nb && ok; ++i, r.next(t.stages)) {
+        ok = wait_phase(&full_bar[r.s], r.parity);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t sa = smem_u32(smem + s * stage_bytes), sb = sa + kABytes;
+        const uint32_t sa = smem_u32(smem) + r.s * stage_bytes;
+        const uint32_t sb = t.norm ? smem_u32(smem) + t.norm + i * x_box : sa + kABytes;
 #pragma unroll
         for (int kk = 0; kk < kBK / 16; ++kk)
           umma_bf16(tmem, umma_desc_sw128(sa + kk * 32), umma_desc_sw128(sb + kk * 32), idesc,
                     (i > 0 || kk > 0) ? 1u : 0u);
-        if (i + t.stages < nb) umma_commit(&empty_bar[s]);  // the last ones no load waits for
+        if (i + t.stages < nb) umma_commit(&empty_bar[r.s]);  // the last ones no load waits for
       }
       umma_commit(&done_bar);
       if (!ok) report_error(a.err, kErrTimeout);
     }
     __syncwarp();
   } else {
+    if (t.norm)
+      for (int i = threadIdx.x - 64; i < nb * x_box / 16; i += 128)
+        reinterpret_cast<uint4*>(smem + t.norm)[i] = make_uint4(0u, 0u, 0u, 0u);
     griddep_wait();  // bias, residual, and y behind whoever reads it
     b = wr < a.wide && a.bias != nullptr ? bf16_at(a.bias, wr) : 0.f;
-    if (!mbar_wait(&done_bar, 0)) report_error(a.err, kErrTimeout);
+    if (t.norm) {
+      named_barrier(1, 128);
+      norm_rows(a, smem + t.norm, norm_part, x0, t.bn, kb0, nb, threadIdx.x - 64);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&norm_bar);
+    }
+    fin.ask(a, wr, x0 + first, lane);
+    if (!wait_phase(&done_bar, 0)) report_error(a.err, kErrTimeout);
     tc_fence_after();
   }
   const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16);
   if (t.split == 1) {
-    if (warp >= 2) {
+    if (warp >= 2 && warp < 6) {
       for (int c0 = 0; c0 < t.bn && x0 + c0 < a.rows; c0 += 16) {
         float v[16];
         tmem_ld_32x32b_x16(src + c0, v);
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const float w[4] = {v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
-          finish4<ACT, GATED>(a, w, b, wr, x0 + c0 + 4 * g, lane);
-        }
+        fin.template make<ACT>(a, v, b, wr, x0 + c0, lane);
+        if (c0 + 16 < t.bn) fin.ask(a, wr, x0 + c0 + 16, lane);
       }
     }
   } else {
-    // The rings are done with on all sides; each CTA's sums of group g (four rows of x) go to the CTA that
-    // finishes it: [CTA they come from][group][row of W], 16 bytes each.
-    __syncthreads();
-    cluster_arrive_release();
+    // Each CTA's sums of group g (four rows of x) go to the CTA that finishes it: [CTA they come from][group][row of W],
+    // 16 bytes each, counted there.
+    if (t.join == 0) {  // into the rings, once they are done with on all sides
+      __syncthreads();
+      cluster_arrive_release();
+    }
     cluster_wait_acquire();
-    const uint32_t mine = smem_u32(smem) + (quad * 32 + lane) * 16;
-    if (warp >= 2) {
+    if (warp >= 2 && warp < 6) {
+      const uint32_t mine = smem_u32(smem) + t.join + (quad * 32 + lane) * 16;
+      int g = 0, to = 0;  // the group within those of CTA `to`
       for (int c0 = 0; c0 < t.bn; c0 += 16) {
         float v[16];
         tmem_ld_32x32b_x16(src + c0, v);
 #pragma unroll
-        for (int g4 = 0; g4 < 4; ++g4) {
-          const int g = c0 / 4 + g4, to = g / t.per_rank;
-          st_shared_cluster_v4(mapa_shared(mine + (rank * t.per_rank + g - to * t.per_rank) * (kTW * 16), to),
-                               make_float4(v[4 * g4], v[4 * g4 + 1], v[4 * g4 + 2], v[4 * g4 + 3]));
+        for (int i = 0; i < 4; ++i) {
+          const int there = min(t.per_rank, t.bn / 4 - to * t.per_rank);
+          st_async_v4(mapa_shared(mine + (rank * there + g) * (kTW * 16), to), v[4 * i], v[4 * i + 1], v[4 * i + 2],
+                      v[4 * i + 3], mapa_shared(smem_u32(&join_bar), to));
+          if (++g == there) {
+            g = 0;
+            ++to;
+          }
         }
       }
-    }
-    cluster_arrive_release();
-    cluster_wait_acquire();
-    if (warp >= 2) {
-      const float4* part = reinterpret_cast<const float4*>(smem) + quad * 32 + lane;
-      for (int g = 0; g < t.per_rank; ++g) {
-        const int c = (rank * t.per_rank + g) * 4;
-        if (c >= t.bn || x0 + c >= a.rows) break;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int r = 0; r < t.split; ++r) {
-          const float4 p = part[(r * t.per_rank + g) * kTW];
-          v[0] += p.x;
-          v[1] += p.y;
-          v[2] += p.z;
-          v[3] += p.w;
+      if (groups > 0) {
+        if (!wait_phase(&join_bar, 0)) report_error(a.err, kErrTimeout);
+        const float4* part = reinterpret_cast<const float4*>(smem + t.join) + quad * 32 + lane;
+        const int end = first + groups * 4;
+        for (int c0 = first, g0 = 0; c0 < end && x0 + c0 < a.rows; c0 += 16, g0 += 4) {
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = 0.f;
+          for (int r = 0; r < t.split; ++r) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (g0 + i >= groups) break;
+              const float4 p = part[(r * groups + g0 + i) * kTW];
+              v[4 * i] += p.x;
+              v[4 * i + 1] += p.y;
+              v[4 * i + 2] += p.z;
+              v[4 * i + 3] += p.w;
+            }
+          }
+          fin.template make<ACT>(a, v, b, wr, x0 + c0, lane, x0 + end);
+          if (c0 + 16 < end) fin.ask(a, wr, x0 + c0 + 16, lane);
         }
-        finish4<ACT, GATED>(a, v, b, wr, x0 + c, lane);
       }
     }
   }
@@ -323,6 +440,7 @@ struct TilesPlan {
   int boxes;   // of K
   int wt, xt;  // tiles of W, of x
   int pairs;   // CTA pairs
+  int band;    // tiles of x that are walked side by side
   bool y_vec, r_vec;  // rows of y, of the residual on 16-byte boundaries
 };
 
@@ -354,7 +472,7 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t addr) {
 }
 // As mbar_wait, behind arrivals from both CTAs.
 __device__ __forceinline__ bool mbar_wait_pair(uint64_t* bar, uint32_t parity) {
-  const bool ok = mbar_wait(bar, parity);
+  const bool ok = wait_phase(bar, parity);
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
   return ok;
 }
@@ -427,6 +545,15 @@ __device__ __forceinline__ void stage_to_y(const LinearArgs& a, bool vec, const 
   }
 }
 
+// Tiles in bands of t.band tiles of x (the last may be narrower); within a band tile of W by tile of W, so that those who
+// work side by side share tiles of both.
+__device__ __forceinline__ void tile_at(const TilesPlan& t, int tile, int& wt, int& xt) {
+  const int per = t.band * t.wt, b = tile / per, rest = tile - b * per;
+  const int width = min(t.band, t.xt - b * t.band);
+  wt = rest / width;
+  xt = b * t.band + rest % width;
+}
+
 template <int ACT, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_tiles_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
@@ -467,28 +594,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      griddep_wait();
-      griddep_launch_dependents();
+  if (warp == 0 || warp == 6) {
+    if (lane == 0) {  // (as above) warp 0 loads W, warp 6 x
+      const bool is_w = warp == 0;
       const int half_w = t.bn / 2;
       const uint32_t bytes = 2u * (kHalfBytes + half_w * kBK * 2);
+      const uint32_t full0 = mapa_shared(smem_u32(&full_bar[0]), 0);
+      const CUtensorMap* map = is_w ? &tm_w : &tm_x;
+      uint8_t* dst = smem + (is_w ? kHalfBytes : 0);
+      griddep_wait();
+      griddep_launch_dependents();
       bool ok = true;
+      Ring r;
       int q = 0;
       for (int i = 0; i < mine && ok; ++i) {
-        const int tile = pair + i * t.pairs;
-        const int w0 = tile % t.wt * t.bn + rank * half_w, x0 = tile / t.wt * kPairRows + rank * 128;
-        for (int kb = 0; kb < t.boxes; ++kb, ++q) {
-          const int s = q % kPairStages;
-          if (q >= kPairStages && !mbar_wait(&empty_bar[s], (q / kPairStages - 1) & 1)) {
+        int wt, xt;
+        tile_at(t, pair + i * t.pairs, wt, xt);
+        const int y0 = is_w ? wt * t.bn + rank * half_w : xt * kPairRows + rank * 128;
+        for (int kb = 0; kb < t.boxes; ++kb, ++q, r.next(kPairStages)) {
+          if (q >= kPairStages && !wait_phase(&empty_bar[r.s], r.parity ^ 1)) {
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&full_bar[s], bytes);
-          const uint32_t bar = mapa_shared(smem_u32(&full_bar[s]), 0);
-          uint8_t* st = smem + s * kPairStage;
-          tma_load_2d_pair(st, &tm_x, bar, kb * kBK, x0);  // rows past x's, and W's, read 0
-          tma_load_2d_pair(st + kHalfBytes, &tm_w, bar, kb * kBK, w0);
+          if (is_w && rank == 0) mbar_arrive_expect_tx(&full_bar[r.s], bytes);
+          tma_load_2d_pair(dst + r.s * kPairStage, map, full0 + r.s * 8, kb * kBK, y0);  // rows past the last read 0
         }
       }
       if (!ok) report_error(a.err, kErrTimeout);
@@ -499,6 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t idesc = umma_idesc_bf16(256, t.bn);
       const int total = mine * t.boxes;
       bool ok = true;
+      Ring r;
       int q = 0;
       for (int i = 0; i < mine && ok; ++i) {
         const int buf = i & 1;
@@ -508,19 +638,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + buf * 256;
-        for (int kb = 0; kb < t.boxes; ++kb, ++q) {
-          const int s = q % kPairStages;
-          if (!mbar_wait(&full_bar[s], (q / kPairStages) & 1)) {
+        for (int kb = 0; kb < t.boxes; ++kb, ++q, r.next(kPairStages)) {
+          if (!wait_phase(&full_bar[r.s], r.parity)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * kPairStage), sb = sa + kHalfBytes;
+          const uint32_t sa = smem_u32(smem) + r.s * kPairStage, sb = sa + kHalfBytes;
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
             umma_bf16_pair(d, umma_desc_sw128(sa + kk * 32), umma_desc_sw128(sb + kk * 32), idesc,
                            (kb > 0 || kk > 0) ? 1u : 0u);
-          if (q + kPairStages < total) umma_commit_pair(&empty_bar[s]);  // the last ones no load waits for
+          if (q + kPairStages < total) umma_commit_pair(&empty_bar[r.s]);  // the last ones no load waits for
         }
         umma_commit_pair(&tfull_bar[buf]);
       }
@@ -537,12 +666,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     griddep_wait();
     for (int i = 0; i < mine; ++i) {
-      const int buf = i & 1, tile = pair + i * t.pairs;
-      const int w0 = tile % t.wt * t.bn, n0 = GATED ? w0 / 2 : w0;
-      const int64_t row0 = static_cast<int64_t>(tile / t.wt) * kPairRows + rank * 128 + quad * 32;
+      const int buf = i & 1;
+      int wt, xt;
+      tile_at(t, pair + i * t.pairs, wt, xt);
+      const int w0 = wt * t.bn, n0 = GATED ? w0 / 2 : w0;
+      const int64_t row0 = static_cast<int64_t>(xt) * kPairRows + rank * 128 + quad * 32;
       const int cols = min(out_bn, a.n - n0);  // of y
       if (has_r) residual_to_stage(a, t.r_vec, stage0, row0, n0, cols, lane);
-      if (ok && !mbar_wait(&tfull_bar[buf], (i >> 1) & 1)) {
+      if (ok && !wait_phase(&tfull_bar[buf], (i >> 1) & 1)) {
         report_error(a.err, kErrTimeout);
         ok = false;
       }
@@ -625,20 +756,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------ host
-RowsPlan rows_plan(const LinearArgs& a, int bn, int split, int ring_bytes) {
+// Shared memory of a CTA: two fit an SM, so that one's loads go on while the other finishes.
+constexpr int kRowsSmem = 108 * 1024;
+
+RowsPlan rows_plan(const LinearArgs& a, int bn, int split, bool norm) {
   RowsPlan t;
   t.bn = bn;
   t.split = split;
   t.boxes = (a.k + kBK - 1) / kBK;
-  const int stage = kABytes + bn * kBK * 2;
-  const int share = (t.boxes + split - 1) / split;
-  t.stages = ring_bytes / stage;
-  t.stages = t.stages > kMaxStages ? kMaxStages : t.stages;
-  t.stages = t.stages > share ? share : t.stages;
+  t.xt = (a.rows + bn - 1) / bn;
   t.per_rank = (bn / 4 + split - 1) / split;
+  const int share = (t.boxes + split - 1) / split, x_box = bn * kBK * 2;
+  const int join = split > 1 ? split * t.per_rank * kTW * 16 : 0, xhat = norm ? share * x_box : 0;
+  const int stage = kABytes + (norm ? 0 : x_box);
+  const bool aside = join > 0 && join <= kRowsSmem / 3;  // else the parts meet in the ring
+  t.stages = (kRowsSmem - xhat - (aside ? join : 0)) / stage;
+  t.stages = t.stages > kMaxStages ? kMaxStages : t.stages < 2 ? 2 : t.stages;
+  t.stages = t.stages > share ? share : t.stages;
+  t.norm = norm ? t.stages * stage : 0;
+  t.join = aside ? t.stages * stage + xhat : 0;
+  t.smem = t.stages * stage + xhat;
+  t.smem = (aside ? t.smem + join : t.smem > join ? t.smem : join) + 1024;
   t.cols = 32;
   while (t.cols < static_cast<uint32_t>(bn)) t.cols *= 2;
-  t.xt = (a.rows + bn - 1) / bn;
   return t;
 }
 
@@ -647,18 +787,15 @@ cudaError_t launch_rows(const LinearArgs& a, const RowsPlan& t, cudaStream_t str
   CUtensorMap tm_w, tm_x;
   cudaError_t e = encode_rows_sw128(&tm_w, a.w, a.k, a.wide, a.k, kBK, kTW);
   if (e == cudaSuccess)
-    e = a.gain != nullptr ? encode_rows_sw128(&tm_x, a.xhat, a.k, a.rows, a.k, kBK, t.bn)
-                          : encode_rows_sw128(&tm_x, a.x, a.k, a.rows, a.x_stride, kBK, t.bn);
+    e = a.gain != nullptr && t.norm == 0 ? encode_rows_sw128(&tm_x, a.xhat, a.k, a.rows, a.k, kBK, t.bn)
+                                         : encode_rows_sw128(&tm_x, a.x, a.k, a.rows, a.x_stride, kBK, t.bn);
   if (e != cudaSuccess) return e;
-  int smem = t.stages * (kABytes + t.bn * kBK * 2);
-  const int join = t.split > 1 ? t.split * t.per_rank * kTW * 16 : 0;
-  smem = (smem > join ? smem : join) + 1024;
-  e = cudaFuncSetAttribute(linear_rows_kernel<ACT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = cudaFuncSetAttribute(linear_rows_kernel<ACT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, t.smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((a.wide + kTW - 1) / kTW) * t.xt * t.split);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = t.smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -683,6 +820,7 @@ cudaError_t launch_tiles(const LinearArgs& a, int bn, int num_sms, cudaStream_t 
   t.xt = (a.rows + kPairRows - 1) / kPairRows;
   t.pairs = num_sms / 2;
   if (t.pairs > t.wt * t.xt) t.pairs = t.wt * t.xt;
+  t.band = t.xt < 8 ? t.xt : 8;
   t.y_vec = rows16(a.y, a.y_stride);
   t.r_vec = a.residual != nullptr && rows16(a.residual, a.r_stride);
   CUtensorMap tm_w, tm_x;
@@ -706,27 +844,94 @@ cudaError_t launch_tiles(const LinearArgs& a, int bn, int num_sms, cudaStream_t 
   return cudaLaunchKernelEx(&cfg, linear_tiles_kernel<ACT, GATED>, tm_w, tm_x, a, t);
 }
 
+// ------------------------------------------------------------ which kernel, which tiles
+struct Choice {
+  bool tiles;   // linear_tiles_kernel, else linear_rows_kernel
+  int bn;       // rows of W, or of x, to a tile
+  int split;    // CTAs that share a tile's K
+  bool norm;    // the rows are normed inside the kernel
+};
+
+constexpr int kNormBytes = 40 * 1024;  // of shared memory that rows normed inside may take
+
+// Whether rows_plan's CTAs norm their rows themselves: where they are done in two rounds, while the first boxes of W come
+// (one row of 4096: 13.1 us for 14.8 with the norm's kernel in front, and a launch less on the host).
+bool norm_inside(const LinearArgs& a, int bn, int split) {
+  const int lanes = norm_lanes(a.k), boxes = (a.k + kBK - 1) / kBK;
+  return a.gain != nullptr && lanes <= kNormMaxLanes && (bn < a.rows ? bn : a.rows) * lanes <= 2 * kNormMaxLanes &&
+         (boxes + split - 1) / split * bn * kBK * 2 <= kNormBytes;
+}
+
+// What each kernel takes, in us: fitted to 230 shapes (1 to 2048 rows, K 256 to 12288, 256 to 24576 rows of W) with every
+// tile and split; the choice is within 2% of the best on average and 32% at worst.  A box of 64 columns costs a CTA the
+// longer of the MMAs' own pace, its bytes' way from L2, shared with the other CTAs, and the ring's latency.
+float rows_us(const LinearArgs& a, int bn, int split, int num_sms) {
+  const RowsPlan t = rows_plan(a, bn, split, false);
+  const int wt = (a.wide + kTW - 1) / kTW;
+  const int64_t ctas = static_cast<int64_t>(wt) * t.xt * split;
+  const int64_t waves = (ctas + 2 * num_sms - 1) / (2 * num_sms) + (split > 4 && ctas > 9 * num_sms / 5 ? 1 : 0);
+  const float kb = 16.f + bn / 8.f;
+  const float box = fmaxf(fmaxf(0.29f, 0.99f / t.stages), kb * 0.0082f * (ctas > num_sms ? 2 : 1));
+  const float one = (t.boxes + split - 1) / split * box + 0.38f + (split > 1 ? 0.46f + 0.045f * bn : 0.033f * bn);
+  const float dram = static_cast<float>(a.wide) * a.k * 2.f / 6.7e6f + (split > 1 ? 0.46f : 0.f);
+  return 2.2f + fmaxf(waves * one, dram) + 0.05f * fminf(waves * one, dram);
+}
+
+float tiles_us(const LinearArgs& a, int bn, int num_sms) {
+  const int boxes = (a.k + kBK - 1) / kBK, pairs = num_sms / 2;
+  const int64_t tiles = (static_cast<int64_t>(a.wide) + bn - 1) / bn * ((a.rows + kPairRows - 1) / kPairRows);
+  const int64_t waves = (tiles + pairs - 1) / pairs;
+  const float busy = tiles < pairs ? static_cast<float>(tiles) / pairs : 1.f;
+  const float box = fmaxf(0.287f, (32.f + bn / 4.f) * busy * 0.00307f);
+  const float work = waves * boxes * box + 0.01f * bn, dram = static_cast<float>(a.wide) * a.k * 2.f / 6.7e6f;
+  return 3.2f + fmaxf(work, dram) + 0.05f * fminf(work, dram);
+}
+
+Choice choose(const LinearArgs& a, int num_sms) {
+  Choice best = {};
+  float least = INFINITY;
+  for (int bn = 64; bn <= 256; bn += 32) {
+    const float us = tiles_us(a, bn, num_sms);
+    if (us < least) {
+      least = us;
+      best = {true, bn, 1, false};
+    }
+  }
+  if (a.rows > 4096) return best;  // (rows_us does not come near)
+  int last = 0;
+  for (int most : {128, 96, 64, 48, 32, 16}) {
+    const int xt = (a.rows + most - 1) / most, bn = ((a.rows + xt - 1) / xt + 15) / 16 * 16;
+    if (bn == last) continue;
+    last = bn;
+    for (int split : {1, 2, 3, 4, 5, 8}) {
+      if (split > (a.k + kBK - 1) / kBK) break;
+      const float us = rows_us(a, bn, split, num_sms);
+      if (us < least) {
+        least = us;
+        best = {false, bn, split, norm_inside(a, bn, split)};
+      }
+    }
+  }
+  return best;
+}
+
 template <int ACT, bool GATED>
-cudaError_t launch_product(const LinearArgs& a, int num_sms, cudaStream_t stream) {
-  const int boxes = (a.k + kBK - 1) / kBK;
-  if (a.rows > 256) return launch_tiles<ACT, GATED>(a, 256, num_sms, stream);
-  const int bn = (a.rows + 15) / 16 * 16;
-  int split = num_sms / ((a.wide + kTW - 1) / kTW);
-  split = split < 1 ? 1 : split > kMaxSplit ? kMaxSplit : split;
-  split = split > boxes ? boxes : split;
-  return launch_rows<ACT, GATED>(a, rows_plan(a, bn, split, 200 * 1024), stream);
+cudaError_t launch_product(const LinearArgs& a, const Choice& c, int num_sms, cudaStream_t stream) {
+  return c.tiles ? launch_tiles<ACT, GATED>(a, c.bn, num_sms, stream)
+                 : launch_rows<ACT, GATED>(a, rows_plan(a, c.bn, c.split, c.norm), stream);
 }
 
 template <int ACT>
-cudaError_t launch_act(const LinearArgs& a, int num_sms, cudaStream_t stream) {
-  return a.gated ? launch_product<ACT, true>(a, num_sms, stream) : launch_product<ACT, false>(a, num_sms, stream);
+cudaError_t launch_act(const LinearArgs& a, const Choice& c, int num_sms, cudaStream_t stream) {
+  return a.gated ? launch_product<ACT, true>(a, c, num_sms, stream) : launch_product<ACT, false>(a, c, num_sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   if (a.rows <= 0) return cudaSuccess;
-  if (a.gain != nullptr) {
+  const Choice c = choose(a, num_sms);
+  if (a.gain != nullptr && !c.norm) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.rows);
     cfg.blockDim = dim3(kNormThreads);
@@ -741,13 +946,13 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   }
   switch (a.act) {
     case kActSilu:
-      return launch_act<kActSilu>(a, num_sms, stream);
+      return launch_act<kActSilu>(a, c, num_sms, stream);
     case kActGelu:
-      return launch_act<kActGelu>(a, num_sms, stream);
+      return launch_act<kActGelu>(a, c, num_sms, stream);
     case kActGeluTanh:
-      return launch_act<kActGeluTanh>(a, num_sms, stream);
+      return launch_act<kActGeluTanh>(a, c, num_sms, stream);
     default:
-      return launch_act<kActNone>(a, num_sms, stream);
+      return launch_act<kActNone>(a, c, num_sms, stream);
   }
 }
 
