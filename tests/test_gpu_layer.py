@@ -283,7 +283,7 @@ def test_token_scores(dtype, m, v, pad):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-@pytest.mark.parametrize("scale", [0.25, 1.5, 40.0])
+@pytest.mark.parametrize("scale", [1e-6, 0.01, 0.25, 1.5, 40.0, 50.0, 1e4])
 def test_token_scores_at_a_temperature(dtype, scale):
     x = lu.randn((20, 3001), 1, 4.0, dtype)
     tokens = _tokens(20, 3001)
@@ -297,7 +297,7 @@ def test_token_scores_at_a_temperature(dtype, scale):
 def test_token_scores_under_masks(dtype, v):
     """-inf, the type's lowest value, next to nothing left, nothing left, and rows of one value."""
     lowest = torch.finfo(dtype).min
-    x = lu.randn((13, v), v, 3.0, dtype)
+    x = lu.randn((22, v), v, 3.0, dtype)
     u = torch.rand(x.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
     x[0].masked_fill_(u[0] < 0.9, -math.inf)
     x[1].masked_fill_(u[1] < 0.9, lowest)
@@ -315,7 +315,12 @@ def test_token_scores_under_masks(dtype, v):
     x[9] = -1e30
     x[10] = torch.linspace(-20, 20, v, device="cuda")
     x[11] = torch.linspace(20, -20, v, device="cuda")
-    tokens = _tokens(13, v)
+    for i, low in enumerate((-1e4, -1e5, -1e9, -1e10, -1e20)):  # finite masks, in front of what is left
+        x[13 + i, :v - 20] = low
+    x[18], x[19] = x[18] * 1e4, x[19] * 1e20  # large logits
+    x[20] = x[20] - 3e4
+    x[21, 5] = 2e4
+    tokens = _tokens(22, v)
     tokens[6] = v // 3
     for top in (1, 20, 32):
         got, bits = _scores(x, tokens, top, 1.0)
