@@ -4,17 +4,19 @@
 //   lse = c M + log s,  entropy = log s - a / s,  log p(t) = c (x_t - M) - log s,
 // and the top_k largest with the lowest index first among equals.
 //
-// A CTA takes a row, or where rows are few a cluster of up to eight does: each CTA every
-// eighth stretch of the row, and the first one joins what they leave in its shared memory.
-// A thread takes 16-byte pieces, a stretch apart, four at a time, and keeps its running
-// (reference, s, a), raised once a batch.  Exponents are powers of two: u = x c log2 e - R is
-// one FMA from the reference R, two elements to an instruction.
+// A team takes a row: a CTA, or where rows are many a warp, or where they are few a cluster
+// of up to eight CTAs (each every eighth stretch of the row, the first one joins what they
+// leave in its shared memory).  A thread takes 16-byte pieces, a stretch apart, four at a
+// time, through places of its own in shared memory that are filled two steps ahead (no
+// thread waits for another), and keeps its running (reference, s, a), raised once a step.
+// Exponents are powers of two: u = x c log2 e - R is one FMA from the reference R, two
+// elements to an instruction.
 //
 // For the alternatives a thread keeps its largest value with the first piece that holds it.
 // These pairs are all different, and each stands for an element, so a value that top_k of
 // them reach is a bound: an element below it (smaller, or equal and in a later piece) has
-// top_k others before it.  The bound is the top_k-th largest of the pairs of 64 groups of
-// four threads; only threads whose own pair is at or above it hold such elements, hardly
+// top_k others before it.  The bound is the top_k-th largest of the pairs of 32 groups of
+// threads; only threads whose own pair is at or above it hold such elements, hardly
 // more than top_k of them: their pieces alone are read again, and what passes is ranked.
 #include <math.h>
 
@@ -25,12 +27,10 @@ namespace dllm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 4;          // pieces a thread has on their way
+constexpr int kBatch = 4;          // pieces of a step
+constexpr int kRing = 3;           // steps a thread has in shared memory or on their way there
+constexpr int kRingBytes = kRing * kBatch * kThreads * 16;
 constexpr int kMaxCluster = 8;
-constexpr int kGroups = kThreads / 4;
-constexpr int kOwners = 4 * kMaxTop;  // threads that can reach the bound
-constexpr int kList = 512;         // elements ranked at once
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // The fast form takes what lies below kLow for kLow, which as a power of two times c log2 e is exact, so that masked logits
@@ -63,6 +63,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 // max that keeps a NaN
 __device__ __forceinline__ float max_nan(float x, float y) {
@@ -193,13 +196,13 @@ struct Row {
   __device__ __forceinline__ uint4 get(int v) const { return whole(v) ? load(v) : edge(v); }
 };
 
-// The slow form's sums of all pieces, by one CTA.
-template <typename T>
+// The slow form's sums of all pieces, by one team.
+template <typename T, int TEAM>
 __device__ __noinline__ Stat<true> slow_sums(const Row<T>& row, float c, int tid) {
   constexpr int N = Piece<T>::N;
   constexpr float kMin = -3.402823466e38f;
   Stat<true> t = {kMin, 0.f, 0.f};
-  for (int v = tid; v < row.pieces; v += kThreads) {
+  for (int v = tid; v < row.pieces; v += TEAM) {
     float x[N];
     Piece<T>::get(row.get(v), x);
     Stat<true> p = {kMin, 0.f, 0.f};
@@ -216,26 +219,76 @@ __device__ __noinline__ Stat<true> slow_sums(const Row<T>& row, float c, int tid
   return t;
 }
 
-// The sums of a CTA's threads, in a fixed order, to all of them.
-template <bool SLOW>
-__device__ __forceinline__ Stat<SLOW> block_join(Stat<SLOW> t, float c, float (*sh)[3], int tid) {
+template <int TEAM>
+struct Shared {
+  static constexpr int kWarps = TEAM / 32;
+  static constexpr int kList = TEAM == 32 ? 256 : 512;  // elements ranked at once
+  float ref[kWarps];
+  float2 sum[kWarps];
+  uint64_t key[TEAM > 32 ? TEAM : 1];  // the threads' pairs
+  uint64_t list[kList];
+  uint64_t best[kMaxTop];  // the alternatives, largest first
+  uint64_t prev, round[kWarps];
+  int owners[TEAM], n_owners, n_list;
+};
+// What the CTAs of a cluster leave with the first one.
+struct Parts {
+  float stat[kMaxCluster][3];
+  uint64_t best[kMaxCluster * kMaxTop];
+};
+
+template <int TEAM>
+__device__ __forceinline__ void team_sync() {
+  if (TEAM == 32)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+
+// The sums of a team's threads, in a fixed order, to all of them: the reference first, then all relative to it.
+template <int TEAM, bool SLOW>
+__device__ __forceinline__ Stat<SLOW> team_join(Stat<SLOW> t, float c, Shared<TEAM>& sh, int tid) {
+  constexpr int W = TEAM / 32;
   const int lane = tid & 31, warp = tid >> 5;
+  float n = t.r;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
+  if (W > 1) {
+    if (lane == 0) sh.ref[warp] = n;
+    team_sync<TEAM>();
+#pragma unroll
+    for (int w = 0; w < W; ++w) n = fmaxf(n, sh.ref[w]);
+  }
+  const float d = Stat<SLOW>::apart(t.r, n, c), f = ex2(d);
+  float s = f * t.s, a = f * (t.a + t.s * d);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    Stat<SLOW> y = {__shfl_down_sync(0xffffffffu, t.r, o), __shfl_down_sync(0xffffffffu, t.s, o),
-                    __shfl_down_sync(0xffffffffu, t.a, o)};
-    t.join(y, c);
+    s += __shfl_xor_sync(0xffffffffu, s, o);
+    a += __shfl_xor_sync(0xffffffffu, a, o);
   }
-  if (lane == 0) {
-    sh[warp][0] = t.r;
-    sh[warp][1] = t.s;
-    sh[warp][2] = t.a;
+  if (W > 1) {
+    if (lane == 0) sh.sum[warp] = make_float2(s, a);
+    team_sync<TEAM>();
+    s = a = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      s += sh.sum[w].x;
+      a += sh.sum[w].y;
+    }
   }
-  __syncthreads();
-  t = {sh[0][0], sh[0][1], sh[0][2]};
-#pragma unroll 1
-  for (int w = 1; w < kWarps; ++w) t.join({sh[w][0], sh[w][1], sh[w][2]}, c);
-  return t;
+  return {n, s, a};
+}
+
+// The want-th largest of a warp's 64-bit values (all different, but for 0: none), or 0 where there are fewer.
+__device__ __forceinline__ uint64_t nth_largest(uint64_t g, int want) {
+  uint32_t hi = static_cast<uint32_t>(g >> 32), lo = static_cast<uint32_t>(g);
+  for (;;) {
+    const uint32_t h = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t l = __reduce_max_sync(0xffffffffu, hi == h ? lo : 0u);
+    if (h == 0) return 0;
+    if (--want == 0) return static_cast<uint64_t>(h) << 32 | l;
+    if (hi == h && lo == l) hi = 0;
+  }
 }
 
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
@@ -245,257 +298,271 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-struct Shared {
-  float stat[kWarps][3];
-  uint64_t group[kGroups];
-  uint64_t list[kList];
-  uint64_t best[kMaxTop];  // this CTA's alternatives, largest first
-  uint64_t bound, prev, round[kWarps];
-  int owners[kOwners], n_owners, n_list;
-  // what the CTAs of a cluster leave with the first one
-  float part[kMaxCluster][3];
-  uint64_t part_key[kMaxCluster];
-  uint64_t part_best[kMaxCluster * kMaxTop];
-};
-
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) token_scores_kernel(const ScoreArgs a, int cluster) {
-  constexpr int N = Piece<T>::N;
-  __shared__ Shared sh;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = cluster > 1 ? static_cast<int>(blockIdx.x) % cluster : 0;
-  const int stretch = kThreads * cluster;
+template <typename T, int TEAM, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, TEAM == 32 ? 3 : 4) token_scores_kernel(const ScoreArgs a, int cluster) {
+  constexpr int N = Piece<T>::N, kTeams = kThreads / TEAM;
+  using Sh = Shared<TEAM>;
+  __shared__ Sh shared[kTeams];
+  extern __shared__ uint4 ring_all[];
+  const int team = static_cast<int>(threadIdx.x) / TEAM, tid = static_cast<int>(threadIdx.x) % TEAM;
+  const int lane = tid & 31, warp = tid >> 5;
+  Sh& sh = shared[team];
+  uint4* const ring = ring_all + threadIdx.x;  // this thread's places, kThreads apart
+  const int rank = CLUSTER ? static_cast<int>(blockIdx.x) % cluster : 0;
+  const int stretch = CLUSTER ? TEAM * cluster : TEAM;
   const float c = fminf(a.scale * kLog2e, 3.402823466e38f);
+  if (CLUSTER) cluster_arrive_release();  // this CTA runs: the others may write to it
   griddep_wait();
   griddep_launch_dependents();
+  const int j = CLUSTER ? static_cast<int>(blockIdx.x) / cluster : static_cast<int>(blockIdx.x) * kTeams + team;
+  if (j >= a.rows) return;  // (a warp's: no barrier of a CTA follows there)
+  const Row<T> row(static_cast<const T*>(a.logits) + j * a.stride, a.vocab);
+  int tok = -1;  // thread 0: the given token, and its logit on its way
+  float tok_x = 0.f;
+  if (tid == 0 && rank == 0 && a.tokens != nullptr) {
+    tok = __ldg(a.tokens + j);
+    if (tok >= 0 && tok < a.vocab) tok_x = Piece<T>::one(row.p + tok);
+  }
 
-  for (int j = static_cast<int>(blockIdx.x) / cluster; j < a.rows; j += static_cast<int>(gridDim.x) / cluster) {
-    const Row<T> row(static_cast<const T*>(a.logits) + j * a.stride, a.vocab);
-    const int whole_from = row.lead > 0 ? 1 : 0, whole_to = (row.lead + row.n) / N;  // whole pieces
-    // ---- sums, and this thread's largest
-    float m = kLow, r = kLow * c, top = -INFINITY;
-    int top_v = 0;
-    float2 s2 = {0.f, 0.f}, a2 = {0.f, 0.f};
-    for (int v0 = rank * kThreads + tid; v0 < row.pieces; v0 += kBatch * stretch) {
-      uint4 q[kBatch];
-      if (v0 >= whole_from && v0 + (kBatch - 1) * stretch < whole_to) {
+  // ---- sums, and this thread's largest
+  float m = kLow, r = kLow * c, top = -INFINITY;
+  int top_v = 0;
+  float2 s2 = {0.f, 0.f}, a2 = {0.f, 0.f};
+  const int v_first = rank * TEAM + tid;  // this thread's first piece
+  const int steps = (row.pieces + kBatch * stretch - 1) / (kBatch * stretch);
+  // steps [from, to) have whole pieces only
+  const int whole_to = (row.lead + row.n) / N - (kBatch - 1) * stretch - v_first;
+  const int to = whole_to > 0 ? (whole_to + kBatch * stretch - 1) / (kBatch * stretch) : 0;
+  const int from = row.lead > 0 && v_first == 0 ? 1 : 0;
+  const T* next = row.p + static_cast<int64_t>(row.first(v_first));
+  // step i's pieces to their places (those behind the row's last: all -inf)
+  auto ask = [&](int i, int place) {
+    if (i >= from && i < to) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) q[b] = row.load(v0 + b * stretch);
-      } else {
+      for (int b = 0; b < kBatch; ++b)
+        cp_async16(smem_u32(ring + (place * kBatch + b) * kThreads), next + b * stretch * N);
+    } else if (i < steps) {
 #pragma unroll 1
-        for (int b = 0; b < kBatch; ++b) {
-          const uint4 u = row.get(v0 + b * stretch);
+      for (int b = 0; b < kBatch; ++b)
+        ring[(place * kBatch + b) * kThreads] = row.get(v_first + (i * kBatch + b) * stretch);
+    }
+    next += kBatch * stretch * N;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto step = [&](int i, int place) {
+    ask(i + kRing - 1, (place + kRing - 1) % kRing);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    uint4 q[kBatch];
 #pragma unroll
-          for (int k = 0; k < kBatch; ++k)
-            if (k == b) q[k] = u;
-        }
-      }
-      float most = m;
+    for (int b = 0; b < kBatch; ++b) q[b] = ring[(place * kBatch + b) * kThreads];
+    float most = m;
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const float l = Piece<T>::largest(q[b]);
-        most = fmaxf(most, l);
-        if (l > top) {
-          top = l;
-          top_v = v0 + b * stretch;
-        }
-      }
-      const float now = most * c, d = r - now, f = ex2(d);
-      a2 = fma2(s2, {d, d}, a2);
-      a2 = fma2(a2, {f, f}, {0.f, 0.f});
-      s2 = fma2(s2, {f, f}, {0.f, 0.f});
-      m = most;
-      r = now;
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        float2 p[N / 2];
-        Piece<T>::pairs(q[b], p);
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) {
-          const float2 u = fma2(p[i], {c, c}, {-r, -r});
-          const float2 e = {ex2(u.x), ex2(u.y)};
-          s2 = add2(s2, e);
-          a2 = fma2(e, u, a2);
-        }
+    for (int b = 0; b < kBatch; ++b) {
+      const float l = Piece<T>::largest(q[b]);
+      most = fmaxf(most, l);
+      if (l > top) {
+        top = l;
+        top_v = i * kBatch + b;
       }
     }
-    const uint64_t best = key_of(top, top_v);
-    Stat<false> t = {r, s2.x + s2.y, a2.x + a2.y};
-    t = block_join(t, c, sh.stat, tid);
-
-    // ---- this CTA's alternatives (the row's largest at least), as keys of element numbers
-    const int want = a.top > 0 ? a.top : 1;
-    {
-      uint64_t g = best;
+    const float now = most * c, d = r - now, f = ex2(d);
+    a2 = fma2(s2, {d, d}, a2);
+    a2 = fma2(a2, {f, f}, {0.f, 0.f});
+    s2 = fma2(s2, {f, f}, {0.f, 0.f});
+    m = most;
+    r = now;
 #pragma unroll
-      for (int o = 1; o < 4; o <<= 1) {
-        const uint64_t y = __shfl_xor_sync(0xffffffffu, g, o);
-        g = y > g ? y : g;
+    for (int b = 0; b < kBatch; ++b) {
+      float2 p[N / 2];
+      Piece<T>::pairs(q[b], p);
+#pragma unroll
+      for (int k = 0; k < N / 2; ++k) {
+        const float2 u = fma2(p[k], {c, c}, {-r, -r});
+        const float2 e = {ex2(u.x), ex2(u.y)};
+        s2 = add2(s2, e);
+        a2 = fma2(e, u, a2);
       }
-      if ((tid & 3) == 0) sh.group[tid >> 2] = g;
-      if (tid == 0) {
-        sh.bound = 0;
-        sh.n_owners = sh.n_list = 0;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) ask(i, i);
+#pragma unroll 1
+  for (int i = 0; i < steps; i += kRing) {
+#pragma unroll
+    for (int k = 0; k < kRing; ++k)
+      if (k == 0 || i + k < steps) step(i + k, k);
+  }
+  const uint64_t best = key_of(top, v_first + top_v * stretch);
+  Stat<false> t = {r, s2.x + s2.y, a2.x + a2.y};
+  t = team_join<TEAM>(t, c, sh, tid);
+
+  // ---- this team's alternatives (the row's largest at least), as keys of element numbers
+  const int want = a.top > 0 ? a.top : 1;
+  {
+    uint64_t g = best;
+    if (tid == 0) sh.n_owners = sh.n_list = 0;
+    if (tid < kMaxTop) sh.best[tid] = 0;
+    if (TEAM > 32) {  // (a group is a lane of all warps: each has something wherever 32 threads do)
+      sh.key[tid] = best;
+      team_sync<TEAM>();
+#pragma unroll
+      for (int w = 0; w < TEAM / 32; ++w) g = sh.key[w * 32 + lane] > g ? sh.key[w * 32 + lane] : g;
+    }
+    const uint64_t bound = nth_largest(g, want);  // (every warp for itself)
+    team_sync<TEAM>();
+    if (best != 0 && best >= bound) sh.owners[atomicAdd(&sh.n_owners, 1)] = tid;
+    team_sync<TEAM>();
+    const int no = sh.n_owners, each = (row.pieces + stretch - 1) / stretch;
+    const bool here = steps <= kRing;  // the whole row is still in the ring
+    for (int i0 = tid; i0 < no * each; i0 += 2 * TEAM) {
+      int v[2];
+      uint4 u[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = i0 + k * TEAM, q = i / no;
+        v[k] = row.pieces;
+        if (i < no * each) {
+          const int o = sh.owners[i - q * no];
+          v[k] = o + rank * TEAM + q * stretch;
+          if (v[k] < row.pieces) u[k] = here ? ring_all[q * kThreads + team * TEAM + o] : row.get(v[k]);
+        }
       }
-      if (tid < kMaxTop) sh.best[tid] = 0;
-      __syncthreads();
-      if (tid < kGroups) {
-        const uint64_t mine = sh.group[tid];
-        int before = 0;
-#pragma unroll 8
-        for (int i = 0; i < kGroups; ++i) before += sh.group[i] > mine;
-        if (mine != 0 && before == want - 1) sh.bound = mine;  // none where fewer hold anything
-      }
-      __syncthreads();
-      const uint64_t bound = sh.bound;
-      if (best != 0 && best >= bound) sh.owners[atomicAdd(&sh.n_owners, 1)] = tid;
-      __syncthreads();
-      const int no = sh.n_owners, each = (row.pieces + stretch - 1) / stretch;
-      for (int i = tid; i < no * each; i += kThreads) {
-        const int v = sh.owners[i % no] + rank * kThreads + i / no * stretch;
-        if (v >= row.pieces) continue;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (v[k] >= row.pieces || key_of(Piece<T>::largest(u[k]), v[k]) < bound) continue;
         float x[N];
-        Piece<T>::get(row.get(v), x);
+        Piece<T>::get(u[k], x);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          if (x[e] > -INFINITY && key_of(x[e], v) >= bound) {
+          if (x[e] > -INFINITY && key_of(x[e], v[k]) >= bound) {
             const int at = atomicAdd(&sh.n_list, 1);
-            if (at < kList) sh.list[at] = key_of(x[e], row.first(v) + e);
+            if (at < Sh::kList) sh.list[at] = key_of(x[e], row.first(v[k]) + e);
           }
         }
       }
-      __syncthreads();
-      const int nl = sh.n_list;
-      if (nl <= kList) {
-        for (int i = tid; i < nl; i += kThreads) {
-          int before = 0;
-          for (int o = 0; o < nl; ++o) before += sh.list[o] > sh.list[i];
-          if (before < want) sh.best[before] = sh.list[i];
-        }
-      } else {  // so many in so few threads' pieces: one after the other
-        if (tid == 0) sh.prev = ~0ull;
-        __syncthreads();
-        for (int k = 0; k < want; ++k) {
-          const uint64_t prev = sh.prev;
-          uint64_t most = 0;
-          for (int i = tid; i < no * each; i += kThreads) {
-            const int v = sh.owners[i % no] + rank * kThreads + i / no * stretch;
-            if (v >= row.pieces) continue;
-            float x[N];
-            Piece<T>::get(row.get(v), x);
+    }
+    team_sync<TEAM>();
+    const int nl = sh.n_list;
+    if (nl <= Sh::kList) {
+      for (int i = tid; i < nl; i += TEAM) {
+        const uint64_t mine = sh.list[i];
+        int before = 0;
+        for (int o = 0; o < nl; ++o) before += sh.list[o] > mine;
+        if (before < want) sh.best[before] = mine;
+      }
+    } else {  // so many in so few threads' pieces: one after the other
+      if (tid == 0) sh.prev = ~0ull;
+      team_sync<TEAM>();
+      for (int k = 0; k < want; ++k) {
+        const uint64_t prev = sh.prev;
+        uint64_t most = 0;
+        for (int i = tid; i < no * each; i += TEAM) {
+          const int v = sh.owners[i % no] + rank * TEAM + i / no * stretch;
+          if (v >= row.pieces) continue;
+          float x[N];
+          Piece<T>::get(row.get(v), x);
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-              const uint64_t key = key_of(x[e], row.first(v) + e);
-              if (key < prev && key > most) most = key;
-            }
+          for (int e = 0; e < N; ++e) {
+            const uint64_t key = key_of(x[e], row.first(v) + e);
+            if (key < prev && key > most) most = key;
           }
+        }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            const uint64_t y = __shfl_xor_sync(0xffffffffu, most, o);
-            most = y > most ? y : most;
-          }
-          if (lane == 0) sh.round[warp] = most;
-          __syncthreads();
-          if (tid == 0) {
-            for (int w = 1; w < kWarps; ++w) most = sh.round[w] > most ? sh.round[w] : most;
-            sh.prev = sh.best[k] = most;
-          }
-          __syncthreads();
+        for (int o = 16; o > 0; o >>= 1) {
+          const uint64_t y = __shfl_xor_sync(0xffffffffu, most, o);
+          most = y > most ? y : most;
         }
-      }
-      __syncthreads();
-    }
-
-    // ---- the cluster's parts meet in its first CTA
-    if (cluster > 1) {
-      const uint32_t base = mapa_shared(smem_u32(&sh), 0) - smem_u32(&sh);
-      if (tid == 0) {
-        st_cluster_f32(base + smem_u32(&sh.part[rank][0]), t.r);
-        st_cluster_f32(base + smem_u32(&sh.part[rank][1]), t.s);
-        st_cluster_f32(base + smem_u32(&sh.part[rank][2]), t.a);
-      }
-      if (tid < want) st_cluster_u64(base + smem_u32(&sh.part_best[rank * want + tid]), sh.best[tid]);
-      cluster_arrive_release();
-      cluster_wait_acquire();
-      if (rank == 0) {
-        t = {sh.part[0][0], sh.part[0][1], sh.part[0][2]};
-        for (int i = 1; i < cluster; ++i) t.join({sh.part[i][0], sh.part[i][1], sh.part[i][2]}, c);
-        if (tid < kMaxTop) sh.best[tid] = 0;
-        __syncthreads();
-        if (tid < cluster * want) {
-          const uint64_t mine = sh.part_best[tid];
-          int before = 0;
-          for (int i = 0; i < cluster * want; ++i) before += sh.part_best[i] > mine;
-          if (mine != 0 && before < want) sh.best[before] = mine;
+        if (lane == 0) sh.round[warp] = most;
+        team_sync<TEAM>();
+        if (tid == 0) {
+          for (int w = 1; w < Sh::kWarps; ++w) most = sh.round[w] > most ? sh.round[w] : most;
+          sh.prev = sh.best[k] = most;
         }
-        __syncthreads();
+        team_sync<TEAM>();
       }
     }
+    team_sync<TEAM>();
+  }
 
-    // ---- results
-    if (rank == 0) {
-      const uint64_t first = sh.best[0];
-      const float largest = first != 0 ? value_of(first) : -INFINITY;
-      const bool slow = largest != INFINITY && (c < kLeast || c > kMost ||
-                                                (first != 0 && (fabsf(largest) > kFar || fabsf(largest) * c > kFar)));
-      float ref = t.r, s = t.s, wa = t.a;
-      if (slow) {
-        const Stat<true> z = block_join(slow_sums(row, c, tid), c, sh.stat, tid);
-        ref = z.r;
-        s = z.s;
-        wa = z.a;
-      }
-      const bool bad = !(s < INFINITY) || largest == INFINITY;  // a NaN or +inf
-      const bool empty = !bad && first == 0;
-      const float nan = __int_as_float(0x7FFFFFFF), ls = lg2(s);
-      // log of the sum relative to the largest; log p of a logit
-      const float log_s = ((slow ? 0.f : fmaf(-largest, c, ref)) + ls) * kLn2;
-      auto logp = [&](float x) { return fmaf(x - largest, a.scale, -log_s); };
-      if (tid == 0) {
-        if (bad) report_error(a.err, kErrRange);
-        if (a.lse != nullptr)
-          a.lse[j] = bad ? nan : empty ? -INFINITY : fmaf(largest, a.scale, log_s);
-        if (a.entropy != nullptr) a.entropy[j] = bad ? nan : empty ? 0.f : (ls - wa / s) * kLn2;
-      }
-      if (tid == 32 && a.tokens != nullptr) {
-        const int tok = a.tokens[j];
-        float lp = 0.f;
-        if (tok >= a.vocab) report_error(a.err, kErrBadShape);
-        if (bad || tok >= a.vocab)
-          lp = nan;
-        else if (tok >= 0)
-          lp = empty ? -INFINITY : logp(Piece<T>::one(row.p + tok));
-        a.logp[j] = lp;
-      }
-      if (tid >= 64 && tid - 64 < a.top) {
-        const uint64_t key = bad ? 0 : sh.best[tid - 64];
-        const int64_t at = static_cast<int64_t>(j) * a.top + tid - 64;
-        a.top_ids[at] = key != 0 ? place_of(key) : -1;
-        a.top_logp[at] = bad ? nan : key != 0 ? logp(value_of(key)) : -INFINITY;
-      }
+  // ---- the cluster's parts meet in its first CTA
+  if constexpr (CLUSTER) {
+    __shared__ Parts parts;
+    cluster_wait_acquire();
+    const uint32_t base = mapa_shared(smem_u32(&parts), 0) - smem_u32(&parts);
+    if (tid == 0) {
+      st_cluster_f32(base + smem_u32(&parts.stat[rank][0]), t.r);
+      st_cluster_f32(base + smem_u32(&parts.stat[rank][1]), t.s);
+      st_cluster_f32(base + smem_u32(&parts.stat[rank][2]), t.a);
     }
-    __syncthreads();  // the next row's
-    if (cluster > 1) {  // what the first CTA has of this row is read
-      cluster_arrive_release();
-      cluster_wait_acquire();
+    if (tid < want) st_cluster_u64(base + smem_u32(&parts.best[rank * want + tid]), sh.best[tid]);
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    if (rank != 0) return;
+    t = {parts.stat[0][0], parts.stat[0][1], parts.stat[0][2]};
+    for (int i = 1; i < cluster; ++i) t.join({parts.stat[i][0], parts.stat[i][1], parts.stat[i][2]}, c);
+    __syncthreads();
+    if (tid < kMaxTop) sh.best[tid] = 0;
+    __syncthreads();
+    if (tid < cluster * want) {
+      const uint64_t mine = parts.best[tid];
+      int before = 0;
+      for (int i = 0; i < cluster * want; ++i) before += parts.best[i] > mine;
+      if (mine != 0 && before < want) sh.best[before] = mine;
     }
+    __syncthreads();
+  }
+
+  // ---- results
+  const uint64_t first = sh.best[0];
+  const float largest = first != 0 ? value_of(first) : -INFINITY;
+  const bool slow = largest != INFINITY && (c < kLeast || c > kMost ||
+                                            (first != 0 && (fabsf(largest) > kFar || fabsf(largest) * c > kFar)));
+  float ref = t.r, s = t.s, wa = t.a;
+  if (slow) {
+    const Stat<true> z = team_join<TEAM>(slow_sums<T, TEAM>(row, c, tid), c, sh, tid);
+    ref = z.r;
+    s = z.s;
+    wa = z.a;
+  }
+  if (warp != 0) return;
+  const bool bad = !(s < INFINITY) || largest == INFINITY;  // a NaN or +inf
+  const bool empty = !bad && first == 0;
+  const float nan = __int_as_float(0x7FFFFFFF), ls = log2f(s);
+  // log of the sum relative to the largest; log p of a logit
+  const float log_s = ((slow ? 0.f : fmaf(-largest, c, ref)) + ls) * kLn2;
+  auto logp = [&](float x) { return fmaf(x - largest, a.scale, -log_s); };
+  if (tid == 0) {
+    if (bad) report_error(a.err, kErrRange);
+    if (a.lse != nullptr) a.lse[j] = bad ? nan : empty ? -INFINITY : fmaf(largest, a.scale, log_s);
+    if (a.entropy != nullptr) a.entropy[j] = bad ? nan : empty ? 0.f : (ls - wa / s) * kLn2;
+    if (a.tokens != nullptr) {
+      float lp = 0.f;
+      if (tok >= a.vocab) report_error(a.err, kErrBadShape);
+      if (bad || tok >= a.vocab)
+        lp = nan;
+      else if (tok >= 0)
+        lp = empty ? -INFINITY : logp(tok_x);
+      a.logp[j] = lp;
+    }
+  }
+  if (tid < a.top) {
+    const uint64_t key = bad ? 0 : sh.best[tid];
+    const int64_t at = static_cast<int64_t>(j) * a.top + tid;
+    a.top_ids[at] = key != 0 ? place_of(key) : -1;
+    a.top_logp[at] = bad ? nan : key != 0 ? logp(value_of(key)) : -INFINITY;
   }
 }
 
-}  // namespace
-
-cudaError_t launch_token_scores(const ScoreArgs& a, int num_sms, cudaStream_t stream) {
-  if (a.rows <= 0) return cudaSuccess;
-  // Few rows: a cluster to each, so that all of them fill the SMs, as long as a CTA has a batch of pieces for each thread.
-  const int pieces = a.vocab / (a.fp32 ? 4 : 8);
-  int cluster = 1;
-  while (cluster < kMaxCluster && static_cast<int64_t>(a.rows) * cluster * 2 <= 4 * num_sms &&
-         pieces >= cluster * 2 * kThreads * kBatch)
-    cluster *= 2;
-  const int most = 4 * num_sms / cluster;  // rows at once
+template <typename T, int TEAM, bool CLUSTER>
+cudaError_t launch_scores(const ScoreArgs& a, int cluster, cudaStream_t stream) {
+  const auto kernel = token_scores_kernel<T, TEAM, CLUSTER>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e != cudaSuccess) return e;
+  constexpr int kTeams = kThreads / TEAM;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.rows < most ? a.rows : most) * cluster);
+  cfg.gridDim = dim3(CLUSTER ? a.rows * cluster : (a.rows + kTeams - 1) / kTeams);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kRingBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -505,9 +572,32 @@ cudaError_t launch_token_scores(const ScoreArgs& a, int num_sms, cudaStream_t st
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return a.fp32 ? cudaLaunchKernelEx(&cfg, token_scores_kernel<float>, a, cluster)
-                : cudaLaunchKernelEx(&cfg, token_scores_kernel<__nv_bfloat16>, a, cluster);
+  cfg.numAttrs = CLUSTER ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, cluster);
+}
+
+template <typename T>
+cudaError_t launch_type(const ScoreArgs& a, int num_sms, cudaStream_t stream) {
+  // Few rows: a cluster to each, as long as a CTA has a step for each thread (126464 bf16, two alternatives, with 1, 2, 4, 8
+  // CTAs: one row 14.3, 11.8, 9.4, 8.6 us; 32 rows 11.2, 9.2, 7.7, 7.8; 128 rows 11.6, 11.7, 12.8, 18.6; 300 rows 20.6, 22.2).
+  const int pieces = a.vocab / Piece<T>::N;
+  int cluster = 1;
+  while (cluster < kMaxCluster && static_cast<int64_t>(a.rows) * cluster * 2 <= 2 * num_sms &&
+         pieces >= cluster * 2 * kThreads * kBatch)
+    cluster *= 2;
+  if (cluster > 1) return launch_scores<T, kThreads, true>(a, cluster, stream);
+  // Many short rows: a warp to each, which waits for no other (2500 of 4000 bf16: 9.4 us for 28.0; of 16000: 24 for 35).
+  // With more alternatives most of a warp's threads hold one, and most of the row is read twice (2500 of 16000, 20
+  // alternatives: 51 for 42; of 4000: 20 for 35).
+  if (a.rows >= 4 * num_sms && pieces <= (a.top <= 4 ? 2048 : 512)) return launch_scores<T, 32, false>(a, 1, stream);
+  return launch_scores<T, kThreads, false>(a, 1, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_token_scores(const ScoreArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.rows <= 0) return cudaSuccess;
+  return a.fp32 ? launch_type<float>(a, num_sms, stream) : launch_type<__nv_bfloat16>(a, num_sms, stream);
 }
 
 }  // namespace dllm

@@ -386,3 +386,19 @@ def test_token_scores_rows_beyond_32_bits_of_elements():
     got, bits = _scores(x, tokens, 3, 1.0)
     assert bits == 0
     lu.assert_scores([t[-5:] for t in got], x[-5:], tokens[-5:], 3, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,v,top", [(3000, 130, 32), (1300, 1001, 20), (700, 4100, 4), (2100, 33, 5), (650, 1000, 20)])
+def test_token_scores_of_many_short_rows(dtype, m, v, top):
+    x = lu.randn((m, v + 3), m, 3.0, dtype)[:, :v]
+    x[5] = -math.inf
+    x[6] = torch.finfo(dtype).min
+    x[7, 1:] = -math.inf
+    x[8] = 1.5
+    x[9, ::2] = -1e9
+    x[10] = x[10] * 1e5
+    tokens = _tokens(m, v)
+    got, bits = _scores(x, tokens, top, 1.0)
+    assert bits == 0
+    lu.assert_scores(got, x, tokens, top, 1.0)
