@@ -7,44 +7,49 @@
 // pair lie with one lane: pieces l and l + rotary_dim / 16 where halves turn together, 2 l
 // and 2 l + 1 where neighbours do (the lanes behind the rotated elements take theirs two by
 // two).  So the only exchange is the sum of squares, over 8 (d = 128) or 4 lanes, and a warp
-// instruction moves whole 128-byte runs of 4 or 8 heads.  A lane's eight pairs have the same
-// numbers in every head: their cos and sin are loaded once for all heads of a row.
+// instruction moves whole 128-byte runs of 4 or 8 heads: a step.  A warp takes some of a
+// row's steps, two at a time and two on their way; its position, and behind that the cos and
+// sin of each lane's eight pairs, the same in every head, come once.
 #include "layer_ops.cuh"
+#include "pairs.cuh"
 #include "sm103.cuh"
 
 namespace dllm {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 
-__device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+__device__ __forceinline__ void unpack8(const uint4& u, float2 (&v)[4]) {
+  v[0] = unpack2(u.x);
+  v[1] = unpack2(u.y);
+  v[2] = unpack2(u.z);
+  v[3] = unpack2(u.w);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ uint4 pack8(const float2 (&v)[4]) {
+  return make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                    pack_bf16x2(v[3].x, v[3].y));
 }
 
-// A warp: one row's heads [first, first + kStep), [first + kStep, ...) of the queries, then of the keys.
+struct Step {
+  uint4 u0, u1;
+};
+
+// Warp: row blockIdx.x kWarps + its number, steps [y per, (y + 1) per) with y = blockIdx.y, of the queries' and then the
+// keys'.
 template <int D, bool NEIGHBOURS>
-__global__ void __launch_bounds__(kWarps * 32) head_rope_kernel(const HeadRopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 5) head_rope_kernel(const HeadRopeArgs a, int per) {
   constexpr int kLanes = D / 16;         // lanes of a head
-  constexpr int kStep = 32 / kLanes;     // heads of a warp instruction
+  constexpr int kHeads = 32 / kLanes;    // heads of a step
   const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
   const int row = blockIdx.x * kWarps + (threadIdx.x >> 5);
   griddep_wait();
   griddep_launch_dependents();
   if (row >= a.rows) return;
   const int pos = __ldg(a.row_pos + row);
-  if (pos < 0 || pos >= a.max_pos) {
-    if (pos != -1 && lane == 0) report_error(a.err, kErrBadShape);
-    return;
-  }
+  const int q_steps = (a.q.n_heads + kHeads - 1) / kHeads;
+  const int first = blockIdx.y * per;
+  const int end = min(first + per, q_steps + (a.k.n_heads + kHeads - 1) / kHeads);
   const int turned = a.rotary_dim / 16;  // lanes whose elements turn
   const bool turns = l < turned;
   int p0, p1;  // this lane's pieces of a head
@@ -55,83 +60,115 @@ __global__ void __launch_bounds__(kWarps * 32) head_rope_kernel(const HeadRopeAr
     p0 = turns ? l : 2 * l;  // behind the 2 turned pieces: 2 turned + 2 (l - turned)
     p1 = turns ? l + turned : p0 + 1;
   }
-  float cs[16];
+  const uint16_t* q_in = static_cast<const uint16_t*>(a.q.in) + row * a.q.in_row + sub * a.q.in_head;
+  const uint16_t* k_in = static_cast<const uint16_t*>(a.k.in) + row * a.k.in_row + sub * a.k.in_head;
+  auto load = [&](int s) {
+    Step t = {};
+    if (s >= end) return t;
+    const bool is_k = s >= q_steps;
+    const int h0 = (is_k ? s - q_steps : s) * kHeads;
+    if (h0 + sub < (is_k ? a.k.n_heads : a.q.n_heads)) {
+      const uint4* src = reinterpret_cast<const uint4*>(is_k ? k_in + h0 * a.k.in_head : q_in + h0 * a.q.in_head);
+      t.u0 = src[p0];
+      t.u1 = src[p1];
+    }
+    return t;
+  };
+  Step now[2] = {load(first), load(first + 1)};
+  if (pos < 0 || pos >= a.max_pos) {
+    if (pos != -1 && lane == 0) report_error(a.err, kErrBadShape);
+    return;
+  }
+  float2 cs[8];  // of the lane's pairs; halves: cos of two and sin of two in turn
   if (turns) {
     const float4* t = reinterpret_cast<const float4*>(a.table + (static_cast<size_t>(pos) * turned + l) * 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 f = __ldg(t + i);
-      cs[4 * i] = f.x;
-      cs[4 * i + 1] = f.y;
-      cs[4 * i + 2] = f.z;
-      cs[4 * i + 3] = f.w;
+      cs[2 * i] = NEIGHBOURS ? make_float2(f.x, f.y) : make_float2(f.x, f.z);
+      cs[2 * i + 1] = NEIGHBOURS ? make_float2(f.z, f.w) : make_float2(f.y, f.w);
     }
   }
+  uint16_t* q_out = static_cast<uint16_t*>(a.q.out) + row * a.q.out_row + sub * a.q.out_head;
+  uint16_t* k_out = static_cast<uint16_t*>(a.k.out) + row * a.k.out_row + sub * a.k.out_head;
+  uint4 g0 = {}, g1 = {};
+  bool norm = false;
 #pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
-    const HeadRows& r = side ? a.k : a.q;
-    const uint16_t* in = static_cast<const uint16_t*>(r.in) + row * r.in_row;
-    uint16_t* out = static_cast<uint16_t*>(r.out) + row * r.out_row;
-    uint4 g0 = {}, g1 = {};
-    const bool norm = r.gain != nullptr;
-    if (norm) {
-      g0 = __ldg(static_cast<const uint4*>(r.gain) + p0);
-      g1 = __ldg(static_cast<const uint4*>(r.gain) + p1);
-    }
-#pragma unroll 2
-    for (int h = sub; h < r.n_heads + sub; h += kStep) {  // the same turns for every lane
-      const bool there = h < r.n_heads;
-      uint4 u0 = {}, u1 = {};
-      if (there) {
-        const uint4* src = reinterpret_cast<const uint4*>(in + h * r.in_head);
-        u0 = src[p0];
-        u1 = src[p1];
+  for (int s0 = first; s0 < end; s0 += 2) {
+    const Step next[2] = {load(s0 + 2), load(s0 + 3)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int s = s0 + i;
+      if (s >= end) break;  // (the same for all lanes)
+      const bool is_k = s >= q_steps;
+      if (s == first || s == q_steps) {  // the gains of this side
+        const void* gain = is_k ? a.k.gain : a.q.gain;
+        norm = gain != nullptr;
+        if (norm) {
+          g0 = __ldg(static_cast<const uint4*>(gain) + p0);
+          g1 = __ldg(static_cast<const uint4*>(gain) + p1);
+        }
       }
-      float x0[8], x1[8];
-      unpack8(u0, x0);
-      unpack8(u1, x1);
+      float2 x0[4], x1[4];
+      unpack8(now[i].u0, x0);
+      unpack8(now[i].u1, x1);
       if (norm) {
-        float s = 0.f;
+        float2 sq = mul2(x0[0], x0[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(x0[i], x0[i], fmaf(x1[i], x1[i], s));
+        for (int k = 1; k < 4; ++k) sq = fma2(x0[k], x0[k], sq);
 #pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float inv = rsqrtf(s * (1.f / D) + a.eps);
-        float w0[8], w1[8];
+        for (int k = 0; k < 4; ++k) sq = fma2(x1[k], x1[k], sq);
+        float sum = sq.x + sq.y;
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float inv = rsqrtf(sum * (1.f / D) + a.eps);
+        float2 w0[4], w1[4];
         unpack8(g0, w0);
         unpack8(g1, w1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x0[i] = x0[i] * inv * w0[i];
-          x1[i] = x1[i] * inv * w1[i];
+        for (int k = 0; k < 4; ++k) {
+          x0[k] = mul2(mul2(x0[k], {inv, inv}), w0[k]);
+          x1[k] = mul2(mul2(x1[k], {inv, inv}), w1[k]);
         }
       }
       if (turns) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float& p = NEIGHBOURS ? (i < 4 ? x0[2 * i] : x1[2 * i - 8]) : x0[i];
-          float& q = NEIGHBOURS ? (i < 4 ? x0[2 * i + 1] : x1[2 * i - 7]) : x1[i];
-          const float c = cs[2 * i], s = cs[2 * i + 1], u = p;
-          p = u * c - q * s;
-          q = u * s + q * c;
+        for (int k = 0; k < 4; ++k) {
+          if (NEIGHBOURS) {
+            float2 &p = x0[k], &q = x1[k];
+            p = make_float2(p.x * cs[k].x - p.y * cs[k].y, p.x * cs[k].y + p.y * cs[k].x);
+            q = make_float2(q.x * cs[4 + k].x - q.y * cs[4 + k].y, q.x * cs[4 + k].y + q.y * cs[4 + k].x);
+          } else {
+            const float2 c = cs[2 * k], n = cs[2 * k + 1], u = x0[k], v = x1[k];
+            const float2 w = mul2(v, n);
+            x0[k] = fma2(u, c, make_float2(-w.x, -w.y));
+            x1[k] = fma2(u, n, mul2(v, c));
+          }
         }
       }
-      if (there) {
-        uint4* dst = reinterpret_cast<uint4*>(out + h * r.out_head);
+      const int h0 = (is_k ? s - q_steps : s) * kHeads;
+      if (h0 + sub < (is_k ? a.k.n_heads : a.q.n_heads)) {
+        uint4* dst = reinterpret_cast<uint4*>(is_k ? k_out + h0 * a.k.out_head : q_out + h0 * a.q.out_head);
         dst[p0] = pack8(x0);
         dst[p1] = pack8(x1);
       }
     }
+    now[0] = next[0];
+    now[1] = next[1];
   }
 }
 
-}  // namespace
-
-cudaError_t launch_head_rope(const HeadRopeArgs& a, int num_sms, cudaStream_t stream) {
-  (void)num_sms;
-  if (a.rows <= 0) return cudaSuccess;
+template <int D, bool NEIGHBOURS>
+cudaError_t launch(const HeadRopeArgs& a, int num_sms, cudaStream_t stream) {
+  constexpr int kHeads = 512 / D;
+  const int steps = (a.q.n_heads + kHeads - 1) / kHeads + (a.k.n_heads + kHeads - 1) / kHeads;
+  // As many steps to a warp as leave every SM some twenty warps, the same for all.
+  const int64_t most = static_cast<int64_t>(a.rows) * steps / (20 * num_sms);
+  int per = most < 1 ? 1 : most > steps ? steps : static_cast<int>(most);
+  const int parts = (steps + per - 1) / per;
+  per = (steps + parts - 1) / parts;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((a.rows + kWarps - 1) / kWarps);
+  cfg.gridDim = dim3((a.rows + kWarps - 1) / kWarps, parts);
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -139,11 +176,15 @@ cudaError_t launch_head_rope(const HeadRopeArgs& a, int num_sms, cudaStream_t st
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (a.head_dim == 128)
-    return a.neighbours ? cudaLaunchKernelEx(&cfg, head_rope_kernel<128, true>, a)
-                        : cudaLaunchKernelEx(&cfg, head_rope_kernel<128, false>, a);
-  return a.neighbours ? cudaLaunchKernelEx(&cfg, head_rope_kernel<64, true>, a)
-                      : cudaLaunchKernelEx(&cfg, head_rope_kernel<64, false>, a);
+  return cudaLaunchKernelEx(&cfg, head_rope_kernel<D, NEIGHBOURS>, a, per);
+}
+
+}  // namespace
+
+cudaError_t launch_head_rope(const HeadRopeArgs& a, int num_sms, cudaStream_t stream) {
+  if (a.rows <= 0) return cudaSuccess;
+  if (a.head_dim == 128) return a.neighbours ? launch<128, true>(a, num_sms, stream) : launch<128, false>(a, num_sms, stream);
+  return a.neighbours ? launch<64, true>(a, num_sms, stream) : launch<64, false>(a, num_sms, stream);
 }
 
 }  // namespace dllm

@@ -21,6 +21,7 @@
 #include <math.h>
 
 #include "layer_ops.cuh"
+#include "pairs.cuh"
 #include "sm103.cuh"
 
 namespace dllm {
@@ -43,27 +44,7 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float lg2(float x) { return log2f(x); }
 
-// Two floats to an instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -83,10 +64,6 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t x, uint32_t y) {
   asm("max.bf16x2 %0, %1, %2;" : "=r"(z) : "r"(x), "r"(y));
   return z;
 }
-__device__ __forceinline__ float2 unpack(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-
 // A 16-byte piece: N values; its largest (a NaN only where there is nothing else); its pairs, none below kLow.
 template <typename T>
 struct Piece;
@@ -117,19 +94,19 @@ struct Piece<__nv_bfloat16> {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack(w[i]);
+      const float2 f = unpack2(w[i]);
       v[2 * i] = f.x;
       v[2 * i + 1] = f.y;
     }
   }
   static __device__ __forceinline__ float largest(const uint4& u) {
-    const float2 f = unpack(max_bf16x2(max_bf16x2(u.x, u.y), max_bf16x2(u.z, u.w)));
+    const float2 f = unpack2(max_bf16x2(max_bf16x2(u.x, u.y), max_bf16x2(u.z, u.w)));
     return fmaxf(f.x, f.y);
   }
   static __device__ __forceinline__ void pairs(const uint4& u, float2 (&p)[4]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = unpack(max_nan_bf16x2(w[i], kLow2));
+    for (int i = 0; i < 4; ++i) p[i] = unpack2(max_nan_bf16x2(w[i], kLow2));
   }
   static __device__ __forceinline__ uint32_t bits(const __nv_bfloat16* p) {
     return __ldg(reinterpret_cast<const unsigned short*>(p));

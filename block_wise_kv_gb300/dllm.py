@@ -412,8 +412,8 @@ def dllm_linear_workspace_size(layer, rows: int, normed: bool) -> int:
 
 
 def _vector_ok(t, dtype, n: int, dev: int) -> bool:
-    """None, or a contiguous tensor of n values or more."""
-    return t is None or (t.dtype is dtype and t.numel() >= n and t.is_contiguous() and t.get_device() == dev)
+    """Whether t is a contiguous tensor of n values or more."""
+    return t.dtype is dtype and t.numel() >= n and t.is_contiguous() and t.get_device() == dev
 
 
 def dllm_linear(layer, x: torch.Tensor, w, y, rms_gain=None, bias=None, residual=None, ws=None, error=None,
@@ -423,24 +423,29 @@ def dllm_linear(layer, x: torch.Tensor, w, y, rms_gain=None, bias=None, residual
     dllm_linear_workspace_size bytes (with a gain); error: an int32 word."""
     k, n = layer.in_features, layer.out_features
     wide = 2 * n if layer.gated else n
-    m, dev, xs, ys = x.shape[0], x.get_device(), x.stride(), y.stride()
-    rs = ys if residual is None else residual.stride()
-    if (x.dtype is not _BF16 or tuple(x.shape) != (m, k) or xs[1] != 1 and k > 1
-            or w.dtype is not _BF16 or tuple(w.shape) != (wide, k) or not w.is_contiguous() or w.get_device() != dev
-            or y.dtype is not _BF16 or tuple(y.shape) != (m, n) or ys[1] != 1 and n > 1 or y.get_device() != dev
-            or residual is not None and (
-                residual.dtype is not _BF16 or tuple(residual.shape) != (m, n) or rs[1] != 1 and n > 1
-                or residual.get_device() != dev)
-            or not _vector_ok(rms_gain, _BF16, k, dev) or not _vector_ok(bias, _BF16, wide, dev)
-            or not _vector_ok(error, _INT32, 1, dev)
+    shape, xs, ys, dev = x.shape, x.stride(), y.stride(), x.get_device()
+    m = shape[0]
+    if (shape != (m, k) or y.shape != (m, n) or w.shape != (wide, k) or x.dtype is not _BF16 or w.dtype is not _BF16
+            or y.dtype is not _BF16 or xs[1] != 1 and k > 1 or ys[1] != 1 and n > 1 or not w.is_contiguous()
+            or w.get_device() != dev or y.get_device() != dev
+            or rms_gain is not None and not _vector_ok(rms_gain, _BF16, k, dev)
+            or bias is not None and not _vector_ok(bias, _BF16, wide, dev)
+            or error is not None and not _vector_ok(error, _INT32, 1, dev)
             or ws is not None and (not ws.is_contiguous() or ws.get_device() != dev)
             or dev != torch._C._cuda_getDevice()):
         raise DllmError("dllm_linear", DLLM_ERR_INVALID_ARGUMENT)
+    rp, rs = None, n
+    if residual is not None:
+        st = residual.stride()
+        if (residual.dtype is not _BF16 or residual.shape != (m, n) or st[1] != 1 and n > 1
+                or residual.get_device() != dev):
+            raise DllmError("dllm_linear", DLLM_ERR_INVALID_ARGUMENT)
+        rp, rs = residual.data_ptr(), st[0] if m > 1 else n
     status = (_lib or load()).dllm_linear(
         layer, m, x.data_ptr(), xs[0] if m > 1 else k, None if rms_gain is None else rms_gain.data_ptr(), w.data_ptr(),
-        None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
-        rs[0] if m > 1 else n, y.data_ptr(), ys[0] if m > 1 else n, None if error is None else error.data_ptr(),
-        None if ws is None else ws.data_ptr(), 0 if ws is None else ws.nbytes, _on(dev, stream))
+        None if bias is None else bias.data_ptr(), rp, rs, y.data_ptr(), ys[0] if m > 1 else n,
+        None if error is None else error.data_ptr(), None if ws is None else ws.data_ptr(),
+        0 if ws is None else ws.nbytes, _on(dev, stream))
     if status:
         raise DllmError("dllm_linear", status)
 
@@ -450,9 +455,12 @@ def _head_rows(t, out, gain, m: int, d: int, dev: int):
     ts, os_, shape = t.stride(), out.stride(), t.shape
     if (len(ts) != 3 or shape != out.shape or shape[0] != m or shape[2] != d or ts[2] != 1 or os_[2] != 1
             or t.dtype is not _BF16 or out.dtype is not _BF16 or t.get_device() != dev or out.get_device() != dev
-            or not _vector_ok(gain, _BF16, d, dev)):
+            or gain is not None and not _vector_ok(gain, _BF16, d, dev)):
         return None
     h = shape[1]
+    if m > 1 and h > 1:
+        return HeadRowsC(t.data_ptr(), ts[0], ts[1], out.data_ptr(), os_[0], os_[1],
+                         None if gain is None else gain.data_ptr(), h)
     return HeadRowsC(t.data_ptr(), ts[0] if m > 1 else h * d, ts[1] if h > 1 else d, out.data_ptr(),
                      os_[0] if m > 1 else h * d, os_[1] if h > 1 else d, None if gain is None else gain.data_ptr(), h)
 
@@ -462,13 +470,12 @@ def dllm_head_norm_rope(desc, q: torch.Tensor, q_out, k, k_out, row_pos, rope_ta
     """q, q_out: bf16 [M][n_heads][head_dim], k, k_out: bf16 [M][any number of heads][head_dim] or None, the last
     dimension contiguous, outputs the inputs themselves or apart from them; row_pos: contiguous int32 of M positions
     (more are fine); rope_table: contiguous float32 [positions][rotary_dim / 2][2]; gains: bf16 [head_dim] or None."""
-    d, m, dev = desc.head_dim, q.shape[0], q.get_device()
+    d, m, dev, ts = desc.head_dim, q.shape[0], q.get_device(), rope_table.shape
     queries = _head_rows(q, q_out, q_gain, m, d, dev)
     keys = None if k is None else _head_rows(k, k_out, k_gain, m, d, dev)
-    ts = rope_table.shape
-    if (queries is None or k is not None and keys is None or not _vector_ok(row_pos, _INT32, m, dev) or row_pos is None
+    if (queries is None or k is not None and keys is None or row_pos is None or not _vector_ok(row_pos, _INT32, m, dev)
             or rope_table.dtype is not _FP32 or len(ts) != 3 or ts[2] != 2 or not rope_table.is_contiguous()
-            or rope_table.get_device() != dev or not _vector_ok(error, _INT32, 1, dev)
+            or rope_table.get_device() != dev or error is not None and not _vector_ok(error, _INT32, 1, dev)
             or dev != torch._C._cuda_getDevice()):
         raise DllmError("dllm_head_norm_rope", DLLM_ERR_INVALID_ARGUMENT)
     status = (_lib or load()).dllm_head_norm_rope(
@@ -483,26 +490,27 @@ def dllm_token_scores(logits: torch.Tensor, tokens=None, logp=None, lse=None, en
     """logits: bf16 or float32 [M][vocab], any row stride; tokens: int32 and logp: float32 of M values, or both None;
     lse, entropy: float32 of M values or None; top_ids: contiguous int32 and top_logp: contiguous float32 [M][top_k], or
     both None."""
-    dev, shape, ls = logits.get_device(), logits.shape, logits.stride()
+    dev, shape, ls, dtype = logits.get_device(), logits.shape, logits.stride(), logits.dtype
     if len(shape) != 2:
         raise DllmError("dllm_token_scores", DLLM_ERR_INVALID_ARGUMENT)
     m, vocab = shape
     top = 0 if top_ids is None else top_ids.shape[-1]
-    if (logits.dtype is not _BF16 and logits.dtype is not _FP32 or ls[1] != 1 and vocab > 1
+    if (dtype is not _BF16 and dtype is not _FP32 or ls[1] != 1 and vocab > 1
             or (tokens is None) != (logp is None) or (top_ids is None) != (top_logp is None)
-            or top_ids is not None and (tuple(top_ids.shape) != (m, top) or tuple(top_logp.shape) != (m, top))
-            or not _vector_ok(tokens, _INT32, m, dev) or not _vector_ok(logp, _FP32, m, dev)
-            or not _vector_ok(lse, _FP32, m, dev) or not _vector_ok(entropy, _FP32, m, dev)
-            or not _vector_ok(top_ids, _INT32, m * top, dev) or not _vector_ok(top_logp, _FP32, m * top, dev)
-            or not _vector_ok(error, _INT32, 1, dev) or dev != torch._C._cuda_getDevice()):
+            or top_ids is not None and (
+                top_ids.shape != (m, top) or top_logp.shape != (m, top) or not _vector_ok(top_ids, _INT32, m * top, dev)
+                or not _vector_ok(top_logp, _FP32, m * top, dev))
+            or tokens is not None and (not _vector_ok(tokens, _INT32, m, dev) or not _vector_ok(logp, _FP32, m, dev))
+            or lse is not None and not _vector_ok(lse, _FP32, m, dev)
+            or entropy is not None and not _vector_ok(entropy, _FP32, m, dev)
+            or error is not None and not _vector_ok(error, _INT32, 1, dev) or dev != torch._C._cuda_getDevice()):
         raise DllmError("dllm_token_scores", DLLM_ERR_INVALID_ARGUMENT)
     status = (_lib or load()).dllm_token_scores(
-        m, vocab, logits.data_ptr(), DLLM_TYPE_BF16 if logits.dtype is _BF16 else DLLM_TYPE_FP32,
-        ls[0] if m > 1 else vocab, scale, None if tokens is None else tokens.data_ptr(),
-        None if logp is None else logp.data_ptr(), None if lse is None else lse.data_ptr(),
-        None if entropy is None else entropy.data_ptr(), top, None if top_ids is None else top_ids.data_ptr(),
-        None if top_logp is None else top_logp.data_ptr(), None if error is None else error.data_ptr(),
-        _on(dev, stream))
+        m, vocab, logits.data_ptr(), DLLM_TYPE_BF16 if dtype is _BF16 else DLLM_TYPE_FP32, ls[0] if m > 1 else vocab,
+        scale, None if tokens is None else tokens.data_ptr(), None if logp is None else logp.data_ptr(),
+        None if lse is None else lse.data_ptr(), None if entropy is None else entropy.data_ptr(), top,
+        None if top_ids is None else top_ids.data_ptr(), None if top_logp is None else top_logp.data_ptr(),
+        None if error is None else error.data_ptr(), _on(dev, stream))
     if status:
         raise DllmError("dllm_token_scores", status)
 
