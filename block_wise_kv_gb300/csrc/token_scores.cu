@@ -83,6 +83,7 @@ struct Piece<float> {
     p[0] = make_float2(max_nan(__uint_as_float(u.x), kLow), max_nan(__uint_as_float(u.y), kLow));
     p[1] = make_float2(max_nan(__uint_as_float(u.z), kLow), max_nan(__uint_as_float(u.w), kLow));
   }
+  static __device__ __forceinline__ uint4 none() { return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u); }
   static __device__ __forceinline__ float one(const float* p) { return __ldg(p); }
   static __device__ __forceinline__ uint32_t bits(const float* p) { return __float_as_uint(__ldg(p)); }
 };
@@ -108,6 +109,7 @@ struct Piece<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = unpack2(max_nan_bf16x2(w[i], kLow2));
   }
+  static __device__ __forceinline__ uint4 none() { return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
   static __device__ __forceinline__ uint32_t bits(const __nv_bfloat16* p) {
     return __ldg(reinterpret_cast<const unsigned short*>(p));
   }
@@ -319,9 +321,17 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 3 : 4) token_scores_ker
       for (int b = 0; b < kBatch; ++b)
         cp_async16(smem_u32(ring + (place * kBatch + b) * kThreads), next + b * stretch * N);
     } else if (i < steps) {
-#pragma unroll 1
-      for (int b = 0; b < kBatch; ++b)
-        ring[(place * kBatch + b) * kThreads] = row.get(v_first + (i * kBatch + b) * stretch);
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int v = v_first + (i * kBatch + b) * stretch;
+        uint4* place_b = ring + (place * kBatch + b) * kThreads;
+        if (v >= row.pieces)
+          *place_b = Piece<T>::none();
+        else if (row.whole(v))
+          cp_async16(smem_u32(place_b), next + b * stretch * N);
+        else
+          *place_b = row.edge(v);
+      }
     }
     next += kBatch * stretch * N;
     asm volatile("cp.async.commit_group;" ::: "memory");
