@@ -7,8 +7,9 @@
 // A team takes a row: a CTA, or where rows are many a warp, or where they are few a cluster
 // of up to eight CTAs (each every eighth stretch of the row, the first one joins what they
 // leave in its shared memory).  A thread takes 16-byte pieces, a stretch apart, four at a
-// time, through places of its own in shared memory that are filled two steps ahead (no
-// thread waits for another), and keeps its running (reference, s, a), raised once a step.
+// time with the next four on their way, and keeps its running (reference, s, a), raised once
+// a step.  (In places of its own in shared memory, filled two steps ahead, they cost as many
+// instructions again: 512 rows of 126464 took 31.0 us, not 26.6.)
 // Exponents are powers of two: u = x c log2 e - R is one FMA from the reference R, two
 // elements to an instruction.
 //
@@ -28,9 +29,7 @@ namespace dllm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;          // pieces of a step
-constexpr int kRing = 3;           // steps a thread has in shared memory or on their way there
-constexpr int kRingBytes = kRing * kBatch * kThreads * 16;
+constexpr int kBatch = 4;  // pieces of a step
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -45,9 +44,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 // max that keeps a NaN
 __device__ __forceinline__ float max_nan(float x, float y) {
   float z;
@@ -282,11 +278,9 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 3 : 4) token_scores_ker
   constexpr int N = Piece<T>::N, kTeams = kThreads / TEAM;
   using Sh = Shared<TEAM>;
   __shared__ Sh shared[kTeams];
-  extern __shared__ uint4 ring_all[];
   const int team = static_cast<int>(threadIdx.x) / TEAM, tid = static_cast<int>(threadIdx.x) % TEAM;
   const int lane = tid & 31, warp = tid >> 5;
   Sh& sh = shared[team];
-  uint4* const ring = ring_all + threadIdx.x;  // this thread's places, kThreads apart
   const int rank = CLUSTER ? static_cast<int>(blockIdx.x) % cluster : 0;
   const int stretch = CLUSTER ? TEAM * cluster : TEAM;
   const float c = fminf(a.scale * kLog2e, 3.402823466e38f);
@@ -314,34 +308,20 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 3 : 4) token_scores_ker
   const int to = whole_to > 0 ? (whole_to + kBatch * stretch - 1) / (kBatch * stretch) : 0;
   const int from = row.lead > 0 && v_first == 0 ? 1 : 0;
   const T* next = row.p + static_cast<int64_t>(row.first(v_first));
-  // step i's pieces to their places (those behind the row's last: all -inf)
-  auto ask = [&](int i, int place) {
+  auto ask = [&](int i, uint4 (&q)[kBatch]) {
     if (i >= from && i < to) {
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-        cp_async16(smem_u32(ring + (place * kBatch + b) * kThreads), next + b * stretch * N);
+      for (int b = 0; b < kBatch; ++b) q[b] = __ldg(reinterpret_cast<const uint4*>(next + b * stretch * N));
     } else if (i < steps) {
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
         const int v = v_first + (i * kBatch + b) * stretch;
-        uint4* place_b = ring + (place * kBatch + b) * kThreads;
-        if (v >= row.pieces)
-          *place_b = Piece<T>::none();
-        else if (row.whole(v))
-          cp_async16(smem_u32(place_b), next + b * stretch * N);
-        else
-          *place_b = row.edge(v);
+        q[b] = v >= row.pieces ? Piece<T>::none() : row.whole(v) ? row.load(v) : row.edge(v);
       }
     }
     next += kBatch * stretch * N;
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto step = [&](int i, int place) {
-    ask(i + kRing - 1, (place + kRing - 1) % kRing);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-    uint4 q[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b) q[b] = ring[(place * kBatch + b) * kThreads];
+  auto step = [&](int i, const uint4 (&q)[kBatch]) {
     float most = m;
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
@@ -371,13 +351,16 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 3 : 4) token_scores_ker
       }
     }
   };
-#pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) ask(i, i);
+  uint4 qa[kBatch], qb[kBatch];
+  ask(0, qa);
 #pragma unroll 1
-  for (int i = 0; i < steps; i += kRing) {
-#pragma unroll
-    for (int k = 0; k < kRing; ++k)
-      if (k == 0 || i + k < steps) step(i + k, k);
+  for (int i = 0; i < steps; i += 2) {
+    ask(i + 1, qb);
+    step(i, qa);
+    if (i + 1 < steps) {
+      ask(i + 2, qa);
+      step(i + 1, qb);
+    }
   }
   const uint64_t best = key_of(top, v_first + top_v * stretch);
   Stat<false> t = {r, s2.x + s2.y, a2.x + a2.y};
@@ -400,7 +383,6 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 3 : 4) token_scores_ker
     if (best != 0 && best >= bound) sh.owners[atomicAdd(&sh.n_owners, 1)] = tid;
     team_sync<TEAM>();
     const int no = sh.n_owners, each = (row.pieces + stretch - 1) / stretch;
-    const bool here = steps <= kRing;  // the whole row is still in the ring
     for (int i0 = tid; i0 < no * each; i0 += 2 * TEAM) {
       int v[2];
       uint4 u[2];
@@ -411,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 3 : 4) token_scores_ker
         if (i < no * each) {
           const int o = sh.owners[i - q * no];
           v[k] = o + rank * TEAM + q * stretch;
-          if (v[k] < row.pieces) u[k] = here ? ring_all[q * kThreads + team * TEAM + o] : row.get(v[k]);
+          if (v[k] < row.pieces) u[k] = row.get(v[k]);
         }
       }
 #pragma unroll
@@ -543,13 +525,10 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 3 : 4) token_scores_ker
 template <typename T, int TEAM, bool CLUSTER>
 cudaError_t launch_scores(const ScoreArgs& a, int cluster, cudaStream_t stream) {
   const auto kernel = token_scores_kernel<T, TEAM, CLUSTER>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-  if (e != cudaSuccess) return e;
   constexpr int kTeams = kThreads / TEAM;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(CLUSTER ? a.rows * cluster : (a.rows + kTeams - 1) / kTeams);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kRingBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
