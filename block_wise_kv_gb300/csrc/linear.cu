@@ -485,6 +485,21 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Rows that do not lie on 16-byte boundaries go two elements a lane: those of a word, or, where the row begins in the middle
+// of one, of the words behind that and (the last lane) the two at its ends.
+struct Pair {
+  int a, b;
+  bool apart;
+};
+__device__ __forceinline__ Pair pair_of(const void* row, int lane) {
+  const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(row) >> 1) & 1;
+  if (odd && lane == 31) return {0, kStageCols - 1, true};
+  return {2 * lane + odd, 2 * lane + 1 + odd, false};
+}
+__device__ __forceinline__ uint16_t* at_stage(uint8_t* stage, int row, int e) {
+  return reinterpret_cast<uint16_t*>(stage + sw128_offset(row, e >> 3)) + (e & 7);
+}
+
 // Columns [c0, c0 + kStageCols) of 32 rows of y or the residual, as one warp moves them to or from its staging
 // tile (rows of 128 bytes, 16-byte pieces swizzled by the row).
 __device__ __forceinline__ void residual_to_stage(const LinearArgs& a, bool vec, uint8_t* stage, int64_t row0, int c0,
@@ -503,19 +518,37 @@ __device__ __forceinline__ void residual_to_stage(const LinearArgs& a, bool vec,
       }
     }
   } else {
-    for (int row = 0; row < 32 && row0 + row < a.rows; ++row)
+    const int rows = static_cast<int>(a.rows - row0 < 32 ? a.rows - row0 : 32), last = min(cols, a.n - c0);
+    const uint16_t* p0 = reinterpret_cast<const uint16_t*>(r) + row0 * a.r_stride + c0;
+#pragma unroll 1
+    for (int from = 0; from < rows; from += 8) {  // eight rows on their way before any is put down
+      uint32_t v[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int e = h * 32 + lane, c = c0 + e;
-        if (e < cols && c < a.n)
-          reinterpret_cast<__nv_bfloat16*>(stage + sw128_offset(row, e >> 3))[e & 7] = r[(row0 + row) * a.r_stride + c];
+      for (int i = 0; i < 8; ++i) {
+        const uint16_t* p = p0 + (from + i) * a.r_stride;
+        const Pair e = pair_of(p, lane);
+        v[i] = 0;
+        if (from + i >= rows) continue;
+        if (e.b < last && !e.apart) {
+          v[i] = *reinterpret_cast<const uint32_t*>(p + e.a);
+        } else {
+          if (e.a < last) v[i] = p[e.a];
+          if (e.b < last) v[i] |= static_cast<uint32_t>(p[e.b]) << 16;
+        }
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const Pair e = pair_of(p0 + (from + i) * a.r_stride, lane);
+        *at_stage(stage, from + i, e.a) = static_cast<uint16_t>(v[i]);
+        *at_stage(stage, from + i, e.b) = static_cast<uint16_t>(v[i] >> 16);
+      }
+    }
   }
   cp_async_commit();
 }
 
-__device__ __forceinline__ void stage_to_y(const LinearArgs& a, bool vec, const uint8_t* stage, int64_t row0, int c0,
-                                           int cols, int lane) {
+__device__ __forceinline__ void stage_to_y(const LinearArgs& a, bool vec, uint8_t* stage, int64_t row0, int c0, int cols,
+                                           int lane) {
   __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y);
   if (vec) {
 #pragma unroll
@@ -534,14 +567,29 @@ __device__ __forceinline__ void stage_to_y(const LinearArgs& a, bool vec, const 
       }
     }
   } else {
-    for (int row = 0; row < 32 && row0 + row < a.rows; ++row)
+    const int rows = static_cast<int>(a.rows - row0 < 32 ? a.rows - row0 : 32), last = min(cols, a.n - c0);
+    uint16_t* p0 = reinterpret_cast<uint16_t*>(y) + row0 * a.y_stride + c0;
+#pragma unroll 1
+    for (int from = 0; from < rows; from += 8) {
+      uint32_t v[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int e = h * 32 + lane, c = c0 + e;
-        if (e < cols && c < a.n)
-          y[(row0 + row) * a.y_stride + c] =
-              reinterpret_cast<const __nv_bfloat16*>(stage + sw128_offset(row, e >> 3))[e & 7];
+      for (int i = 0; i < 8; ++i) {
+        const Pair e = pair_of(p0 + (from + i) * a.y_stride, lane);
+        v[i] = *at_stage(stage, from + i, e.a) | static_cast<uint32_t>(*at_stage(stage, from + i, e.b)) << 16;
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint16_t* p = p0 + (from + i) * a.y_stride;
+        const Pair e = pair_of(p, lane);
+        if (from + i >= rows) continue;
+        if (e.b < last && !e.apart) {
+          *reinterpret_cast<uint32_t*>(p + e.a) = v[i];
+        } else {
+          if (e.a < last) p[e.a] = static_cast<uint16_t>(v[i]);
+          if (e.b < last) p[e.b] = static_cast<uint16_t>(v[i] >> 16);
+        }
+      }
+    }
   }
 }
 
