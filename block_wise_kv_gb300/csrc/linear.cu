@@ -98,7 +98,7 @@ __device__ __forceinline__ float bf16_at(const void* p, int64_t i) {
 }
 
 // ------------------------------------------------------------ few rows
-constexpr int kThreads = 224;
+constexpr int kThreads = 224;       // warps: W, MMAs, four that make y, x
 constexpr int kBK = 64;
 constexpr int kTW = 128;                 // rows of W to a tile (tcgen05 M)
 constexpr int kABytes = kTW * kBK * 2;
@@ -433,7 +433,9 @@ constexpr int kHalfBytes = 128 * kBK * 2;  // a CTA's half of an operand's box, 
 constexpr int kPairStage = 2 * kHalfBytes;
 constexpr int kStageCols = 64;           // columns of y in a staging tile: 128-byte rows
 constexpr int kStageTile = 32 * kStageCols * 2;
-constexpr int kPairSmem = kPairStages * kPairStage + 4 * 2 * kStageTile + 1024;
+constexpr int kPairWarps = 8;           // that make y: two to a quadrant of TMEM's lanes, every other kStageCols columns each
+constexpr int kPairThreads = 32 * (kPairWarps + 3);
+constexpr int kPairSmem = kPairStages * kPairStage + kPairWarps * kStageTile + 1024;
 
 struct TilesPlan {
   int bn;      // rows of W to a tile: a multiple of 32, at most 256
@@ -500,53 +502,62 @@ __device__ __forceinline__ uint16_t* at_stage(uint8_t* stage, int row, int e) {
   return reinterpret_cast<uint16_t*>(stage + sw128_offset(row, e >> 3)) + (e & 7);
 }
 
-// Columns [c0, c0 + kStageCols) of 32 rows of y or the residual, as one warp moves them to or from its staging
-// tile (rows of 128 bytes, 16-byte pieces swizzled by the row).
-__device__ __forceinline__ void residual_to_stage(const LinearArgs& a, bool vec, uint8_t* stage, int64_t row0, int c0,
-                                                  int cols, int lane) {
-  const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(a.residual);
-  if (vec) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = i * 4 + lane / 8, piece = lane & 7, c = c0 + piece * 8;
-      if (row0 + row >= a.rows || piece * 8 >= cols) continue;
-      const __nv_bfloat16* p = r + (row0 + row) * a.r_stride + c;
-      if (c + 8 <= a.n) {
-        cp_async16(smem_u32(stage) + sw128_offset(row, piece), p);
-      } else {
-        for (int e = 0; c + e < a.n; ++e) reinterpret_cast<__nv_bfloat16*>(stage + sw128_offset(row, piece))[e] = p[e];
-      }
-    }
-  } else {
-    const int rows = static_cast<int>(a.rows - row0 < 32 ? a.rows - row0 : 32), last = min(cols, a.n - c0);
-    const uint16_t* p0 = reinterpret_cast<const uint16_t*>(r) + row0 * a.r_stride + c0;
-#pragma unroll 1
-    for (int from = 0; from < rows; from += 8) {  // eight rows on their way before any is put down
-      uint32_t v[8];
+// The residual of kStageCols columns of 32 rows, as a warp asks for it and then has it in its staging tile (rows of 128
+// bytes, 16-byte pieces swizzled by the row).  Rows on 16-byte boundaries come in pieces.  Others come in words: where a row
+// begins in the middle of one, element e lies at place e + 1, the last at place 0, and the elements that share a word with
+// another row's or chunk's come through a register of the row's lane.
+struct Residual {
+  uint32_t first, last;
+  int n, rows;
+
+  static __device__ __forceinline__ int odd(const void* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 1; }
+
+  // p: the chunk's first element of the first row; cols: columns that exist
+  __device__ __forceinline__ void ask(const LinearArgs& a, bool vec, uint8_t* stage, const uint16_t* p, int64_t row0, int cols,
+                                      int lane) {
+    n = min(kStageCols, cols);
+    rows = static_cast<int>(a.rows - row0 < 32 ? a.rows - row0 : 32);
+    if (vec) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint16_t* p = p0 + (from + i) * a.r_stride;
-        const Pair e = pair_of(p, lane);
-        v[i] = 0;
-        if (from + i >= rows) continue;
-        if (e.b < last && !e.apart) {
-          v[i] = *reinterpret_cast<const uint32_t*>(p + e.a);
+        const int row = i * 4 + lane / 8, e = (lane & 7) * 8;
+        if (row >= rows || e >= n) continue;
+        const uint16_t* from = p + row * a.r_stride + e;
+        if (e + 8 <= n) {
+          cp_async16(smem_u32(stage) + sw128_offset(row, lane & 7), from);
         } else {
-          if (e.a < last) v[i] = p[e.a];
-          if (e.b < last) v[i] |= static_cast<uint32_t>(p[e.b]) << 16;
+          for (int k = 0; e + k < n; ++k) at_stage(stage, row, e)[k] = from[k];
         }
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const Pair e = pair_of(p0 + (from + i) * a.r_stride, lane);
-        *at_stage(stage, from + i, e.a) = static_cast<uint16_t>(v[i]);
-        *at_stage(stage, from + i, e.b) = static_cast<uint16_t>(v[i] >> 16);
+    } else {
+#pragma unroll 8
+      for (int row = 0; row < 32; ++row) {
+        const uint16_t* from = p + row * a.r_stride;
+        const int o = odd(from), e = 2 * lane + o;
+        if (row < rows && e + 1 < n)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(at_stage(stage, row, e + o))), "l"(from + e)
+                       : "memory");
       }
+      const uint16_t* from = p + lane * a.r_stride;
+      const int o = odd(from);
+      first = last = 0;
+      if (lane < rows && o) first = from[0];
+      if (lane < rows && ((n ^ o) & 1)) last = from[n - 1];
     }
+    cp_async_commit();
   }
-  cp_async_commit();
-}
+  __device__ __forceinline__ void settle(const LinearArgs& a, bool vec, uint8_t* stage, const uint16_t* p, int lane) {
+    cp_async_wait<0>();
+    if (!vec && lane < rows) {
+      const int o = odd(p + lane * a.r_stride);
+      if (o) *at_stage(stage, lane, 1) = static_cast<uint16_t>(first);
+      if ((n ^ o) & 1) *at_stage(stage, lane, (n - 1 + o) & (kStageCols - 1)) = static_cast<uint16_t>(last);
+    }
+    __syncwarp();
+  }
+};
 
+// kStageCols columns of 32 rows of y out of a warp's staging tile.
 __device__ __forceinline__ void stage_to_y(const LinearArgs& a, bool vec, uint8_t* stage, int64_t row0, int c0, int cols,
                                            int lane) {
   __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y);
@@ -603,7 +614,7 @@ __device__ __forceinline__ void tile_at(const TilesPlan& t, int tile, int& wt, i
 }
 
 template <int ACT, bool GATED>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_tiles_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                         const LinearArgs a, const TilesPlan t) {
   extern __shared__ uint8_t smem_raw[];
@@ -623,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull_bar[i], 1);
-      mbar_init(&tempty_bar[i], 8);  // rank 0's: the four epilogue warps of both CTAs
+      mbar_init(&tempty_bar[i], 2 * kPairWarps);  // rank 0's: the warps of both CTAs that read it
     }
     fence_barrier_init();
     tma_prefetch_desc(&tm_w);
@@ -642,8 +653,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
 
-  if (warp == 0 || warp == 6) {
-    if (lane == 0) {  // (as above) warp 0 loads W, warp 6 x
+  if (warp == 0 || warp == kPairWarps + 2) {
+    if (lane == 0) {  // (as above) warp 0 loads W, the last one x
       const bool is_w = warp == 0;
       const int half_w = t.bn / 2;
       const uint32_t bytes = 2u * (kHalfBytes + half_w * kBK * 2);
@@ -705,12 +716,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    const int quad = warp & 3;
+    const int quad = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    uint8_t* stage0 = smem + kPairStages * kPairStage + quad * 2 * kStageTile;
+    uint8_t* st = smem + kPairStages * kPairStage + (warp - 2) * kStageTile;
     const bool bias_vec = a.bias != nullptr && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
     const bool has_r = a.residual != nullptr;
     const int out_bn = GATED ? t.bn / 2 : t.bn;
+    Residual res;
     bool ok = true;
     griddep_wait();
     for (int i = 0; i < mine; ++i) {
@@ -720,23 +732,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int w0 = wt * t.bn, n0 = GATED ? w0 / 2 : w0;
       const int64_t row0 = static_cast<int64_t>(xt) * kPairRows + rank * 128 + quad * 32;
       const int cols = min(out_bn, a.n - n0);  // of y
-      if (has_r) residual_to_stage(a, t.r_vec, stage0, row0, n0, cols, lane);
+      const uint16_t* r0 = has_r ? static_cast<const uint16_t*>(a.residual) + row0 * a.r_stride + n0 : nullptr;
+      const int first = half * kStageCols;
+      const uint32_t empty = mapa_shared(smem_u32(&tempty_bar[buf]), 0);
+      if (has_r && first < cols) res.ask(a, t.r_vec, st, r0 + first, row0, cols - first, lane);
       if (ok && !wait_phase(&tfull_bar[buf], (i >> 1) & 1)) {
         report_error(a.err, kErrTimeout);
         ok = false;
       }
       tc_fence_after();
-      for (int c0 = 0, sb = 0; c0 < cols; c0 += kStageCols, sb ^= 1) {
-        uint8_t* st = stage0 + sb * kStageTile;
+      for (int c0 = first; c0 < cols; c0 += 2 * kStageCols) {
+        uint32_t shift = 0, last = 0;  // of this lane's row of the residual
         if (has_r) {
-          if (c0 + kStageCols < cols) {
-            residual_to_stage(a, t.r_vec, stage0 + (sb ^ 1) * kStageTile, row0, n0 + c0 + kStageCols,
-                              cols - c0 - kStageCols, lane);
-            cp_async_wait<1>();
-          } else {
-            cp_async_wait<0>();
+          res.settle(a, t.r_vec, st, r0 + c0, lane);
+          if (!t.r_vec) {
+            shift = Residual::odd(r0 + c0 + lane * a.r_stride);
+            last = *at_stage(st, lane, 0);
           }
-          __syncwarp();
         }
         // 32 columns of the accumulator at a time: 32 or (gated) 16 of y
         constexpr int kOut = GATED ? 16 : 32;
@@ -771,7 +783,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint4* p = reinterpret_cast<uint4*>(st + sw128_offset(lane, o0 / 8 + g));
             if (has_r) {
               const uint4 u = *p;
-              const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+              uint32_t w[4] = {u.x, u.y, u.z, u.w};
+              if (shift) {
+                const int piece = o0 / 8 + g;
+                const uint32_t end = piece == 7 ? last : *at_stage(st, lane, 8 * piece + 8);
+                w[0] = w[0] >> 16 | w[1] << 16;
+                w[1] = w[1] >> 16 | w[2] << 16;
+                w[2] = w[2] >> 16 | w[3] << 16;
+                w[3] = w[3] >> 16 | end << 16;
+              }
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 o[8 * g + 2 * e] += __uint_as_float(w[e] << 16);
@@ -782,15 +802,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             pack_bf16x2(o[8 * g + 4], o[8 * g + 5]), pack_bf16x2(o[8 * g + 6], o[8 * g + 7]));
           }
         }
-        if (c0 + kStageCols >= cols) {  // the accumulator is read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(mapa_shared(smem_u32(&tempty_bar[buf]), 0));
-        }
+        const int c1 = c0 + 2 * kStageCols;
+        if (c1 >= cols) tc_fence_before();
         __syncwarp();
+        if (c1 >= cols && lane == 0) mbar_arrive_at(empty);  // this warp has read the accumulator
         stage_to_y(a, t.y_vec, st, row0, n0 + c0, min(kStageCols, cols - c0), lane);
         __syncwarp();
+        if (has_r && c1 < cols) res.ask(a, t.r_vec, st, r0 + c1, row0, cols - c1, lane);
       }
+      if (first >= cols && lane == 0) mbar_arrive_at(empty);
     }
   }
   tc_fence_before();
@@ -881,7 +901,7 @@ cudaError_t launch_tiles(const LinearArgs& a, int bn, int num_sms, cudaStream_t 
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * t.pairs);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kPairThreads);
   cfg.dynamicSmemBytes = kPairSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -402,3 +402,19 @@ def test_token_scores_of_many_short_rows(dtype, m, v, top):
     got, bits = _scores(x, tokens, top, 1.0)
     assert bits == 0
     lu.assert_scores(got, x, tokens, top, 1.0)
+
+
+@pytest.mark.parametrize("n,pad", [(500, 0), (501, 0), (502, 2), (503, 1), (504, 0), (257, 6), (193, 0), (130, 1)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_linear_rows_on_any_boundary(n, pad, gated):
+    """Rows of y and the residual that begin anywhere, in tiles that end anywhere, into y and in place."""
+    c = Linear(1300, 128, n, "silu", gated, bias=True, residual=True, pad=pad, seed=n + pad)
+    c.call()
+    c.check()
+    before = c.residual.clone()
+    whole = torch.full((1300, n + pad + 1), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = whole[:, 1:n + 1]
+    y.copy_(before)
+    dllm.dllm_linear(c.desc, c.x, c.w, y, bias=c.bias, residual=y)
+    c.check(y, before)
+    assert (whole[:, n + 1:] == 7.0).all() and (whole[:, 0] == 7.0).all()
