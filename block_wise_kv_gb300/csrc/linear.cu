@@ -17,6 +17,7 @@
 
 #include "layer_ops.cuh"
 #include "norm.cuh"
+#include "pairs.cuh"
 #include "sm103.cuh"
 #include "tmap.cuh"
 
@@ -26,10 +27,10 @@ namespace {
 // ------------------------------------------------------------ RMSNorm
 constexpr int kNormThreads = 256;
 
-// x (s_hi + s_lo) g for 8 elements, correctly rounded to bf16.  t = x g is exact, t s_hi + t s_lo = p + e with |e| up to
-// a step of p (half of one from p's rounding, half from s_lo); a second sum leaves |e| at most half a step, so that p alone
-// decides unless it lies on a bf16 midpoint, where the sign of e does.
-__device__ __forceinline__ uint4 normed8(const uint4& u, const uint4& gu, float s_hi, float s_lo) {
+// x (s_hi + s_lo) g for 8 elements, correctly rounded to bf16.  t = x g is exact, p = fl(t s_hi) is off by a step or so (half
+// of one from its rounding, half from s_lo): its own rounding is the right one unless it lies within two steps of a bf16
+// midpoint, as one in 13000 does.
+__device__ __noinline__ uint4 normed8_near(const uint4& u, const uint4& gu, float s_hi, float s_lo) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w}, gw[4] = {gu.x, gu.y, gu.z, gu.w};
   uint32_t o[4];
 #pragma unroll
@@ -42,6 +43,8 @@ __device__ __forceinline__ uint4 normed8(const uint4& u, const uint4& gu, float 
       const float t = __fmul_rn(xf, gv);
       const float p0 = __fmul_rn(t, s_hi);
       const float e0 = __fmaf_rn(t, s_lo, __fmaf_rn(t, s_hi, -p0));
+      // a second sum leaves |e| at most half a step, so that p alone decides unless it lies on the midpoint, where the
+      // sign of e does
       const float p = __fadd_rn(p0, e0), e = __fsub_rn(e0, __fsub_rn(p, p0));
       const uint32_t bits = __float_as_uint(p);
       const uint32_t rn = __bfloat16_as_ushort(__float2bfloat16_rn(p));
@@ -53,43 +56,74 @@ __device__ __forceinline__ uint4 normed8(const uint4& u, const uint4& gu, float 
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
+__device__ __forceinline__ uint4 normed8(const uint4& u, const uint4& gu, float s_hi, float s_lo) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w}, gw[4] = {gu.x, gu.y, gu.z, gu.w};
+  uint32_t o[4];
+  bool near = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = mul2(mul2(unpack2(w[i]), unpack2(gw[i])), {s_hi, s_hi});
+    near |= (__float_as_uint(p.x) & 0xFFFFu) - 0x7FFEu <= 4u;
+    near |= (__float_as_uint(p.y) & 0xFFFFu) - 0x7FFEu <= 4u;
+    o[i] = pack_bf16x2(p.x, p.y);
+  }
+  return near ? normed8_near(u, gu, s_hi, s_lo) : make_uint4(o[0], o[1], o[2], o[3]);
+}
 
+// A row to TEAM threads: a thread's pieces of 8 elements are a chain of eight exact sums each.
+template <int TEAM>
 __global__ void __launch_bounds__(kNormThreads) linear_norm_kernel(const LinearArgs a) {
+  constexpr int kTeams = kNormThreads / TEAM;
   __shared__ float2 part[kNormThreads / 32];
-  __shared__ float2 scale;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nvec = a.k / 8;
   griddep_launch_dependents();  // the product behind reads nothing before its own wait
   griddep_wait();
-  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + blockIdx.x * a.x_stride);
-  uint4* out = static_cast<uint4*>(a.xhat) + static_cast<size_t>(blockIdx.x) * nvec;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kTeams + threadIdx.x / TEAM;
+  const bool there = row < a.rows;
+  const int l = there ? threadIdx.x % TEAM : nvec;
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (there ? row : 0) * a.x_stride);
+  uint4* out = static_cast<uint4*>(a.xhat) + row * nvec;
   const uint4* g = static_cast<const uint4*>(a.gain);
   float hi = 0.f, lo = 0.f;
-  for (int v = threadIdx.x; v < nvec; v += kNormThreads) sumsq_pair_add(__ldg(x + v), hi, lo);
+#pragma unroll 2
+  for (int v = l; v < nvec; v += TEAM) sumsq_pair_add(__ldg(x + v), hi, lo);
 #pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) {
     const float oh = __shfl_xor_sync(0xffffffffu, hi, o), ol = __shfl_xor_sync(0xffffffffu, lo, o);
     pair_add(hi, lo, oh, ol);
   }
-  if (lane == 0) part[warp] = make_float2(hi, lo);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kNormThreads / 32; ++w) pair_add(hi, lo, part[w].x, part[w].y);
-    two_sum(hi, lo, hi, lo);
-    float2 s;
-    rsqrt_pair(hi, lo, a.k, a.rms_eps, s.x, s.y);
-    scale = s;
+  hi = __shfl_sync(0xffffffffu, hi, 0);  // lane 0's sum is the warp's
+  lo = __shfl_sync(0xffffffffu, lo, 0);
+  if (TEAM > 32) {
+    if (lane == 0) part[warp] = make_float2(hi, lo);
+    __syncthreads();
+    const int w0 = threadIdx.x / TEAM * (TEAM / 32);
+    hi = part[w0].x;
+    lo = part[w0].y;
+    for (int w = 1; w < TEAM / 32; ++w) pair_add(hi, lo, part[w0 + w].x, part[w0 + w].y);
   }
-  __syncthreads();
-  const float2 s = scale;
-  for (int v = threadIdx.x; v < nvec; v += kNormThreads) out[v] = normed8(__ldg(x + v), __ldg(g + v), s.x, s.y);
+  two_sum(hi, lo, hi, lo);
+  float s_hi, s_lo;
+  rsqrt_pair(hi, lo, a.k, a.rms_eps, s_hi, s_lo);
+#pragma unroll 2
+  for (int v = l; v < nvec; v += TEAM) out[v] = normed8(__ldg(x + v), __ldg(g + v), s_hi, s_lo);
 }
 
 // ------------------------------------------------------------ the epilogue's arithmetic
+// t / (1 + e^-x), by ex2 and a reciprocal that are each off by about 2^-22 (a division and expf cost four times as much).
+__device__ __forceinline__ float times_sigmoid(float t, float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return t * r;
+}
+
+// (1 + tanh u) / 2 is the sigmoid of 2 u.
 template <int ACT>
 __device__ __forceinline__ float activate(float t) {
-  if (ACT == kActSilu) return t / (1.f + expf(-t));
+  if (ACT == kActSilu) return times_sigmoid(t, t);
   if (ACT == kActGelu) return 0.5f * t * (1.f + erff(t * 0.70710678118654752f));
-  if (ACT == kActGeluTanh) return 0.5f * t * (1.f + tanhf(0.79788456080286536f * (t + 0.044715f * t * t * t)));
+  if (ACT == kActGeluTanh) return times_sigmoid(t, 1.5957691216057308f * (t + 0.044715f * t * t * t));
   return t;
 }
 
@@ -364,8 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c0 = 0; c0 < t.bn && x0 + c0 < a.rows; c0 += 16) {
         float v[16];
         tmem_ld_32x32b_x16(src + c0, v);
+        Finish<GATED> next;
+        if (c0 + 16 < t.bn) next.ask(a, wr, x0 + c0 + 16, lane);
         fin.template make<ACT>(a, v, b, wr, x0 + c0, lane);
-        if (c0 + 16 < t.bn) fin.ask(a, wr, x0 + c0 + 16, lane);
+        fin = next;
       }
     }
   } else {
@@ -412,8 +448,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[4 * i + 3] += p.w;
             }
           }
+          Finish<GATED> next;
+          if (c0 + 16 < end) next.ask(a, wr, x0 + c0 + 16, lane);
           fin.template make<ACT>(a, v, b, wr, x0 + c0, lane, x0 + end);
-          if (c0 + 16 < end) fin.ask(a, wr, x0 + c0 + 16, lane);
+          fin = next;
         }
       }
     }
@@ -488,16 +526,20 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // Rows that do not lie on 16-byte boundaries go two elements a lane: those of a word, or, where the row begins in the middle
-// of one, of the words behind that and (the last lane) the two at its ends.
+// of one, of the words behind that and (the last lane) the two at its ends.  With an odd stride every second row does.
 struct Pair {
   int a, b;
-  bool apart;
+  bool word, one_a, one_b;  // both as a word, or one by one
+  __device__ __forceinline__ Pair(int odd, int lane, int n) {
+    const bool ends = odd && lane == 31;
+    a = ends ? 0 : 2 * lane + odd;
+    b = ends ? kStageCols - 1 : a + 1;
+    word = !ends && b < n;
+    one_a = !word && a < n;
+    one_b = !word && b < n;
+  }
 };
-__device__ __forceinline__ Pair pair_of(const void* row, int lane) {
-  const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(row) >> 1) & 1;
-  if (odd && lane == 31) return {0, kStageCols - 1, true};
-  return {2 * lane + odd, 2 * lane + 1 + odd, false};
-}
+__device__ __forceinline__ int odd_address(const void* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 1; }
 __device__ __forceinline__ uint16_t* at_stage(uint8_t* stage, int row, int e) {
   return reinterpret_cast<uint16_t*>(stage + sw128_offset(row, e >> 3)) + (e & 7);
 }
@@ -510,7 +552,7 @@ struct Residual {
   uint32_t first, last;
   int n, rows;
 
-  static __device__ __forceinline__ int odd(const void* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 1; }
+  static __device__ __forceinline__ int odd(const void* p) { return odd_address(p); }
 
   // p: the chunk's first element of the first row; cols: columns that exist
   __device__ __forceinline__ void ask(const LinearArgs& a, bool vec, uint8_t* stage, const uint16_t* p, int64_t row0, int cols,
@@ -530,15 +572,19 @@ struct Residual {
         }
       }
     } else {
-#pragma unroll 8
-      for (int row = 0; row < 32; ++row) {
-        const uint16_t* from = p + row * a.r_stride;
-        const int o = odd(from), e = 2 * lane + o;
-        if (row < rows && e + 1 < n)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(at_stage(stage, row, e + o))), "l"(from + e)
-                       : "memory");
+      const int o_even = odd(p), o_odd = odd(p + a.r_stride);
+      const uint16_t* from = p;
+#pragma unroll 1
+      for (int r0 = 0; r0 < rows; r0 += 8) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i, from += a.r_stride) {
+          const int o = i & 1 ? o_odd : o_even, e = 2 * lane + o, at = e + o;
+          const uint32_t to = smem_u32(stage) + (r0 + i) * 128 + (((at >> 3) << 4) ^ (i << 4)) + (at & 7) * 2;
+          if (r0 + i < rows && e + 1 < n)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from + e) : "memory");
+        }
       }
-      const uint16_t* from = p + lane * a.r_stride;
+      from = p + lane * a.r_stride;
       const int o = odd(from);
       first = last = 0;
       if (lane < rows && o) first = from[0];
@@ -578,27 +624,22 @@ __device__ __forceinline__ void stage_to_y(const LinearArgs& a, bool vec, uint8_
       }
     }
   } else {
-    const int rows = static_cast<int>(a.rows - row0 < 32 ? a.rows - row0 : 32), last = min(cols, a.n - c0);
-    uint16_t* p0 = reinterpret_cast<uint16_t*>(y) + row0 * a.y_stride + c0;
+    const int rows = static_cast<int>(a.rows - row0 < 32 ? a.rows - row0 : 32), n = min(cols, a.n - c0);
+    uint16_t* p = reinterpret_cast<uint16_t*>(y) + row0 * a.y_stride + c0;
+    const Pair even(odd_address(p), lane, n), odd(odd_address(p + a.y_stride), lane, n);  // of the rows 0, 2, ... and 1, 3, ...
 #pragma unroll 1
     for (int from = 0; from < rows; from += 8) {
-      uint32_t v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const Pair e = pair_of(p0 + (from + i) * a.y_stride, lane);
-        v[i] = *at_stage(stage, from + i, e.a) | static_cast<uint32_t>(*at_stage(stage, from + i, e.b)) << 16;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint16_t* p = p0 + (from + i) * a.y_stride;
-        const Pair e = pair_of(p, lane);
+      for (int i = 0; i < 8; ++i, p += a.y_stride) {
+        const Pair& e = i & 1 ? odd : even;
+        // (the address of at_stage, the row's swizzle being i's)
+        const uint8_t* base = stage + from * 128 + i * 128;
+        const uint16_t va = *reinterpret_cast<const uint16_t*>(base + (((e.a >> 3) << 4) ^ (i << 4)) + (e.a & 7) * 2);
+        const uint16_t vb = *reinterpret_cast<const uint16_t*>(base + (((e.b >> 3) << 4) ^ (i << 4)) + (e.b & 7) * 2);
         if (from + i >= rows) continue;
-        if (e.b < last && !e.apart) {
-          *reinterpret_cast<uint32_t*>(p + e.a) = v[i];
-        } else {
-          if (e.a < last) p[e.a] = static_cast<uint16_t>(v[i]);
-          if (e.b < last) p[e.b] = static_cast<uint16_t>(v[i] >> 16);
-        }
+        if (e.word) *reinterpret_cast<uint32_t*>(p + e.a) = va | static_cast<uint32_t>(vb) << 16;
+        if (e.one_a) p[e.a] = va;
+        if (e.one_b) p[e.b] = vb;
       }
     }
   }
@@ -1000,8 +1041,9 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   if (a.rows <= 0) return cudaSuccess;
   const Choice c = choose(a, num_sms);
   if (a.gain != nullptr && !c.norm) {
+    const int team = a.k <= 256 ? 32 : a.k <= 1024 ? 128 : kNormThreads, per_cta = kNormThreads / team;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.rows);
+    cfg.gridDim = dim3((a.rows + per_cta - 1) / per_cta);
     cfg.blockDim = dim3(kNormThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -1009,7 +1051,9 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_norm_kernel, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, team == 32    ? linear_norm_kernel<32>
+                                                   : team == 128 ? linear_norm_kernel<128>
+                                                                 : linear_norm_kernel<kNormThreads>, a);
     if (e != cudaSuccess) return e;
   }
   switch (a.act) {
