@@ -30,7 +30,7 @@ constexpr int kNormThreads = 256;
 // x (s_hi + s_lo) g for 8 elements, correctly rounded to bf16.  t = x g is exact, p = fl(t s_hi) is off by a step or so (half
 // of one from its rounding, half from s_lo): its own rounding is the right one unless it lies within two steps of a bf16
 // midpoint, as one in 13000 does.
-__device__ __noinline__ uint4 normed8_near(const uint4& u, const uint4& gu, float s_hi, float s_lo) {
+__device__ __forceinline__ uint4 normed8_near(const uint4& u, const uint4& gu, float s_hi, float s_lo) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w}, gw[4] = {gu.x, gu.y, gu.z, gu.w};
   uint32_t o[4];
 #pragma unroll
@@ -865,6 +865,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }
 
 // ------------------------------------------------------------ host
+bool rows16(const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0; }
+
 // Shared memory of a CTA: two fit an SM, so that one's loads go on while the other finishes.
 constexpr int kRowsSmem = 108 * 1024;
 
@@ -917,8 +919,6 @@ cudaError_t launch_rows(const LinearArgs& a, const RowsPlan& t, cudaStream_t str
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, linear_rows_kernel<ACT, GATED>, tm_w, tm_x, a, t);
 }
-
-bool rows16(const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0; }
 
 template <int ACT, bool GATED>
 cudaError_t launch_tiles(const LinearArgs& a, int bn, int num_sms, cudaStream_t stream) {
@@ -981,7 +981,8 @@ float rows_us(const LinearArgs& a, int bn, int split, int num_sms) {
   const int64_t waves = (ctas + 2 * num_sms - 1) / (2 * num_sms) + (split > 4 && ctas > 9 * num_sms / 5 ? 1 : 0);
   const float kb = 16.f + bn / 8.f;
   const float box = fmaxf(fmaxf(0.29f, 0.99f / t.stages), kb * 0.0082f * (ctas > num_sms ? 2 : 1));
-  const float one = (t.boxes + split - 1) / split * box + 0.38f + (split > 1 ? 0.46f + 0.045f * bn : 0.033f * bn);
+  const float col = 0.033f + (a.residual != nullptr ? 0.015f : 0.f) + (a.act == kActGelu ? 0.04f : a.act != kActNone ? 0.01f : 0.f);
+  const float one = (t.boxes + split - 1) / split * box + 0.38f + (split > 1 ? 0.46f + (0.035f + 0.3f * col) * bn : col * bn);
   const float dram = static_cast<float>(a.wide) * a.k * 2.f / 6.7e6f + (split > 1 ? 0.46f : 0.f);
   return 2.2f + fmaxf(waves * one, dram) + 0.05f * fminf(waves * one, dram);
 }
@@ -992,7 +993,13 @@ float tiles_us(const LinearArgs& a, int bn, int num_sms) {
   const int64_t waves = (tiles + pairs - 1) / pairs;
   const float busy = tiles < pairs ? static_cast<float>(tiles) / pairs : 1.f;
   const float box = fmaxf(0.287f, (32.f + bn / 4.f) * busy * 0.00307f);
-  const float work = waves * boxes * box + 0.01f * bn, dram = static_cast<float>(a.wide) * a.k * 2.f / 6.7e6f;
+  // making y of a tile, in us for 256 columns: less where it is hidden behind the next tile's MMAs
+  const bool apart = !rows16(a.y, a.y_stride);
+  const float out = 2.6f + (apart ? 2.2f : 0.f) + (a.residual != nullptr ? 1.7f : 0.f) + (a.bias != nullptr ? 0.8f : 0.f) +
+                    (a.act == kActGelu ? 4.7f : a.act != kActNone ? 1.2f : 0.f);
+  const float mma = boxes * box, last = 1.5f + (out - 1.5f) * bn / 256;
+  const float work = (waves - 1) * fmaxf(mma, last) + mma + last;
+  const float dram = static_cast<float>(a.wide) * a.k * 2.f / 6.7e6f;
   return 3.2f + fmaxf(work, dram) + 0.05f * fminf(work, dram);
 }
 
@@ -1006,12 +1013,13 @@ Choice choose(const LinearArgs& a, int num_sms) {
       best = {true, bn, 1, false};
     }
   }
-  if (a.rows > 4096) return best;  // (rows_us does not come near)
   int last = 0;
   for (int most : {128, 96, 64, 48, 32, 16}) {
     const int xt = (a.rows + most - 1) / most, bn = ((a.rows + xt - 1) / xt + 15) / 16 * 16;
     if (bn == last) continue;
     last = bn;
+    // (of many CTAs the pairs' tiles are always the better ones)
+    if (static_cast<int64_t>((a.wide + kTW - 1) / kTW) * xt > 4 * num_sms) continue;
     for (int split : {1, 2, 3, 4, 5, 8}) {
       if (split > (a.k + kBK - 1) / kBK) break;
       const float us = rows_us(a, bn, split, num_sms);
