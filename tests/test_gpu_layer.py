@@ -7,7 +7,7 @@ import torch
 
 import layer_util as lu
 from block_wise_kv_gb300 import dllm
-from kv8_util import Batch, attention, ints, random_pools
+from kv8_util import Batch, assert_attention, ints
 
 pytestmark = pytest.mark.gpu
 ACT = {"none": dllm.DLLM_ACT_NONE, "silu": dllm.DLLM_ACT_SILU, "gelu": dllm.DLLM_ACT_GELU,
@@ -418,3 +418,118 @@ def test_linear_rows_on_any_boundary(n, pad, gated):
     dllm.dllm_linear(c.desc, c.x, c.w, y, bias=c.bias, residual=y)
     c.check(y, before)
     assert (whole[:, n + 1:] == 7.0).all() and (whole[:, 0] == 7.0).all()
+
+
+# ------------------------------------------------------------------ together
+def test_a_captured_step_of_a_layer_of_grouped_heads():
+    """Plan, projection, heads' norm and rotation in place, cache write, attention, output projection, gated feed-forward
+    block, head and scores: captured once, replayed while requests grow, end and come.  Each stage against its 64-bit form on
+    what the stage before it left."""
+    import random
+
+    kv, H, d, D, F, V, batch, width, P = 2, 8, 128, 512, 640, 1003, 5, 12, 30
+    r = random.Random(7)
+    dev = {k: ints([0] * batch) for k in ("n", "start", "rows", "held", "held_out")}
+    dev.update(table=ints([[0] * 8] * batch), cub=ints([0] * (batch + 1)), cus=ints([0] * (batch + 1)), err=ints([0]))
+    ring, cap = dllm.PageRing.full(P), batch * width
+    pos = ints([-1] * cap)
+    view = dllm.BatchView(dev["table"], dev["n"], dev["start"], dev["rows"], dev["cub"], dev["cus"], cap, batch * 512, width, 512,
+                          dev["err"])
+    kv8 = dllm.Kv8Cache(P, kv, d)
+    desc = dllm.layer_desc(D, H, d, 1e4)
+    w = {k: lu.randn(s, 20 + i, 1 / math.sqrt(s[1])) for i, (k, s) in enumerate(dict(
+        qkv=((H + 2 * kv) * d, D), o=(D, H * d), gu=(2 * F, D), down=(D, F), head=(V, D)).items())}
+    bias, gains = lu.randn(((H + 2 * kv) * d,), 30, 0.2), [(1 + lu.randn((D,), 31 + i, 0.2).float()).bfloat16() for i in range(3)]
+    q_gain, k_gain = lu.randn((d,), 40), lu.randn((d,), 41)
+    table = dllm_table(d, 512)
+    lay = dict(qkv=dllm.linear_desc(D, (H + 2 * kv) * d), o=dllm.linear_desc(H * d, D), down=dllm.linear_desc(F, D),
+               gu=dllm.linear_desc(D, F, dllm.DLLM_ACT_SILU, True), head=dllm.linear_desc(D, V))
+    ws = dllm.workspace(max(dllm.dllm_linear_workspace_size(lay[k], cap, True) for k in ("qkv", "gu", "head")))
+    ws_att = dllm.workspace(dllm.dllm_kv8_attention_workspace_size(desc, view.c, kv8.c))
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    x, qkv, raw, o, h1, a, h2, logits = (bf(cap, n) for n in (D, (H + 2 * kv) * d, (H + 2 * kv) * d, H * d, D, F, D, V))
+    heads = qkv.view(cap, H + 2 * kv, d)
+    q, k, v = heads[:, :H], heads[:, H:H + kv], heads[:, H + kv:]
+    lse = torch.zeros(cap, H, device="cuda")
+    tokens, ids = ints([0] * cap), torch.zeros(cap, 4, dtype=torch.int32, device="cuda")
+    logp, row_lse, entropy, best = (torch.zeros(s, device="cuda") for s in ((cap,), (cap,), (cap,), (cap, 4)))
+
+    def step():
+        dllm.dllm_batch_plan(view.c, dev["held"], dev["held_out"], dev["table"], dev["cub"], dev["cus"], ring.c, row_pos=pos)
+        dllm.dllm_linear(lay["qkv"], x, w["qkv"], qkv, rms_gain=gains[0], bias=bias, ws=ws, error=dev["err"])
+        raw.copy_(qkv)
+        dllm.dllm_head_norm_rope(desc, q, q, k, k, pos, table, q_gain, k_gain, error=dev["err"])
+        dllm.dllm_kv8_write(desc, view.c, k, v, kv8.c)
+        dllm.dllm_kv8_attention(desc, view.c, q, kv8.c, o.view(cap, H, d), lse, ws_att)
+        dllm.dllm_linear(lay["o"], o, w["o"], h1, residual=x, error=dev["err"])
+        dllm.dllm_linear(lay["gu"], h1, w["gu"], a, rms_gain=gains[1], ws=ws, error=dev["err"])
+        dllm.dllm_linear(lay["down"], a, w["down"], h2, residual=h1, error=dev["err"])
+        dllm.dllm_linear(lay["head"], h2, w["head"], logits, rms_gain=gains[2], ws=ws, error=dev["err"])
+        dllm.dllm_token_scores(logits, tokens, logp, row_lse, entropy, ids, best, error=dev["err"])
+        dev["held"].copy_(dev["held_out"])
+        ring.state.copy_(ring.state_out)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()  # nothing planned yet
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+
+    def near(got, want_off):
+        assert ((got.double() - want_off[0]).abs() <= want_off[1]).all()
+
+    n = [0] * batch
+    for i in range(6):
+        new = [r.choice([1, r.randint(0, width)]) for _ in range(batch)]
+        n = [0 if r.random() < 0.1 else y for y in n]
+        start, n = n, [y + c for y, c in zip(n, new)]
+        for key, val in (("n", n), ("start", start), ("rows", new)):
+            dev[key].copy_(ints(val))
+        x.copy_(lu.randn((cap, D), 100 + i))
+        tokens.copy_(_tokens(cap, V, i))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert dev["err"].item() == 0
+        M = sum(new)
+        assert pos.tolist() == [s + j for s, c in zip(start, new) for j in range(c)] + [-1] * (cap - M)
+        near(raw, lu.linear(x, w["qkv"], gains[0], bias))
+        before = raw.view(cap, H + 2 * kv, d)
+        near(q[:M], lu.head_norm_rope(before[:M, :H], q_gain, pos[:M], table, d, False, 1e-5))
+        near(k[:M], lu.head_norm_rope(before[:M, H:H + kv], k_gain, pos[:M], table, d, False, 1e-5))
+        assert torch.equal(heads[M:], before[M:]) and torch.equal(v, before[:, H + kv:])
+        b = Batch([1], [0], [1])
+        b.n, b.start, b.rows, b.table, b.M = n, start, new, dev["table"].tolist(), cap
+        assert_attention(b, q, kv8, o.view(cap, H, d), lse)
+        near(h1, lu.linear(o, w["o"], residual=x))
+        near(a, lu.linear(h1, w["gu"], gains[1], name="silu", gated=True))
+        near(h2, lu.linear(a, w["down"], residual=h1))
+        near(logits, lu.linear(h2, w["head"], gains[2]))
+        lu.assert_scores((row_lse, entropy, logp, ids, best), logits, tokens, 4, 1.0)
+
+
+def dllm_table(d, positions):
+    """cos and sin as the library makes them."""
+    table = torch.zeros(positions, d // 2, 2, device="cuda")
+    dllm.dllm_rope_table_build(dllm.layer_desc(128, 128 // d, d, 1e4), positions, table)
+    assert (table - lu.rope_table(positions, d)).abs().max() < 1e-6
+    return table
+
+
+def test_scores_of_the_block_heads_logits():
+    """Beside dllm_block_lm_head: its log-sum-exp, argmax and confidence are of the logits before their rounding to bf16 (off
+    by at most 2^-8 of the largest); the scores' are of the rounded ones."""
+    n, D, V = 40, 256, 1000
+    lay = dllm.BatchLayout([[0]], [n], [8], [32])
+    desc = dllm.layer_desc(D, 2, 128, 1e4)
+    h, w, gain = lu.randn((n, D), 1), lu.randn((V, D), 2, 0.2), torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    logits = torch.zeros(32, V, dtype=torch.bfloat16, device="cuda")
+    lse, arg, p = torch.zeros(32, device="cuda"), ints([0] * 32), torch.zeros(32, device="cuda")
+    ws = dllm.workspace(dllm.dllm_lm_head_workspace_size(desc, lay.c, V))
+    dllm.dllm_block_lm_head(desc, lay.c, V, h, gain, w, logits, lse, arg, p, ws)
+    (lse2, _, logp, ids, best), bits = _scores(logits, arg, 2, 1.0)
+    assert bits == 0
+    lu.assert_scores((lse2, None, logp, ids, best), logits, arg, 2, 1.0)
+    off = lu.HALF_BF16 * logits.float().abs().amax(1) + 1e-4
+    assert ((lse - lse2).abs() <= off).all() and ((p.log() - logp).abs() <= 2 * off).all()
