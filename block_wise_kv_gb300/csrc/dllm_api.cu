@@ -762,7 +762,9 @@ dllm_status dllm_linear(const dllm_linear_layer* layer, int32_t rows, const void
     if (ws_bytes < need) return DLLM_ERR_WORKSPACE_TOO_SMALL;
     if (!aligned(ws, 256)) return DLLM_ERR_INVALID_ARGUMENT;
     const Extent we = {ws, 1, 0, 1, 0, rows * k};
-    if (may_overlap(we, ye) || may_overlap(we, {x, rows, x_stride, 1, 0, k}) || may_overlap(we, {w, 1, 0, 1, 0, wide * k}))
+    if (may_overlap(we, ye) || may_overlap(we, {x, rows, x_stride, 1, 0, k}) || may_overlap(we, {w, 1, 0, 1, 0, wide * k}) ||
+        may_overlap(we, {rms_gain, 1, 0, 1, 0, k}) || (bias != nullptr && may_overlap(we, {bias, 1, 0, 1, 0, wide})) ||
+        (residual != nullptr && may_overlap(we, {residual, rows, residual_stride, 1, 0, n})))
       return DLLM_ERR_INVALID_ARGUMENT;
   }
   LinearArgs a = {};
@@ -797,6 +799,7 @@ Extent out_extent(const dllm_head_rows* h, int32_t rows, int32_t d) {
 
 dllm_status check_head_rows(const dllm_head_rows* h, int32_t rows, int32_t d) {
   if (h->n_heads < 1) return DLLM_ERR_INVALID_ARGUMENT;
+  if (static_cast<int64_t>(h->n_heads) * d > 65535 * 128) return DLLM_ERR_UNSUPPORTED;  // (as check_desc)
   if (!rows_ok(h->in, h->in_row_stride, h->in_head_stride) || !rows_ok(h->out, h->out_row_stride, h->out_head_stride))
     return DLLM_ERR_INVALID_ARGUMENT;
   if (h->gain != nullptr && !aligned(h->gain, 16)) return DLLM_ERR_INVALID_ARGUMENT;

@@ -625,7 +625,8 @@ dllm_status dllm_head_norm_rope(const dllm_layer_desc* desc, int32_t rows, const
  *   tokens: device int32 [rows]; logp: device fp32 [rows]; both nullable together.
  *   lse, entropy: device fp32 [rows], each nullable.
  *   top_k: 0 to 32; top_ids: device int32 [rows][top_k], top_logp: device fp32
- *   [rows][top_k] (not read or written for top_k 0).
+ *   [rows][top_k] (not read or written for top_k 0).  The outputs overlap
+ *   neither each other nor anything that the call reads.
  * Sums and statistics are fp32, relative to the row's largest logit; the same
  * call gives the same bits. */
 dllm_status dllm_token_scores(int32_t rows, int32_t vocab, const void* logits, int32_t logits_type, int64_t row_stride,

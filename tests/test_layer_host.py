@@ -54,7 +54,9 @@ def test_linear_layer_is_checked(kw, status):
     # y over what the call reads
     (dict(y=A), 1), (dict(y=A + 16), 1), (dict(y=A + FAR), 1), (dict(bias=A + 2 * FAR), 1),
     (dict(r=A + 2 * FAR + 2), 1), (dict(r=A + 2 * FAR, rs=520), 1), (dict(gain=A + FAR, ws=A + 2 * FAR, wsb=1 << 20), 1),
-    (dict(gain=A + FAR, ws=A, wsb=1 << 20), 1)])
+    (dict(gain=A + FAR, ws=A, wsb=1 << 20), 1), (dict(gain=A + FAR, ws=A + FAR, wsb=1 << 20), 1),
+    (dict(gain=A + 5 * FAR, ws=A + 5 * FAR, wsb=1 << 20), 1), (dict(gain=A + 5 * FAR, bias=A + 6 * FAR, ws=A + 6 * FAR, wsb=1 << 20), 1),
+    (dict(gain=A + 5 * FAR, r=A + 6 * FAR, ws=A + 6 * FAR, wsb=1 << 20), 1)])
 def test_linear_arguments_are_checked(kw, status):
     assert _linear(**kw) == status
 
@@ -105,6 +107,8 @@ def test_rope_rows_are_checked(kw, status):
 def test_rope_keys_are_checked():
     assert _rope(k=_rows(A + 2 * FAR, 256, 128, A, 256, 128, None, 2)) == 1      # over the queries' input
     assert _rope(k=_rows(A + 2 * FAR, 256, 128, A + 3 * FAR, 128, 128, None, 2)) == 1
+    many = 1 << 17
+    assert _rope(k=_rows(A + 2 * FAR, many * 128, 128, A + 40 * FAR, many * 128, 128, None, many)) == 2
     assert _rope(rows=0, pos=None) == 0
 
 
