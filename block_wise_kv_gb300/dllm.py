@@ -452,17 +452,26 @@ def dllm_linear(layer, x: torch.Tensor, w, y, rms_gain=None, bias=None, residual
 
 def _head_rows(t, out, gain, m: int, d: int, dev: int):
     """The dllm_head_rows of bf16 tensors [m][heads][d], or None where they do not fit."""
-    ts, os_, shape = t.stride(), out.stride(), t.shape
-    if (len(ts) != 3 or shape != out.shape or shape[0] != m or shape[2] != d or ts[2] != 1 or os_[2] != 1
-            or t.dtype is not _BF16 or out.dtype is not _BF16 or t.get_device() != dev or out.get_device() != dev
-            or gain is not None and not _vector_ok(gain, _BF16, d, dev)):
+    shape = t.shape
+    if (len(shape) != 3 or out.shape != shape or t.dtype is not _BF16 or out.dtype is not _BF16
+            or t.get_device() != dev or out.get_device() != dev):
         return None
-    h = shape[1]
-    if m > 1 and h > 1:
-        return HeadRowsC(t.data_ptr(), ts[0], ts[1], out.data_ptr(), os_[0], os_[1],
-                         None if gain is None else gain.data_ptr(), h)
-    return HeadRowsC(t.data_ptr(), ts[0] if m > 1 else h * d, ts[1] if h > 1 else d, out.data_ptr(),
-                     os_[0] if m > 1 else h * d, os_[1] if h > 1 else d, None if gain is None else gain.data_ptr(), h)
+    rows, h, width = shape
+    ti, th, te = t.stride()
+    oi, oh, oe = out.stride()
+    if rows != m or width != d or te != 1 or oe != 1:
+        return None
+    if gain is None:
+        g = None
+    elif gain.dtype is _BF16 and gain.numel() >= d and gain.is_contiguous() and gain.get_device() == dev:
+        g = gain.data_ptr()
+    else:
+        return None
+    if m == 1:
+        ti = oi = h * d
+    if h == 1:
+        th = oh = d
+    return HeadRowsC(t.data_ptr(), ti, th, out.data_ptr(), oi, oh, g, h)
 
 
 def dllm_head_norm_rope(desc, q: torch.Tensor, q_out, k, k_out, row_pos, rope_table, q_gain=None, k_gain=None,
@@ -470,13 +479,13 @@ def dllm_head_norm_rope(desc, q: torch.Tensor, q_out, k, k_out, row_pos, rope_ta
     """q, q_out: bf16 [M][n_heads][head_dim], k, k_out: bf16 [M][any number of heads][head_dim] or None, the last
     dimension contiguous, outputs the inputs themselves or apart from them; row_pos: contiguous int32 of M positions
     (more are fine); rope_table: contiguous float32 [positions][rotary_dim / 2][2]; gains: bf16 [head_dim] or None."""
-    d, m, dev, ts = desc.head_dim, q.shape[0], q.get_device(), rope_table.shape
+    d, m, dev, ts = desc.head_dim, q.shape[0], torch._C._cuda_getDevice(), rope_table.shape
     queries = _head_rows(q, q_out, q_gain, m, d, dev)
     keys = None if k is None else _head_rows(k, k_out, k_gain, m, d, dev)
-    if (queries is None or k is not None and keys is None or row_pos is None or not _vector_ok(row_pos, _INT32, m, dev)
+    if (queries is None or k is not None and keys is None or row_pos is None or row_pos.dtype is not _INT32
+            or row_pos.numel() < m or not row_pos.is_contiguous() or row_pos.get_device() != dev
             or rope_table.dtype is not _FP32 or len(ts) != 3 or ts[2] != 2 or not rope_table.is_contiguous()
-            or rope_table.get_device() != dev or error is not None and not _vector_ok(error, _INT32, 1, dev)
-            or dev != torch._C._cuda_getDevice()):
+            or rope_table.get_device() != dev or error is not None and not _vector_ok(error, _INT32, 1, dev)):
         raise DllmError("dllm_head_norm_rope", DLLM_ERR_INVALID_ARGUMENT)
     status = (_lib or load()).dllm_head_norm_rope(
         desc, m, row_pos.data_ptr(), queries, keys, rope_table.data_ptr(), ts[0], 2 * ts[1], pairs,
