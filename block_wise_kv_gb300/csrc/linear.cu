@@ -1,18 +1,33 @@
 // linear.cu — products with a weight: y = act(x^ W^T + b) + r, also of gate and up units
 // side by side, on tcgen05 (sm_103a).
 //
-//  * linear_norm_kernel  x^ = RMSNorm(x), correctly rounded to bf16, one CTA a row (only
-//    where the call has a gain).
-//  * linear_rows_kernel  few rows: 128 rows of W are the tensor core's M, up to 256 rows of
-//    x its N.  K is cut over the CTAs of a cluster, so that all SMs read W; the parts meet in
-//    shared memory, each CTA adds up some of the columns in the order of K.  Warp 0 streams
-//    boxes of 64 columns through a ring, warp 1 issues the MMAs into TMEM, warps 2-5 make y
-//    (a thread: one row of W; a warp's 32 neighbouring columns of y are one 64-byte run).
+//  * linear_norm_kernel  x^ = RMSNorm(x), correctly rounded to bf16, 32 to 256 threads a row
+//    (only where the call has a gain, and rows are not so few that the product norms them).
+//  * linear_rows_kernel  few rows: 128 rows of W are the tensor core's M, up to 128 rows of
+//    x its N.  K is cut over the CTAs of a cluster, so that all SMs read W; each CTA's sums go
+//    to the one that finishes them, 16 bytes a store, counted by a barrier there, and are
+//    added in the order of K.  Warps 0 and 6 stream boxes of 64 columns of W and x through a
+//    ring, warp 1 issues the MMAs into TMEM, warps 2-5 make y (a thread: one row of W; a warp's
+//    32 neighbouring columns of y are one 64-byte run).
 //  * linear_tiles_kernel many rows: a pair of CTAs (cta_group::2) takes 256 rows of x by up
 //    to 256 rows of W, each CTA half of either operand, and walks such tiles.  Two
-//    accumulators in TMEM: warps 2-5 of each CTA make y of one tile (a thread: one row of x)
-//    while the tensor cores work on the next, through a staging tile that makes whole runs
-//    of the rows of y and of the residual.
+//    accumulators in TMEM: warps 2-9 of each CTA make y of one tile (a thread: one row of x)
+//    while the tensor cores work on the next, through staging tiles that make whole runs of
+//    the rows of y and of the residual.
+//
+// Bound and measured (us, calls one behind the other, W from memory).  One row, K 4096, 6144
+// rows of W, normed: 13.1 (floor 7.4; 11.9 without the norm): W comes at 6 TB/s in 8.4 of it,
+// the rest is the first box's way (1.3), the parts' (2), and from a kernel's end to the next
+// one's start (1.2).  64 rows, 4096 x 4096: 11.7 (5.2).  512 rows, K 4096, 2 x 12288 gated and
+// normed: 70 (53.7), of which the norm is 4: tensor pipe 75% busy, held up by what L2 delivers
+// (14.5 TB/s for all SMs; 256 x 224 tiles need 60 KB for 0.24 us of MMAs).  20480 rows, K 12288,
+// 4096: 1077 to 1100 in a burst (1073), 1256 at the clock that the power limit leaves (the
+// measured sustained rate: 1207).  Library products of the same sizes: 10.1, 8.2, 65.
+//
+// The waits sleep without reading the timer as mbar_wait does: reading it, or trying more
+// often, slows the CTA down (prompts 1179, 1190, gated 87, 87).  Lines of W asked for ahead,
+// as far as L2, by the copy engine or by idle warps, before or behind the wait for the kernel
+// in front, made every case slower.
 #include <math.h>
 
 #include "layer_ops.cuh"
@@ -329,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first = t.split > 1 ? rank * t.per_rank * 4 : 0;  // the first row of x that this CTA finishes
 
   if (warp == 0 || warp == 6) {
-    // Warp 0 loads W, warp 6 x: a thread is done with a load only after about 100 ns.
+    // Warp 0 loads W, warp 6 x: a thread's next load goes out some 100 ns behind the one before.
     if (lane == 0 && (warp == 0 || t.norm == 0)) {
       const bool is_w = warp == 0;
       const CUtensorMap* map = is_w ? &tm_w : &tm_x;
@@ -867,7 +882,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // ------------------------------------------------------------ host
 bool rows16(const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0; }
 
-// Shared memory of a CTA: two fit an SM, so that one's loads go on while the other finishes.
+// Shared memory of a CTA: two fit an SM, so that one's loads go on while the other finishes, and a cluster finds room (one row:
+// 12.2 us with 100 KB, 18.5 with 200 KB, where 48 clusters of three do not fit at once; 64 rows 11.9 and 12.0 to 19).
 constexpr int kRowsSmem = 108 * 1024;
 
 RowsPlan rows_plan(const LinearArgs& a, int bn, int split, bool norm) {
@@ -964,7 +980,8 @@ struct Choice {
 constexpr int kNormBytes = 40 * 1024;  // of shared memory that rows normed inside may take
 
 // Whether rows_plan's CTAs norm their rows themselves: where they are done in two rounds, while the first boxes of W come
-// (one row of 4096: 13.1 us for 14.8 with the norm's kernel in front, and a launch less on the host).
+// (one row of 4096: 13.1 us for 13.5 with the norm's kernel in front, and 2 us less on the host; two rows took 14.7 for
+// 13.7, so that they have the kernel).
 bool norm_inside(const LinearArgs& a, int bn, int split) {
   const int lanes = norm_lanes(a.k), boxes = (a.k + kBK - 1) / kBK;
   return a.gain != nullptr && lanes <= kNormMaxLanes && (bn < a.rows ? bn : a.rows) * lanes <= 2 * kNormMaxLanes &&
@@ -972,8 +989,10 @@ bool norm_inside(const LinearArgs& a, int bn, int split) {
 }
 
 // What each kernel takes, in us: fitted to 230 shapes (1 to 2048 rows, K 256 to 12288, 256 to 24576 rows of W) with every
-// tile and split; the choice is within 2% of the best on average and 32% at worst.  A box of 64 columns costs a CTA the
-// longer of the MMAs' own pace, its bytes' way from L2, shared with the other CTAs, and the ring's latency.
+// tile and split, where the choice was within 2% of the best on average and 32% at worst, and to a dozen with other ways to
+// y.  A box of 64 columns costs a CTA the longer of the MMAs' own pace, its bytes' way from L2, shared with the other CTAs,
+// and the ring's latency.  (512 rows of 4096 x 4096: 23 us on pairs of 128 rows of W, 36 on 128 x 128 tiles; 64 rows: 11.7
+// with K cut in eight, 24 uncut; 777 x 1000 x 1003: 11.0 as 64-row tiles, 46 on 256 x 256 ones.)
 float rows_us(const LinearArgs& a, int bn, int split, int num_sms) {
   const RowsPlan t = rows_plan(a, bn, split, false);
   const int wt = (a.wide + kTW - 1) / kTW;

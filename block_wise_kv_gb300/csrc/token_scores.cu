@@ -19,6 +19,11 @@
 // top_k others before it.  The bound is the top_k-th largest of the pairs of 32 groups of
 // threads; only threads whose own pair is at or above it hold such elements, hardly
 // more than top_k of them: their pieces alone are read again, and what passes is ranked.
+//
+// Measured: 512 rows of 126464 bf16, two alternatives: 26.7 us (floor 19.1); 1500 rows 71
+// (5.4 TB/s): the SMs' exponentials (16 a clock, 56% of the time) and issue slots (50%), and
+// the fourth row that every third SM has.  333 rows of 32003 fp32: 13.4 us (6.3), of which the
+// alternatives behind the last piece take about 4.  One row, 20 alternatives: 8.1 us.
 #include <math.h>
 
 #include "layer_ops.cuh"
@@ -544,8 +549,8 @@ cudaError_t launch_scores(const ScoreArgs& a, int cluster, cudaStream_t stream) 
 
 template <typename T>
 cudaError_t launch_type(const ScoreArgs& a, int num_sms, cudaStream_t stream) {
-  // Few rows: a cluster to each, as long as a CTA has a step for each thread (126464 bf16, two alternatives, with 1, 2, 4, 8
-  // CTAs: one row 14.3, 11.8, 9.4, 8.6 us; 32 rows 11.2, 9.2, 7.7, 7.8; 128 rows 11.6, 11.7, 12.8, 18.6; 300 rows 20.6, 22.2).
+  // Few rows: a cluster to each, as long as a CTA has a step for each thread (126464 bf16 with 1, 2, 4, 8 CTAs: one row 13.7,
+  // 11.0, 8.6, 8.1 us; 32 rows 10.3, 8.5, 6.8, 6.6; 128 rows 13.3, 11.4, 11.0, 15.6; 300 rows 18.2, 18.5, 26.8, 35.0).
   const int pieces = a.vocab / Piece<T>::N;
   int cluster = 1;
   while (cluster < kMaxCluster && static_cast<int64_t>(a.rows) * cluster * 2 <= 2 * num_sms &&
