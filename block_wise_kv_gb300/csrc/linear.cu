@@ -85,10 +85,30 @@ __device__ __forceinline__ uint4 normed8(const uint4& u, const uint4& gu, float 
   return near ? normed8_near(u, gu, s_hi, s_lo) : make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// A row to TEAM threads: a thread's pieces of 8 elements are a chain of eight exact sums each.
+// Add the exact squares of 8 bf16 values to the sums (hi, lo) of two at a time, as sumsq_pair_add does one by one.
+__device__ __forceinline__ void sumsq2_add(const uint4& u, float2& hi, float2& lo) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  const float2 minus = {-1.f, -1.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack2(w[i]), b = mul2(x, x), a = hi;
+    hi = add2(a, b);
+    const float2 bp = fma2(a, minus, hi);
+    const float2 e = add2(fma2(fma2(bp, minus, hi), minus, a), fma2(bp, minus, b));
+    lo = add2(lo, e);
+  }
+}
+// The two sums as one.
+__device__ __forceinline__ void sums_of(const float2& hi2, const float2& lo2, float& hi, float& lo) {
+  hi = hi2.x;
+  lo = lo2.x;
+  pair_add(hi, lo, hi2.y, lo2.y);
+}
+
+// A row to TEAM threads, each with up to four pieces of 8 elements in registers; what is behind those is read twice.
 template <int TEAM>
 __global__ void __launch_bounds__(kNormThreads) linear_norm_kernel(const LinearArgs a) {
-  constexpr int kTeams = kNormThreads / TEAM;
+  constexpr int kTeams = kNormThreads / TEAM, kHeld = 4;
   __shared__ float2 part[kNormThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nvec = a.k / 8;
   griddep_launch_dependents();  // the product behind reads nothing before its own wait
@@ -99,9 +119,16 @@ __global__ void __launch_bounds__(kNormThreads) linear_norm_kernel(const LinearA
   const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + (there ? row : 0) * a.x_stride);
   uint4* out = static_cast<uint4*>(a.xhat) + row * nvec;
   const uint4* g = static_cast<const uint4*>(a.gain);
-  float hi = 0.f, lo = 0.f;
-#pragma unroll 2
-  for (int v = l; v < nvec; v += TEAM) sumsq_pair_add(__ldg(x + v), hi, lo);
+  uint4 u[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) u[i] = l + i * TEAM < nvec ? __ldg(x + l + i * TEAM) : make_uint4(0u, 0u, 0u, 0u);
+  float2 hi2 = {0.f, 0.f}, lo2 = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (l + i * TEAM < nvec) sumsq2_add(u[i], hi2, lo2);
+  for (int v = l + kHeld * TEAM; v < nvec; v += TEAM) sumsq2_add(__ldg(x + v), hi2, lo2);
+  float hi, lo;
+  sums_of(hi2, lo2, hi, lo);
 #pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) {
     const float oh = __shfl_xor_sync(0xffffffffu, hi, o), ol = __shfl_xor_sync(0xffffffffu, lo, o);
@@ -120,8 +147,12 @@ __global__ void __launch_bounds__(kNormThreads) linear_norm_kernel(const LinearA
   two_sum(hi, lo, hi, lo);
   float s_hi, s_lo;
   rsqrt_pair(hi, lo, a.k, a.rms_eps, s_hi, s_lo);
-#pragma unroll 2
-  for (int v = l; v < nvec; v += TEAM) out[v] = normed8(__ldg(x + v), __ldg(g + v), s_hi, s_lo);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int v = l + i * TEAM;
+    if (v < nvec) out[v] = normed8(u[i], __ldg(g + v), s_hi, s_lo);
+  }
+  for (int v = l + kHeld * TEAM; v < nvec; v += TEAM) out[v] = normed8(__ldg(x + v), __ldg(g + v), s_hi, s_lo);
 }
 
 // ------------------------------------------------------------ the epilogue's arithmetic
@@ -268,9 +299,11 @@ __device__ __forceinline__ void norm_rows(const LinearArgs& a, uint8_t* boxes, f
       if (v < nvec) u[i] = __ldg(x + v);
       if (v >= kb0 * 8 && v < (kb0 + nb) * 8 && v < nvec) w[i] = __ldg(g + v);
     }
-    float hi = 0.f, lo = 0.f;
+    float2 hi2 = {0.f, 0.f}, lo2 = {0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < kNormPieces; ++i) sumsq_pair_add(u[i], hi, lo);
+    for (int i = 0; i < kNormPieces; ++i) sumsq2_add(u[i], hi2, lo2);
+    float hi, lo;
+    sums_of(hi2, lo2, hi, lo);
     for (int o = 1; o < lanes && o < 32; o <<= 1) {
       const float oh = __shfl_xor_sync(0xffffffffu, hi, o), ol = __shfl_xor_sync(0xffffffffu, lo, o);
       // (the same order in both lanes: the pair sum is not commutative in its last bits)
@@ -1068,7 +1101,8 @@ cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream)
   if (a.rows <= 0) return cudaSuccess;
   const Choice c = choose(a, num_sms);
   if (a.gain != nullptr && !c.norm) {
-    const int team = a.k <= 256 ? 32 : a.k <= 1024 ? 128 : kNormThreads, per_cta = kNormThreads / team;
+    // (all of a row in registers: 4000 rows of 920 take 4.8 us by warps, 8.0 by four of them; of 2976 11.7 by four, 16.5 by eight)
+    const int team = a.k <= 1024 ? 32 : a.k <= 4096 ? 128 : kNormThreads, per_cta = kNormThreads / team;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.rows + per_cta - 1) / per_cta);
     cfg.blockDim = dim3(kNormThreads);
