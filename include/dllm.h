@@ -538,10 +538,11 @@ typedef struct dllm_linear_layer {
 
 /* y = act(t) + r, or (gated) act(t_gate) * t_up + r, with t = x^ W^T + b and
  *   x^ = x, or with a gain RMSNorm(x) (correctly rounded to bf16).
- * Products are summed in fp32 by the tensor core over all of K (or over equal
- * parts of K, whose sums are added in their order); bias, activation, gate and
- * residual are fp32, and y is rounded to bf16 once.  The same call gives the
- * same bits; how K is cut depends on the sizes and the number of SMs alone.
+ * Products are summed in fp32, by the tensor core over all of K (or over equal
+ * parts of K, whose sums are added in their order) or, where rows are very few,
+ * by multiply-adds in a fixed order; bias, activation, gate and residual are
+ * fp32, and y is rounded to bf16 once.  The same call gives the same bits; how
+ * K is cut depends on the sizes and the number of SMs alone.
  *   x:        device bf16 [rows][in_features], rows x_stride elements apart;
  *             16-byte aligned, the stride a multiple of 8 and >= in_features.
  *   rms_gain: device bf16 [in_features], 16-byte aligned, nullable (no norm).
