@@ -21,7 +21,7 @@ OBJDIR = os.path.join(LIBDIR, "obj")
 LIBPATH = os.path.join(LIBDIR, "libdllm.so")
 
 SOURCES = ["dllm_api.cu", "qkv_gemm.cu", "qkv_wide.cu", "attn_rows.cu", "attn_stream.cu", "misc.cu", "noalloc.cu",
-           "lm_head.cu", "ffn.cu", "batch_plan.cu", "kv8_write.cu", "kv8_attn.cu", "linear.cu", "linear_one.cu",
+           "lm_head.cu", "ffn.cu", "batch_plan.cu", "kv8_write.cu", "kv8_attn.cu", "linear.cu", "linear_few.cu",
            "head_rope.cu", "token_scores.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-I", INCLUDE, "-I",

@@ -3,6 +3,7 @@
 //
 //  * linear_norm_kernel  x^ = RMSNorm(x), correctly rounded to bf16, 32 to 256 threads a row
 //    (only where the call has a gain, and rows are not so few that the product norms them).
+//  * linear_few_kernel   one or two rows (linear_few.cu).
 //  * linear_rows_kernel  few rows: 128 rows of W are the tensor core's M, up to 128 rows of
 //    x its N.  K is cut over the CTAs of a cluster, so that all SMs read W; each CTA's sums go
 //    to the one that finishes them, 16 bytes a store, counted by a barrier there, and are
@@ -15,14 +16,14 @@
 //    while the tensor cores work on the next, through staging tiles that make whole runs of
 //    the rows of y and of the residual.
 //
-// Bound and measured (us, calls one behind the other, W from memory).  One row, K 4096, 6144
-// rows of W, normed: 13.1 (floor 7.4; 11.9 without the norm): W comes at 6 TB/s in 8.4 of it,
-// the rest is the first box's way (1.3), the parts' (2), and from a kernel's end to the next
-// one's start (1.2).  64 rows, 4096 x 4096: 11.7 (5.2).  512 rows, K 4096, 2 x 12288 gated and
-// normed: 70 (53.7), of which the norm is 4: tensor pipe 75% busy, held up by what L2 delivers
-// (14.5 TB/s for all SMs; 256 x 224 tiles need 60 KB for 0.24 us of MMAs).  20480 rows, K 12288,
-// 4096: 1077 to 1100 in a burst (1073), 1256 at the clock that the power limit leaves (the
-// measured sustained rate: 1207).  Library products of the same sizes: 10.1, 8.2, 65.
+// Bound and measured (us, calls one behind the other, W from memory).  64 rows, 4096 x 4096:
+// 11.6 (floor 5.2): W comes at 6 TB/s in 5.6 of it, the rest is the first box's way (1.3), the
+// parts' (2), and from a kernel's end to the next one's start (1.2).  512 rows, K 4096, 2 x
+// 12288 gated and normed: 66.5 (53.7), of which the norm is 3: tensor pipe 75% busy, held up by
+// what L2 delivers (14.5 TB/s for all SMs; 256 x 224 tiles need 60 KB for 0.24 us of MMAs).
+// 20480 rows, K 12288, 4096: 1056 to 1100 in a burst (1073), 1256 at the clock that the power
+// limit leaves (the measured sustained rate: 1207).  Library products of the first two's sizes:
+// 8.2 and 65.
 //
 // The waits sleep without reading the timer as mbar_wait does: reading it, or trying more
 // often, slows the CTA down (prompts 1179, 1190, gated 87, 87).  Lines of W asked for ahead,
@@ -190,16 +191,15 @@ __host__ __device__ inline int norm_lanes(int k) {
   while (t * kNormPieces * 8 < k) t *= 2;
   return t;
 }
-constexpr int kNormMaxLanes = 128;
+constexpr int kNormThreadsInside = 128;
 
 // Four warps (tid: 0 to 127): columns [64 kb0, 64 (kb0 + nb)) of RMSNorm(x) of the rows from x0 on, as the boxes that the
 // MMAs take (rows of 128 bytes, swizzled).  `boxes` is zero where no row or column is.
-__device__ __forceinline__ void norm_rows(const LinearArgs& a, uint8_t* boxes, float2* part, int x0, int bn, int kb0, int nb,
-                                          int tid) {
+__device__ __forceinline__ void norm_rows(const LinearArgs& a, uint8_t* boxes, int x0, int bn, int kb0, int nb, int tid) {
   const int nvec = a.k / 8, lanes = norm_lanes(a.k), sub = tid / lanes, l = tid % lanes;
   const uint4* g = static_cast<const uint4*>(a.gain);
   const int rows = min(bn, a.rows - x0);
-  for (int r0 = 0; r0 < rows; r0 += kNormMaxLanes / lanes) {
+  for (int r0 = 0; r0 < rows; r0 += kNormThreadsInside / lanes) {
     const int row = r0 + sub;
     const bool there = row < rows;
     const uint4* x =
@@ -217,22 +217,13 @@ __device__ __forceinline__ void norm_rows(const LinearArgs& a, uint8_t* boxes, f
     for (int i = 0; i < kNormPieces; ++i) sumsq2_add(u[i], hi2, lo2);
     float hi, lo;
     sums_of(hi2, lo2, hi, lo);
-    for (int o = 1; o < lanes && o < 32; o <<= 1) {
+    for (int o = 1; o < lanes; o <<= 1) {
       const float oh = __shfl_xor_sync(0xffffffffu, hi, o), ol = __shfl_xor_sync(0xffffffffu, lo, o);
       // (the same order in both lanes: the pair sum is not commutative in its last bits)
       float h = (tid & o) ? oh : hi, s = (tid & o) ? ol : lo;
       pair_add(h, s, (tid & o) ? hi : oh, (tid & o) ? lo : ol);
       hi = h;
       lo = s;
-    }
-    if (lanes > 32) {
-      if ((tid & 31) == 0) part[tid >> 5] = make_float2(hi, lo);
-      named_barrier(1, 128);
-      const int w0 = sub * (lanes / 32);
-      hi = part[w0].x;
-      lo = part[w0].y;
-      for (int i = 1; i < lanes / 32; ++i) pair_add(hi, lo, part[w0 + i].x, part[w0 + i].y);
-      named_barrier(1, 128);
     }
     two_sum(hi, lo, hi, lo);
     float s_hi, s_lo;
@@ -255,7 +246,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
   __shared__ uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar, join_bar, norm_bar;
   __shared__ uint32_t tmem_base_sh;
-  __shared__ float2 norm_part[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int x_box = t.bn * kBK * 2, stage_bytes = kABytes + (t.norm ? 0 : x_box);
   const int rank = static_cast<int>(blockIdx.x) % t.split, tile = static_cast<int>(blockIdx.x) / t.split;
@@ -344,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     b = wr < a.wide && a.bias != nullptr ? bf16_at(a.bias, wr) : 0.f;
     if (t.norm) {
       named_barrier(1, 128);
-      norm_rows(a, smem + t.norm, norm_part, x0, t.bn, kb0, nb, threadIdx.x - 64);
+      norm_rows(a, smem + t.norm, x0, t.bn, kb0, nb, threadIdx.x - 64);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the MMAs read it
       __syncwarp();
       if (lane == 0) mbar_arrive(&norm_bar);
@@ -925,12 +915,13 @@ struct Choice {
 
 constexpr int kNormBytes = 40 * 1024;  // of shared memory that rows normed inside may take
 
-// Whether rows_plan's CTAs norm their rows themselves: where they are done in two rounds, while the first boxes of W come
-// (one row of 4096: 13.1 us for 13.5 with the norm's kernel in front, and 2 us less on the host; two rows took 14.7 for
-// 13.7, so that they have the kernel).
+// Whether rows_plan's CTAs norm their rows themselves: rows of a warp's lanes at most, done in two rounds, while the first
+// boxes of W come.  That is a launch less, 2 us on the host; on the GPU 32 rows of 256 x 768 took 4.6 us for 4.7 with the
+// norm's kernel in front, 8 of 1024 x 4096 7.6 for 7.9, 16 of 512 x 2048 5.9 for 5.6; by two warps a row 3 rows of 2048 x 12288
+// took 16.3 for 15.1, so that they have the kernel.
 bool norm_inside(const LinearArgs& a, int bn, int split) {
   const int lanes = norm_lanes(a.k), boxes = (a.k + kBK - 1) / kBK;
-  return a.gain != nullptr && lanes <= kNormMaxLanes && (bn < a.rows ? bn : a.rows) * lanes <= 2 * kNormMaxLanes &&
+  return a.gain != nullptr && lanes <= 32 && (bn < a.rows ? bn : a.rows) * lanes <= 2 * kNormThreadsInside &&
          (boxes + split - 1) / split * bn * kBK * 2 <= kNormBytes;
 }
 
@@ -1012,9 +1003,10 @@ cudaError_t launch_act(const LinearArgs& a, const Choice& c, int num_sms, cudaSt
 
 cudaError_t launch_linear(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   if (a.rows <= 0) return cudaSuccess;
-  // One row: W streamed past registers (4096 x 6144: 9.3 us for 11.6 as the tensor cores' N, normed 10.4 for 12.9; 256 x 768
-  // normed 2.0 for 4.4; 12288 x 4096 17.0 for 19.5; 5000 x 7000 normed 15.7 for 17.2).
-  if (a.rows == 1 && a.k <= kOneMostK) return launch_linear_one(a, num_sms, stream);
+  // One or two rows: W streamed past registers (4096 x 6144, one row 9.2 us for 11.6 as the tensor cores' N, normed 10.6 for
+  // 12.9, two 10.5 and 12.5 for 11.7 and 14.2; 256 x 768 normed 2.0 and 2.4 for 4.4 and 4.2; 12288 x 4096, one row 16.9 for
+  // 19.5.  Two rows of 11008 x 4096 took 18.6 for 17.8, four of 4096 x 6144 11.8 to 15.8 for 11.7 to 14.2.)
+  if (a.rows <= few_rows(a.k)) return launch_linear_few(a, num_sms, stream);
   const Choice c = choose(a, num_sms);
   if (a.gain != nullptr && !c.norm) {
     // (all of a row in registers: 4000 rows of 920 take 4.8 us by warps, 8.0 by four of them; of 2976 11.7 by four, 16.5 by eight)

@@ -1,5 +1,5 @@
 // linear_math.cuh — what the products' kernels share: the norm's arithmetic and what is done
-// to the sums (linear.cu, linear_one.cu).
+// to the sums (linear.cu, linear_few.cu).
 #pragma once
 
 #include <math.h>
@@ -95,8 +95,8 @@ __device__ __forceinline__ float bf16_at(const void* p, int64_t i) {
   return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
 }
 
-// ------------------------------------------------------------ one row (linear_one.cu)
-constexpr int kOneMostK = 16384;  // K, at most
-cudaError_t launch_linear_one(const LinearArgs& a, int num_sms, cudaStream_t stream);
+// ------------------------------------------------------------ a few rows (linear_few.cu)
+constexpr int few_rows(int k) { return k <= 4096 ? 2 : k <= 16384 ? 1 : 0; }  // how many it takes
+cudaError_t launch_linear_few(const LinearArgs& a, int num_sms, cudaStream_t stream);
 
 }  // namespace dllm

@@ -95,16 +95,18 @@ def test_linear_many_rows(m, k, n, gated):
 
 @pytest.mark.parametrize("k", [8, 248, 264, 2048, 2056, 4096, 4104, 8192, 8200, 12344, 16384, 16392])
 @pytest.mark.parametrize("n,gated", [(1, False), (1, True), (37, True), (305, False), (1219, False)])
-def test_linear_one_row(k, n, gated):
+@pytest.mark.parametrize("m", [1, 2])
+def test_linear_few_rows(m, k, n, gated):
     for bias, residual, norm in ((False, False, False), (True, True, True)):
-        c = Linear(1, k, n, "silu" if gated else "none", gated, norm, bias, residual, seed=k + n)
+        c = Linear(m, k, n, "silu" if gated else "none", gated, norm, bias, residual, pad=m - 1, seed=k + n)
         c.call()
         c.check()
 
 
-@pytest.mark.parametrize("k,n,gated", [(8, 60000, True), (72, 200000, False)])
-def test_linear_one_row_of_many_columns(k, n, gated):
-    c = Linear(1, k, n, "gelu" if gated else "none", gated, bias=True, residual=True, pad=3, seed=n)
+@pytest.mark.parametrize("m,k,n,gated", [(1, 8, 60000, True), (1, 72, 200000, False), (2, 16, 100003, False),
+                                         (2, 8, 40001, True)])
+def test_linear_few_rows_of_many_columns(m, k, n, gated):
+    c = Linear(m, k, n, "gelu" if gated else "none", gated, bias=True, residual=True, pad=3, seed=n)
     c.call()
     c.check()
 
