@@ -20,10 +20,11 @@
 // threads; only threads whose own pair is at or above it hold such elements, hardly
 // more than top_k of them: their pieces alone are read again, and what passes is ranked.
 //
-// Measured: 512 rows of 126464 bf16, two alternatives: 26.7 us (floor 19.1); 1500 rows 71
-// (5.4 TB/s): the SMs' exponentials (16 a clock, 56% of the time) and issue slots (50%), and
-// the fourth row that every third SM has.  333 rows of 32003 fp32: 13.4 us (6.3), of which the
-// alternatives behind the last piece take about 4.  One row, 20 alternatives: 8.1 us.
+// Measured: 512 rows of 126464 bf16, two alternatives: 26.6 us (floor 19.1), of which the stream
+// with the launch and the join is 23.4, the alternatives behind it are 1.8, and exponentials
+// and sums, which go on beside the loads, the rest; 1500 rows 71 (5.4 TB/s).  333 rows of 32003
+// fp32: 13.4 us (6.3), the alternatives again 1.8.  One row, 20 alternatives: 8.0 us, of
+// which they are 1.9.
 #include <math.h>
 
 #include "layer_ops.cuh"

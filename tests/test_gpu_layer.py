@@ -93,6 +93,15 @@ def test_linear_many_rows(m, k, n, gated):
     c.check()
 
 
+@pytest.mark.parametrize("m,k", [(33, 16), (900, 1016), (1500, 1032), (1100, 2984), (257, 4096), (600, 4104), (40, 12288),
+                                 (3, 16392)])
+@pytest.mark.parametrize("size", [1.0, 1e-4, 3e4])
+def test_linear_norm_of_rows_of_any_length(m, k, size):
+    c = Linear(m, k, 72, norm=True, pad=1, seed=k, size=size)
+    c.call()
+    c.check()
+
+
 @pytest.mark.parametrize("k", [8, 248, 264, 2048, 2056, 4096, 4104, 8192, 8200, 12344, 16384, 16392])
 @pytest.mark.parametrize("n,gated", [(1, False), (1, True), (37, True), (305, False), (1219, False)])
 @pytest.mark.parametrize("m", [1, 2])
