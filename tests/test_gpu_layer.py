@@ -560,3 +560,79 @@ def test_scores_of_the_block_heads_logits():
     lu.assert_scores((lse2, None, logp, ids, best), logits, arg, 2, 1.0)
     off = lu.HALF_BF16 * logits.float().abs().amax(1) + 1e-4
     assert ((lse - lse2).abs() <= off).all() and ((p.log() - logp).abs() <= 2 * off).all()
+
+
+def test_heads_of_many_rows_in_place():
+    m, h, kv, d = 6001, 8, 2, 128
+    buf = lu.randn((m, h + 2 * kv, d), 1)
+    q, k, before = buf[:, :h], buf[:, h:h + kv], buf.clone()
+    table, gains, error = lu.rope_table(500, d), [lu.randn((d,), 3, 0.5), lu.randn((d,), 4, 0.5)], ints([0])
+    pos = torch.arange(m, device="cuda", dtype=torch.int32) % 500
+    pos[5::97] = -1
+    dllm.dllm_head_norm_rope(dllm.layer_desc(h * d, h, d, 1e4, 1e-6), q, q, k, k, pos, table, *gains, error=error)
+    there = pos >= 0
+    for got, x, g in ((q, before[:, :h], gains[0]), (k, before[:, h:h + kv], gains[1])):
+        want, off = lu.head_norm_rope(x[there], g, pos[there], table, d, False, 1e-6)
+        assert ((got[there].double() - want).abs() <= off).all()
+    assert torch.equal(buf[~there], before[~there]) and torch.equal(buf[:, h + kv:], before[:, h + kv:])
+    assert error.item() == 0
+
+
+class Chain:
+    """A few rows' product, the heads and the scores of one request, each with buffers of its own."""
+
+    def __init__(self, m, seed):
+        self.lin = Linear(m, 1024, 10 * 128, norm=True, bias=True, seed=seed)
+        self.heads = self.lin.y.view(m, 10, 128)
+        self.out = torch.zeros_like(self.heads)
+        self.pos = torch.arange(m, device="cuda", dtype=torch.int32) + seed
+        self.table, self.gain = lu.rope_table(64, 128), lu.randn((128,), seed + 7, 0.5)
+        self.desc = dllm.layer_desc(8 * 128, 8, 128, 1e4, 1e-6)
+        self.logits, self.tokens = self.out.view(m, 1280), _tokens(m, 1280, seed)
+        self.f = [torch.zeros(m, device="cuda") for _ in range(3)]
+        self.ids, self.best = torch.zeros(m, 4, device="cuda", dtype=torch.int32), torch.zeros(m, 4, device="cuda")
+
+    def call(self):
+        self.lin.call()
+        dllm.dllm_head_norm_rope(self.desc, self.heads[:, :8], self.out[:, :8], self.heads[:, 8:], self.out[:, 8:], self.pos,
+                                 self.table, self.gain, self.gain, error=self.lin.error)
+        dllm.dllm_token_scores(self.logits, self.tokens, *self.f, self.ids, self.best, 1.0, self.lin.error)
+
+    def results(self):
+        assert self.lin.error.item() == 0
+        return [t.clone() for t in (self.lin.y, self.out, *self.f, self.ids, self.best)]
+
+
+@pytest.mark.parametrize("m", [1, 2, 5])
+def test_calls_on_two_streams_at_once_and_captured(m):
+    cs = [Chain(m, s) for s in (1, 2)]
+    xs = [c.lin.x.clone() for c in cs]
+    want = {}
+    for i, c in enumerate(cs):  # each of the rows through each of the chains, one call behind the other
+        for j, x in enumerate(xs):
+            c.lin.x.copy_(x)
+            c.call()
+            torch.cuda.synchronize()
+            want[i, j] = c.results()
+            c.lin.check()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for turn in range(6):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            with torch.cuda.stream(s):
+                c.lin.x.copy_(xs[(i + turn) % 2])
+                c.call()
+        torch.cuda.synchronize()
+        for i, c in enumerate(cs):
+            assert all(torch.equal(a, b) for a, b in zip(c.results(), want[i, (i + turn) % 2]))
+    graphs = [torch.cuda.CUDAGraph() for _ in cs]
+    for c, g in zip(cs, graphs):
+        with torch.cuda.graph(g):
+            c.call()
+    for turn in range(4):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            with torch.cuda.stream(s):
+                c.lin.x.copy_(xs[(i + turn) % 2])
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for i, c in enumerate(cs):
+            assert all(torch.equal(a, b) for a, b in zip(c.results(), want[i, (i + turn) % 2]))
