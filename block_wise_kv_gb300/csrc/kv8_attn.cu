@@ -1084,16 +1084,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const Kv8Attn
 
 template <int D>
 cudaError_t encode_codes(CUtensorMap* map, const void* ptr, uint64_t rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (enc == nullptr) return cudaErrorNotSupported;
   cuuint64_t dims[2] = {D, rows};
   cuuint64_t strides[1] = {D};
   cuuint32_t box[2] = {D, kPage};
-  cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, ptr, dims, strides, box,
+                      D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 int grid_of(int nq, int num_sms) { return std::min(ctas_per_sm(nq) * num_sms, kMaxCtas); }

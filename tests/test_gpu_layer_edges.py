@@ -1,0 +1,64 @@
+"""Where a layer's calls can go wrong unseen by one thread's products with random weights."""
+import ctypes
+import math
+import threading
+
+import pytest
+import torch
+
+import layer_util as lu
+from block_wise_kv_gb300 import dllm
+from kv8_util import ints
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from block_wise_kv_gb300 import build
+
+    build.build()
+    dllm.load()
+    torch.cuda.init()
+
+
+# ------------------------------------------------------------------ two host threads
+def _raw(desc, x, w, y, error, stream):
+    """The C call and its arguments, so that little but the call itself holds two threads apart."""
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    args = (ctypes.byref(desc), x.shape[0], p(x), x.shape[1], None, p(w), None, None, y.shape[1], p(y), y.shape[1], p(error),
+            None, 0, ctypes.c_void_p(stream.cuda_stream))
+    return lambda: dllm.load().dllm_linear(*args)
+
+
+def _together(*works):
+    """Each on a thread of its own; what they raise is raised here."""
+    wrong, gate = [], threading.Barrier(len(works))
+
+    def run(work):
+        gate.wait()
+        try:
+            work()
+        except BaseException as e:  # noqa: BLE001
+            wrong.append(e)
+
+    threads = [threading.Thread(target=run, args=(w,)) for w in works]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if wrong:
+        raise wrong[0]
+
+
+def test_a_host_threads_first_call_is_a_product():
+    """Nothing before it has made the device's context the thread's own."""
+    m, k, n = 48, 256, 384
+    x, w, y, error = lu.randn((m, k), 1), lu.randn((n, k), 2, 1 / math.sqrt(k)), lu.randn((m, n), 3), ints([0])
+    stream, status = torch.cuda.Stream(), []
+    call = _raw(dllm.linear_desc(k, n), x, w, y, error, stream)
+    torch.cuda.synchronize()
+    _together(lambda: status.append(call()))
+    torch.cuda.synchronize()
+    want, off = lu.linear(x, w)
+    assert status == [dllm.DLLM_OK] and ((y.double() - want).abs() <= off).all() and error.item() == 0
