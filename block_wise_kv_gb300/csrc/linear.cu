@@ -821,6 +821,7 @@ bool rows16(const void* p, int64_t stride) { return reinterpret_cast<uintptr_t>(
 // Shared memory of a CTA: two fit an SM, so that one's loads go on while the other finishes, and a cluster finds room (one row:
 // 12.2 us with 100 KB, 18.5 with 200 KB, where 48 clusters of three do not fit at once; 64 rows 11.9 and 12.0 to 19).
 constexpr int kRowsSmem = 108 * 1024;
+constexpr int kRowsSmemMost = kRowsSmem + 1024;  // that any plan takes: the ring has two places at least, which fit beside the rest
 
 RowsPlan rows_plan(const LinearArgs& a, int bn, int split, bool norm) {
   RowsPlan t;
@@ -853,7 +854,8 @@ cudaError_t launch_rows(const LinearArgs& a, const RowsPlan& t, cudaStream_t str
     e = a.gain != nullptr && t.norm == 0 ? encode_rows_sw128(&tm_x, a.xhat, a.k, a.rows, a.k, kBK, t.bn)
                                          : encode_rows_sw128(&tm_x, a.x, a.k, a.rows, a.x_stride, kBK, t.bn);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(linear_rows_kernel<ACT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, t.smem);
+  // (the same for every call: the limit is the kernel's, and another thread may set it between this line and the launch)
+  e = cudaFuncSetAttribute(linear_rows_kernel<ACT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmemMost);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((a.wide + kTW - 1) / kTW) * t.xt * t.split);

@@ -62,3 +62,25 @@ def test_a_host_threads_first_call_is_a_product():
     torch.cuda.synchronize()
     want, off = lu.linear(x, w)
     assert status == [dllm.DLLM_OK] and ((y.double() - want).abs() <= off).all() and error.item() == 0
+
+
+@pytest.mark.parametrize("sizes", [((64, 4096, 4096), (16, 256, 768)), ((64, 1024, 256), (3, 64, 128))])
+def test_two_host_threads_call_products_of_one_activation(sizes):
+    """Their kernels take different amounts of shared memory, on two streams."""
+    works = []
+    for i, (m, k, n) in enumerate(sizes):
+        x, w, y, error = lu.randn((m, k), i), lu.randn((n, k), 10 + i, 1 / math.sqrt(k)), lu.randn((m, n), 20), ints([0])
+        stream, want = torch.cuda.Stream(), lu.linear(x, w)
+        call = _raw(dllm.linear_desc(k, n), x, w, y, error, stream)
+
+        def work(call=call, y=y, error=error, stream=stream, want=want):
+            with torch.cuda.stream(stream):
+                for turn in range(4000):
+                    assert call() == dllm.DLLM_OK, turn
+                    if turn % 500 == 499:
+                        assert ((y.double() - want[0]).abs() <= want[1]).all() and error.item() == 0
+                        y.fill_(7.0)
+
+        works.append(work)
+    torch.cuda.synchronize()
+    _together(*works)
