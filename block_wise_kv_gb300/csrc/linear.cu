@@ -112,13 +112,25 @@ struct RowsPlan {
   int xt;         // tiles of x
 };
 
-// A bounded wait without the timer that mbar_wait reads: each try sleeps for up to 20 us, two seconds in all at most.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity) {
+// A bounded wait without the timer that mbar_wait reads.  A try at a phase that is not over takes 3.8 us, whatever time up to
+// 100 us it is given: two seconds and more in all.  (The timer behind every thousand tries, inlined or in a function of its
+// own: 64 rows 10.8 us for 10.7, gated 77.7 for 76.8.)
+constexpr int kTries = 600000;
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, int tries = kTries) {
 #pragma unroll 1
-  for (int i = 0; i < 100000; ++i)
+  for (int i = 0; i < tries; ++i)
     if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
   return false;
 }
+// As that, for a warp that begins to wait while the kernel in front may still run: only what runs out behind that is this
+// kernel's own.  (Waiting for that kernel first: 777 rows of 1000 x 1003 11.26 us for 11.13.)
+__device__ __forceinline__ bool wait_box(uint64_t* bar, uint32_t parity) {
+  if (wait_phase(bar, parity)) return true;
+  griddep_wait();
+  return wait_phase(bar, parity);
+}
+// For what comes once all boxes of a tile are there: one takes 0.3 us.
+__device__ __forceinline__ int tries_of(int boxes) { return kTries + boxes; }
 
 // A place in a ring and the parity of its present use, stepped without divisions: a division by the number of stages costs
 // the one thread that issues the loads about as much as the load (an SM's loads then came at 51 GB/s, not at 100).
@@ -308,10 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = umma_idesc_bf16(kTW, t.bn);
-      bool ok = t.norm == 0 || wait_phase(&norm_bar, 0);
+      bool ok = t.norm == 0 || wait_box(&norm_bar, 0);
       Ring r;
       for (int i = 0; i < nb && ok; ++i, r.next(t.stages)) {
-        ok = wait_phase(&full_bar[r.s], r.parity);
+        ok = wait_box(&full_bar[r.s], r.parity);
         if (!ok) break;
         tc_fence_after();
         const uint32_t sa = smem_u32(smem) + r.s * stage_bytes;
@@ -340,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&norm_bar);
     }
     fin.ask(a, wr, x0 + first, lane);
-    if (!wait_phase(&done_bar, 0)) report_error(a.err, kErrTimeout);
+    if (!wait_phase(&done_bar, 0, tries_of(nb))) report_error(a.err, kErrTimeout);
     tc_fence_after();
   }
   const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -381,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (groups > 0) {
-        if (!wait_phase(&join_bar, 0)) report_error(a.err, kErrTimeout);
+        // (a CTA that gave a wait up sends all the same: not before all have is this one's shared memory let go)
+        if (!wait_phase(&join_bar, 0, 2 * tries_of(nb))) report_error(a.err, kErrTimeout);
         const float4* part = reinterpret_cast<const float4*>(smem + t.join) + quad * 32 + lane;
         const int end = first + groups * 4;
         for (int c0 = first, g0 = 0; c0 < end && x0 + c0 < a.rows; c0 += 16, g0 += 4) {
@@ -677,6 +690,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       const uint32_t idesc = umma_idesc_bf16(256, t.bn);
+      griddep_wait();
       const int total = mine * t.boxes;
       bool ok = true;
       Ring r;
@@ -728,7 +742,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int first = half * kStageCols;
       const uint32_t empty = mapa_shared(smem_u32(&tempty_bar[buf]), 0);
       if (has_r && first < cols) res.ask(a, t.r_vec, st, r0 + first, row0, cols - first, lane);
-      if (ok && !wait_phase(&tfull_bar[buf], (i >> 1) & 1)) {
+      if (ok && !wait_phase(&tfull_bar[buf], (i >> 1) & 1, tries_of(t.boxes))) {
         report_error(a.err, kErrTimeout);
         ok = false;
       }

@@ -84,3 +84,18 @@ def test_two_host_threads_call_products_of_one_activation(sizes):
         works.append(work)
     torch.cuda.synchronize()
     _together(*works)
+
+
+# ------------------------------------------------------------------ long waits
+def test_rows_so_long_that_a_product_takes_most_of_a_second():
+    """2^30 columns, all but some of them zero: the sums are exact, and whoever makes y waits for all of it."""
+    k, m = 1 << 30, 3
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(1, k, dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 1, 63, 64, 12345, k // 8 - 1, k // 8, k // 2 + 7, k - 65, k - 64, k - 1], device="cuda")
+    x[:, at] = torch.arange(1, 1 + m * at.numel(), device="cuda").view(m, -1).bfloat16()
+    w[0, at] = torch.arange(at.numel(), device="cuda").bfloat16() - 4
+    y, error = torch.zeros(m, 1, dtype=torch.bfloat16, device="cuda"), ints([0])
+    dllm.dllm_linear(dllm.linear_desc(k, 1), x, w, y, error=error)
+    want = (x[:, at].double() * w[0, at].double()).sum(1, keepdim=True)
+    assert error.item() == 0 and torch.equal(y, want.bfloat16()), (error.item(), y, want)
