@@ -953,7 +953,7 @@ float rows_us(const LinearArgs& a, int bn, int split, int num_sms) {
   const int64_t waves = (ctas + 2 * num_sms - 1) / (2 * num_sms) + (split > 4 && ctas > 9 * num_sms / 5 ? 1 : 0);
   const float kb = 16.f + bn / 8.f;
   const float box = fmaxf(fmaxf(0.29f, 0.99f / t.stages), kb * 0.0082f * (ctas > num_sms ? 2 : 1));
-  const float col = 0.033f + (a.residual != nullptr ? 0.015f : 0.f) + (a.act == kActGelu ? 0.04f : a.act != kActNone ? 0.01f : 0.f);
+  const float col = 0.033f + (a.residual != nullptr ? 0.015f : 0.f) + (a.act == kActGelu ? 0.02f : a.act != kActNone ? 0.01f : 0.f);
   const float one = (t.boxes + split - 1) / split * box + 0.38f + (split > 1 ? 0.46f + (0.035f + 0.3f * col) * bn : col * bn);
   const float dram = static_cast<float>(a.wide) * a.k * 2.f / 6.7e6f + (split > 1 ? 0.46f : 0.f);
   return 2.2f + fmaxf(waves * one, dram) + 0.05f * fminf(waves * one, dram);
@@ -968,7 +968,7 @@ float tiles_us(const LinearArgs& a, int bn, int num_sms) {
   // making y of a tile, in us for 256 columns: less where it is hidden behind the next tile's MMAs
   const bool apart = !rows16(a.y, a.y_stride);
   const float out = 2.6f + (apart ? 2.2f : 0.f) + (a.residual != nullptr ? 1.7f : 0.f) + (a.bias != nullptr ? 0.8f : 0.f) +
-                    (a.act == kActGelu ? 4.7f : a.act != kActNone ? 1.2f : 0.f);
+                    (a.act == kActGelu ? 2.2f : a.act != kActNone ? 1.2f : 0.f);
   const float mma = boxes * box, last = 1.5f + (out - 1.5f) * bn / 256;
   const float work = (waves - 1) * fmaxf(mma, last) + mma + last;
   const float dram = static_cast<float>(a.wide) * a.k * 2.f / 6.7e6f;

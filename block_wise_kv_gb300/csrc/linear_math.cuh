@@ -82,11 +82,33 @@ __device__ __forceinline__ float times_sigmoid(float t, float x) {
   return t * r;
 }
 
+// t (1 + erf(t / sqrt 2)) / 2 as max(t, 0) - |t| Q(|t|), Q(x) = erfc(x / sqrt 2) / 2 = e^(-x^2 / 2) R(x), which keeps its relative
+// accuracy where t is negative (1 + erf cancels: 4% off at -5).  R falls from 1/2 as 1 / x and is a polynomial of degree 7
+// in w = 1 / (1 + 0.35 x): the coefficients of the least relative error up to x = 14.7, 2^-21.5, by exchange of its extrema
+// (2^-20.1 with the roundings of w and of the sum); behind that the power of two is zero.  It is 2^8 too large and R as much
+// too small, so that ex2, which knows no subnormal numbers, ends below bf16's.  (4096 rows of 1024 x 4096:
+// 32.5 us, 40.5 with erff, 65 with erfcf.)
+__device__ __forceinline__ float gelu(float t) {
+  const float x = fminf(fabsf(t), 16.f);
+  float w, e;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(0.35f, x, 1.f)));
+  float r = 1.905061508e-04f;
+  r = fmaf(r, w, -7.869832334e-04f);
+  r = fmaf(r, w, 9.360692347e-04f);
+  r = fmaf(r, w, -6.327957090e-05f);
+  r = fmaf(r, w, 6.077258731e-04f);
+  r = fmaf(r, w, 5.213141558e-04f);
+  r = fmaf(r, w, 5.478762905e-04f);
+  r = fmaf(r, w, -1.036428117e-07f);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(x * x, -0.72134752044448170f, 8.f)));
+  return fmaf(-x * r, e, t < 0.f ? 0.f : t);  // (a NaN is neither)
+}
+
 // (1 + tanh u) / 2 is the sigmoid of 2 u.
 template <int ACT>
 __device__ __forceinline__ float activate(float t) {
   if (ACT == kActSilu) return times_sigmoid(t, t);
-  if (ACT == kActGelu) return 0.5f * t * (1.f + erff(t * 0.70710678118654752f));
+  if (ACT == kActGelu) return gelu(t);
   if (ACT == kActGeluTanh) return times_sigmoid(t, 1.5957691216057308f * (t + 0.044715f * t * t * t));
   return t;
 }

@@ -99,3 +99,52 @@ def test_rows_so_long_that_a_product_takes_most_of_a_second():
     dllm.dllm_linear(dllm.linear_desc(k, 1), x, w, y, error=error)
     want = (x[:, at].double() * w[0, at].double()).sum(1, keepdim=True)
     assert error.item() == 0 and torch.equal(y, want.bfloat16()), (error.item(), y, want)
+
+
+# ------------------------------------------------------------------ the activations' tails
+ACTS = [("gelu", dllm.DLLM_ACT_GELU)]
+
+
+def _act(t, name):
+    """(value, how far it lies down the tail: z of its e^-z) in 64 bits, without a difference of near numbers."""
+    if name == "gelu":
+        return 0.5 * t * torch.erfc(-t * math.sqrt(0.5)), t.clamp(max=0) ** 2 / 2
+    u = t if name == "silu" else 2 * math.sqrt(2 / math.pi) * (t + 0.044715 * t ** 3)
+    return t * torch.sigmoid(u), (-u).clamp(min=0)
+
+
+def _assert_act(y, t, name):
+    """Relative to the value: bf16's rounding; the exponent z of e^-z comes of a handful of roundings of 2^-24 of it, which are
+    that much of the value; the functions' own error and the last products are counted as 2^-19.  Below bf16's normal range:
+    one of its steps there, 2^-133."""
+    want, z = _act(t, name)
+    off = (lu.HALF_BF16 + 2.0 ** -21 * (4 + z)) * want.abs() + 2.0 ** -133
+    bad = ((y.double() - want).abs() <= off).logical_not().nonzero()[:4].tolist()
+    assert not bad, [(t.expand_as(y)[i, j].item(), y[i, j].item(), want.expand_as(y)[i, j].item()) for i, j in bad]
+
+
+@pytest.mark.parametrize("name,act", ACTS)
+@pytest.mark.parametrize("m", [1, 2, 40, 6000])
+def test_activations_keep_their_tails(name, act, m):
+    """One 1 in each row of W: t is the chosen value without any rounding.  Every bf16 value from -104 to 104, some beyond."""
+    u = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16)
+    t = torch.cat([u[(u.abs() <= 104)], torch.tensor([-3e38, -1e20, -1e5, 1e5, 1e20, 3e38], device="cuda").bfloat16()])
+    assert t.numel() > 33000
+    if m <= 2:  # the values are W's
+        x = torch.zeros(m, 8, dtype=torch.bfloat16, device="cuda")
+        x[:, 0] = 1
+        w = torch.zeros(t.numel(), 8, dtype=torch.bfloat16, device="cuda")
+        w[:, 0] = t
+        y = torch.zeros(m, t.numel(), dtype=torch.bfloat16, device="cuda")
+        dllm.dllm_linear(dllm.linear_desc(8, t.numel(), act), x, w, y)
+        _assert_act(y, t.double()[None], name)
+        return
+    n = 96 if m == 40 else 520
+    w = torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda")
+    w[:, 0] = 1
+    for part in t.split(m):
+        x = torch.zeros(part.numel(), 8, dtype=torch.bfloat16, device="cuda")
+        x[:, 0] = part
+        y = torch.zeros(part.numel(), n, dtype=torch.bfloat16, device="cuda")
+        dllm.dllm_linear(dllm.linear_desc(8, n, act), x, w, y)
+        _assert_act(y, part.double()[:, None], name)
