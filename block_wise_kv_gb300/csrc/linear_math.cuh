@@ -74,12 +74,14 @@ __device__ __forceinline__ void sums_of(const float2& hi2, const float2& lo2, fl
   pair_add(hi, lo, hi2.y, lo2.y);
 }
 
-// t / (1 + e^-x), by ex2 and a reciprocal that are each off by about 2^-22 (a division and expf cost four times as much).
+// t / (1 + e^-x), by ex2 and a reciprocal that are each off by about 2^-22 (a division and expf cost four times as much).  Both
+// terms of the sum, and t, are taken 2^16 times too small: the reciprocal knows no subnormal numbers, and would otherwise be 0
+// from x = -87.3 on, where the value is not yet below bf16's.
 __device__ __forceinline__ float times_sigmoid(float t, float x) {
   float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return t * r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(x, -1.4426950408889634f, -16.f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 0x1p-16f));
+  return t * 0x1p-16f * r;
 }
 
 // t (1 + erf(t / sqrt 2)) / 2 as max(t, 0) - |t| Q(|t|), Q(x) = erfc(x / sqrt 2) / 2 = e^(-x^2 / 2) R(x), which keeps its relative

@@ -102,7 +102,7 @@ def test_rows_so_long_that_a_product_takes_most_of_a_second():
 
 
 # ------------------------------------------------------------------ the activations' tails
-ACTS = [("gelu", dllm.DLLM_ACT_GELU)]
+ACTS = [("silu", dllm.DLLM_ACT_SILU), ("gelu", dllm.DLLM_ACT_GELU), ("gelu_tanh", dllm.DLLM_ACT_GELU_TANH)]
 
 
 def _act(t, name):
