@@ -133,12 +133,20 @@ __device__ __forceinline__ uint64_t key_of(float x, uint32_t at) {
 __device__ __forceinline__ float value_of(uint64_t key) { return unordered(static_cast<uint32_t>(key >> 32)); }
 __device__ __forceinline__ int place_of(uint64_t key) { return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(key)); }
 
+// (x - y) c for x <= y, also where x - y is beyond fp32 and the product is not.
+__device__ __forceinline__ float scaled_apart(float x, float y, float c) {
+  const float d = x - y;
+  return d == -INFINITY ? (0.5f * x - 0.5f * y) * c * 2.f : d * c;
+}
+
 // Sums of weights 2^(u - r) and of weight x (u - r), u = x c log2 e.  The slow form keeps r in units of x, and works on
-// differences of x, which do not overflow.
+// differences of x.
 template <bool SLOW>
 struct Stat {
   float r, s, a;
-  static __device__ __forceinline__ float apart(float x, float y, float c) { return SLOW ? fmaxf((x - y) * c, -1000.f) : x - y; }
+  static __device__ __forceinline__ float apart(float x, float y, float c) {
+    return SLOW ? fmaxf(scaled_apart(x, y, c), -1000.f) : x - y;
+  }
   __device__ __forceinline__ void join(const Stat& y, float c) {
     const float n = fmaxf(r, y.r), dx = apart(r, n, c), dy = apart(y.r, n, c);
     const float fx = ex2(dx), fy = ex2(dy);
@@ -191,7 +199,7 @@ __device__ __noinline__ Stat<true> slow_sums(const Row<T>& row, float c, int tid
     for (int i = 0; i < N; ++i) p.r = fmaxf(p.r, x[i]);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float u = max_nan((x[i] - p.r) * c, -1000.f), e = ex2(u);
+      const float u = max_nan(scaled_apart(x[i], p.r, c), -1000.f), e = ex2(u);
       p.s += e;
       p.a = fmaf(e, u, p.a);
     }
@@ -505,7 +513,10 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 3 : 4) token_scores_ker
   const float nan = __int_as_float(0x7FFFFFFF), ls = log2f(s);
   // log of the sum relative to the largest; log p of a logit
   const float log_s = ((slow ? 0.f : fmaf(-largest, c, ref)) + ls) * kLn2;
-  auto logp = [&](float x) { return fmaf(x - largest, a.scale, -log_s); };
+  auto logp = [&](float x) {
+    const float d = x - largest;
+    return d == -INFINITY && x > -INFINITY ? fmaf(0.5f * x - 0.5f * largest, 2.f * a.scale, -log_s) : fmaf(d, a.scale, -log_s);
+  };
   if (tid == 0) {
     if (bad) report_error(a.err, kErrRange);
     if (a.lse != nullptr) a.lse[j] = bad ? nan : empty ? -INFINITY : fmaf(largest, a.scale, log_s);

@@ -148,3 +148,22 @@ def test_activations_keep_their_tails(name, act, m):
         y = torch.zeros(part.numel(), n, dtype=torch.bfloat16, device="cuda")
         dllm.dllm_linear(dllm.linear_desc(8, n, act), x, w, y)
         _assert_act(y, part.double()[:, None], name)
+
+
+# ------------------------------------------------------------------ logits as far apart as their type holds
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,v", [(3, 37), (3, 5003), (2, 126464), (700, 300)])
+@pytest.mark.parametrize("scale", [2e-38, 1e-37, 1e-3, 0.25, 1.0])
+def test_token_scores_of_logits_whose_difference_is_no_number_of_32_bits(dtype, m, v, scale):
+    lowest = torch.finfo(dtype).min
+    x = lu.randn((m, v), v, 1e38, dtype).clamp(lowest, -lowest)
+    x[0, v // 2], x[0, 1] = -lowest, lowest
+    x[1, 2::3] = lowest
+    x[1, 0] = 2e38
+    tokens = torch.ones(m, dtype=torch.int32, device="cuda")
+    tokens[1] = 2
+    f = lambda *s: torch.full(s, 9.0, device="cuda")  # noqa: E731
+    lse, entropy, logp, ids, best, error = f(m), f(m), f(m), ints([[0] * 32] * m), f(m, 32), ints([0])
+    dllm.dllm_token_scores(x, tokens, logp, lse, entropy, ids, best, scale, error)
+    assert error.item() == 0
+    lu.assert_scores((lse, entropy, logp, ids, best), x, tokens, 32, scale)
