@@ -839,6 +839,7 @@ dllm_status dllm_head_norm_rope(const dllm_layer_desc* desc, int32_t rows, const
   if (rows < 0 || queries == nullptr || rope_max_pos < 1) return DLLM_ERR_INVALID_ARGUMENT;
   if (pairs != DLLM_ROPE_HALVES && pairs != DLLM_ROPE_NEIGHBOURS) return DLLM_ERR_INVALID_ARGUMENT;
   if ((rotary_dim != 64 && rotary_dim != 128) || rotary_dim > desc->head_dim) return DLLM_ERR_UNSUPPORTED;
+  if (rows > kMaxRows - 256) return DLLM_ERR_UNSUPPORTED;  // counted in 32 bits, up to the end of a CTA's
   if (rows == 0) return DLLM_OK;
   const int32_t d = desc->head_dim;
   if (!aligned(row_pos, 4) || !aligned(rope_table, 16)) return DLLM_ERR_INVALID_ARGUMENT;
@@ -882,7 +883,7 @@ dllm_status dllm_token_scores(int32_t rows, int32_t vocab, const void* logits, i
   if (rows < 0 || vocab < 1 || top_k < 0) return DLLM_ERR_INVALID_ARGUMENT;
   if (logits_type != DLLM_TYPE_BF16 && logits_type != DLLM_TYPE_FP32) return DLLM_ERR_INVALID_ARGUMENT;
   if (!(scale > 0.f) || !isfinite(scale)) return DLLM_ERR_INVALID_ARGUMENT;
-  if (top_k > kMaxTop || vocab > (1 << 30)) return DLLM_ERR_UNSUPPORTED;
+  if (top_k > kMaxTop || vocab > (1 << 30) || rows > kMaxRows - 256) return DLLM_ERR_UNSUPPORTED;
   if (rows == 0) return DLLM_OK;
   const int size = logits_type == DLLM_TYPE_BF16 ? 2 : 4;
   if (!aligned(logits, size) || row_stride < vocab) return DLLM_ERR_INVALID_ARGUMENT;
