@@ -829,6 +829,16 @@ HeadRows head_rows(const dllm_head_rows* h) {
   r.n_heads = h->n_heads;
   return r;
 }
+
+// Whether rows of `len` elements of `size` bytes, `stride` elements apart from p on, share a byte with q's.
+bool rows_hold(const void* p, int64_t rows, int64_t stride, int64_t len, int64_t size, const void* q, size_t bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(p), y = reinterpret_cast<uintptr_t>(q);
+  if (y < x) return x - y < bytes;
+  const int64_t first = static_cast<int64_t>((y - x) / size);  // elements behind p
+  if (first >= (rows - 1) * stride + len) return false;
+  const int64_t in_row = static_cast<int64_t>((y - x) % (stride * size));
+  return in_row < len * size || in_row + bytes > static_cast<uint64_t>(stride * size);
+}
 }  // namespace
 
 dllm_status dllm_head_norm_rope(const dllm_layer_desc* desc, int32_t rows, const int32_t* row_pos,
@@ -893,6 +903,20 @@ dllm_status dllm_token_scores(int32_t rows, int32_t vocab, const void* logits, i
                         static_cast<const void*>(entropy), static_cast<const void*>(error_flag)})
     if (p != nullptr && !aligned(p, 4)) return DLLM_ERR_INVALID_ARGUMENT;
   if (top_k > 0 && (!aligned(top_ids, 4) || !aligned(top_logp, 4))) return DLLM_ERR_INVALID_ARGUMENT;
+  // what is written lies apart from all else
+  const size_t n = static_cast<size_t>(rows) * 4;
+  const struct {
+    const void* p;
+    size_t bytes;
+  } parts[] = {{logp, n}, {lse, n}, {entropy, n}, {top_k > 0 ? top_ids : nullptr, n * top_k},
+               {top_k > 0 ? top_logp : nullptr, n * top_k}, {error_flag, 4}, {tokens, n}};
+  for (int i = 0; i < 6; ++i) {
+    if (parts[i].p == nullptr) continue;
+    if (rows_hold(logits, rows, row_stride, vocab, size, parts[i].p, parts[i].bytes)) return DLLM_ERR_INVALID_ARGUMENT;
+    for (int j = i + 1; j < 7; ++j)
+      if (parts[j].p != nullptr && overlap(parts[i].p, parts[i].bytes, parts[j].p, parts[j].bytes))
+        return DLLM_ERR_INVALID_ARGUMENT;
+  }
   ScoreArgs a = {};
   a.logits = logits;
   a.stride = row_stride;

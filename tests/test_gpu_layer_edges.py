@@ -167,3 +167,14 @@ def test_token_scores_of_logits_whose_difference_is_no_number_of_32_bits(dtype, 
     dllm.dllm_token_scores(x, tokens, logp, lse, entropy, ids, best, scale, error)
     assert error.item() == 0
     lu.assert_scores((lse, entropy, logp, ids, best), x, tokens, 32, scale)
+
+
+def test_token_scores_written_between_the_rows_of_the_logits():
+    buf = lu.randn((6, 1100), 1, 3.0)
+    x, lse = buf[:, :1000], buf.view(torch.float32)[2, 502:508]
+    entropy, ids, best = torch.zeros(6, device="cuda"), ints([[0] * 4] * 6), torch.zeros(6, 4, device="cuda")
+    rest = buf.clone()
+    dllm.dllm_token_scores(x, lse=lse, entropy=entropy, top_ids=ids, top_logp=best)
+    lu.assert_scores((lse, entropy, None, ids, best), x, ints([0] * 6), 4, 1.0)
+    rest.view(torch.float32)[2, 502:508] = lse
+    assert torch.equal(buf, rest)
