@@ -101,6 +101,27 @@ def test_rows_so_long_that_a_product_takes_most_of_a_second():
     assert error.item() == 0 and torch.equal(y, want.bfloat16()), (error.item(), y, want)
 
 
+# ------------------------------------------------------------------ the normed rows themselves
+@pytest.mark.parametrize("m,k,at_a_time", [
+    (512, 4096, 1), (512, 4096, 2), (256, 8200, 1),                       # one or two rows
+    (4000, 256, 8), (1500, 1000, 5),                                      # normed inside the product
+    (1500, 1024, 1500), (1200, 1032, 1200), (600, 4096, 600), (300, 4104, 300), (100, 8448, 100)])  # by the norm's kernel
+@pytest.mark.parametrize("size", [1.0, 1e-4, 3e4])
+def test_normed_rows_are_the_nearest_bf16(m, k, at_a_time, size):
+    """With the identity for a weight y is x^ itself.  One value in some 40000 lies within a 32-bit step of the middle of two
+    bf16 values, where a product in 32 bits alone rounds the wrong way."""
+    eps = 2.0 ** -17  # the same in 32 and 64 bits
+    x, gain = lu.randn((m, k), k, size), (1 + lu.randn((k,), 2, 0.3).float()).bfloat16()
+    eye = torch.eye(k, dtype=torch.bfloat16, device="cuda")
+    y = torch.zeros_like(x)
+    desc = dllm.linear_desc(k, k, rms_eps=eps)
+    ws = dllm.workspace(dllm.dllm_linear_workspace_size(desc, at_a_time, True))
+    for i in range(0, m, at_a_time):
+        dllm.dllm_linear(desc, x[i:i + at_a_time], eye, y[i:i + at_a_time], rms_gain=gain, ws=ws)
+    want = lu.nearest_bf16(lu.rms_norm(x, gain, eps))
+    assert torch.equal(y.double(), want), ((y.double() != want).sum().item(), y.numel())
+
+
 # ------------------------------------------------------------------ the activations' tails
 ACTS = [("silu", dllm.DLLM_ACT_SILU), ("gelu", dllm.DLLM_ACT_GELU), ("gelu_tanh", dllm.DLLM_ACT_GELU_TANH)]
 
@@ -148,6 +169,63 @@ def test_activations_keep_their_tails(name, act, m):
         y = torch.zeros(part.numel(), n, dtype=torch.bfloat16, device="cuda")
         dllm.dllm_linear(dllm.linear_desc(8, n, act), x, w, y)
         _assert_act(y, part.double()[:, None], name)
+
+
+# ------------------------------------------------------------------ the kernel in front
+@pytest.mark.parametrize("m", [1, 2, 64, 1500])
+def test_products_of_what_the_librarys_kernel_in_front_wrote(m):
+    """Rows, weight, bias and residual each by a call of this library directly in front (which lets its successor start
+    early), calls one behind the other without a wait; other values every turn."""
+    k, n, turns = 1024, 640, 24
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    table, pos = lu.rope_table(64, 128), torch.arange(m, device="cuda", dtype=torch.int32) % 64
+    srcs = [dict(x=lu.randn((m, k), s), w=lu.randn((n, k), s + 1), z=lu.randn((1, k), s + 2)) for s in (1, 11)]
+    wk, wn, wnn = lu.randn((k, k), 5, 1 / 32), lu.randn((n, k), 6, 1 / 32), lu.randn((n, n), 9, 1 / 25)
+    gain = (1 + lu.randn((k,), 7, 0.2).float()).bfloat16()
+    h, w, bias, r, turned = bf(m, k), bf(n, k), bf(1, n), bf(m, n), bf(m, n)
+    tokens, error = _tokens(m, n), ints([0])
+    square, out = dllm.linear_desc(k, k), dllm.linear_desc(k, n)
+    heads = dllm.layer_desc(n, n // 128, 128, 1e4)
+    ws = dllm.workspace(dllm.dllm_linear_workspace_size(out, m, True))
+
+    def turn(s, ys, logp):
+        dllm.dllm_linear(square, s["w"], wk, w, error=error)
+        dllm.dllm_linear(square, s["x"], wk, h, error=error)
+        dllm.dllm_linear(out, h, w, ys[0], error=error)                                  # rows in front, the weight before
+        dllm.dllm_linear(out, s["z"], wn, bias, error=error)
+        dllm.dllm_linear(out, h, wn, ys[1], bias=bias[0], error=error)                   # bias in front
+        dllm.dllm_linear(out, h, wn, r, rms_gain=gain, ws=ws, error=error)               # (the norm's kernel in front)
+        dllm.dllm_linear(out, s["x"], w, ys[2], residual=r, error=error)                 # residual in front
+        dllm.dllm_linear(out, s["x"], wn, ys[3], rms_gain=gain, ws=ws, error=error)      # the workspace once more
+        dllm.dllm_head_norm_rope(heads, ys[3].view(m, n // 128, 128), turned.view(m, n // 128, 128), None, None, pos, table,
+                                 error=error)
+        dllm.dllm_linear(dllm.linear_desc(n, n), turned, wnn, ys[4], residual=turned, error=error)
+        dllm.dllm_linear(square, s["w"], wk, w, error=error)
+        dllm.dllm_linear(out, s["x"], w, ys[5], error=error)                             # the weight in front
+        dllm.dllm_token_scores(ys[5], tokens, logp, error=error)
+
+    want = []
+    for s in srcs:
+        ys, logp = [bf(m, n) for _ in range(6)], torch.zeros(m, device="cuda")
+        for _ in range(2):
+            turn(s, ys, logp)
+            torch.cuda.synchronize()
+        want.append(ys + [logp])
+    got = [([bf(m, n) for _ in range(6)], torch.zeros(m, device="cuda")) for _ in range(turns)]
+    torch.cuda.synchronize()
+    for i, (ys, logp) in enumerate(got):
+        turn(srcs[i % 2], ys, logp)
+    torch.cuda.synchronize()
+    assert error.item() == 0
+    for i, (ys, logp) in enumerate(got):
+        for j, (a, b) in enumerate(zip(ys + [logp], want[i % 2])):
+            assert torch.equal(a, b), (i, j)
+    ok, off = lu.linear(srcs[(turns - 1) % 2]["x"], w)
+    assert ((got[-1][0][5].double() - ok).abs() <= off).all()
+
+
+def _tokens(m, v):
+    return torch.arange(m, device="cuda", dtype=torch.int32) % v
 
 
 # ------------------------------------------------------------------ logits as far apart as their type holds
