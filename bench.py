@@ -173,8 +173,8 @@ KERNEL_SOURCES = {
 TRAFFIC = {
     # (workload, kernel): (DRAM bytes per launch, sources hash); profiles/attn_stream_stack.md,
     # profiles/qkv_wide_stack.md (the DRAM-only capture listed there)
-    ("stack", "attention"): (969_189_632, "47432f11b3637cc5"),
-    ("stack", "qkv"): (131_329_792, "71aba221426de0ff"),
+    ("stack", "attention"): (969_732_608, "e8df2ede3b94a552"),
+    ("stack", "qkv"): (131_362_816, "66891fdd1335673a"),
 }
 
 
