@@ -16,9 +16,13 @@
 //    while the tensor cores work on the next, through staging tiles that make whole runs of
 //    the rows of y and of the residual.
 //
+// The tensor core's sums go over all of K (or of a CTA's part): one in 140 values of y of K = 12288
+// is the neighbour of the nearest bf16, one in 240 of K = 4096 gated, and the error against 64 bits is
+// that of an fp32 product (relative 1.66e-3, all of it y's rounding).
+//
 // Bound and measured (us, calls one behind the other, W from memory).  64 rows, 4096 x 4096:
-// 11.6 (floor 5.2): W comes at 6 TB/s in 5.6 of it, the rest is the first box's way (1.3), the
-// parts' (2), and from a kernel's end to the next one's start (1.2).  512 rows, K 4096, 2 x
+// 11.2 (floor 5.2; 9.0 with W in L2): W comes at 6 TB/s in 5.6 of it, the rest is the first box's way
+// (1.3), the parts' (2), and from a kernel's end to the next one's start (1.2).  512 rows, K 4096, 2 x
 // 12288 gated and normed: 66.5 (53.7), of which the norm is 3: tensor pipe 75% busy, held up by
 // what L2 delivers (14.5 TB/s for all SMs; 256 x 224 tiles need 60 KB for 0.24 us of MMAs).
 // 20480 rows, K 12288, 4096: 1056 to 1100 in a burst (1073), 1256 at the clock that the power

@@ -199,9 +199,10 @@ cudaError_t launch(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, linear_few_kernel<T, C, R, P, ACT, GATED>, a, team);
 }
 
-// (One row: 1024 threads an SM hold any K's x^ as two pieces each and W's as eight: 4096 x 6144 on two CTAs of 512 threads, a
-// piece each, 9.6 us, not 9.3; 12288 x 4096 with four pieces each, which spill, 24.  Two rows: half the threads, with twice
-// the registers.)
+// (One row: 1024 threads an SM hold any K's x^ as two pieces each and W's as eight, in 64 registers but for some 70 bytes a
+// thread that spill, 24 to 48 with one piece: 4096 x 6144 on two CTAs of 512 threads, a piece each, 9.6 us, not 9.3;
+// 12288 x 4096 with four pieces each, which spill more, 24 for 17.  Two rows: half the threads, with twice the registers and
+// no spills.)
 template <int ACT, bool GATED>
 cudaError_t launch_k(const LinearArgs& a, int num_sms, cudaStream_t stream) {
   if (a.rows == 2)

@@ -4,8 +4,8 @@
 // x is bf16, so every x*x is exact in fp32 and a row's sum of squares is
 // carried as an unevaluated (hi, lo) pair of floats (TwoSum); the scale
 // 1 / sqrt(ss / D + eps) is formed as a float pair as well (relative error
-// ~2^-40), and x^ is the correctly rounded bf16 value of x * scale * g (the
-// product evaluated with its exact error).  fp32 only: fp64 is slow on this
+// ~2^-40), and x^ is x * scale * g rounded to bf16, correctly but for one value
+// in some four million (normalise8).  fp32 only: fp64 is slow on this
 // part.
 #pragma once
 
@@ -69,12 +69,15 @@ __device__ __forceinline__ void rsqrt_pair(float ss_hi, float ss_lo, int D, floa
 }
 
 // x^ = x * (s_hi + s_lo) * g for 8 consecutive elements (bf16 x, g),
-// correctly rounded to bf16 without branches.  t = x * g is exact in fp32
+// rounded to bf16 without branches.  t = x * g is exact in fp32
 // (two 8-bit significands); t * s is formed as p + e with p = fl(t * s_hi)
 // and e = (t * s_hi - p) (exact, FMA) + t * s_lo.  p alone decides the bf16
 // rounding unless p sits exactly on a bf16 midpoint (its 16 discarded bits
-// are 0x8000), in which case the sign of e does (|e| is below half an fp32
-// step of p).
+// are 0x8000), in which case the sign of e does.  That would be right for an |e|
+// of half an fp32 step of p at most; with t * s_lo it can be one and a half, and
+// a p beside a midpoint that e leads across it is rounded to the neighbour: one
+// value in 4.4 million (68 of 3e8 random ones).  linear_math.cuh's normed8 takes
+// another sum and has none; here the results stay as they have been.
 __device__ __forceinline__ uint4 normalise8(const uint4& u, const uint4& gu, float s_hi, float s_lo) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w}, gw[4] = {gu.x, gu.y, gu.z, gu.w};
   uint32_t o[4];

@@ -2,7 +2,7 @@
 // (sm_103a), one kernel.
 //
 // Computes, for a set of token rows t (bf16 x_t), the normalised row
-// x^_t = x_t / sqrt(mean(x_t^2) + eps) * g correctly rounded to bf16,
+// x^_t = x_t / sqrt(mean(x_t^2) + eps) * g rounded to bf16 (norm.cuh),
 // y_t = W_qkv x^_t with fp32 accumulation, rotates the q and k parts (RoPE,
 // rotate-half pairs (i, i + d/2) at the token's absolute position) and
 // writes q, k, v once, as bf16, to their destinations: k, v into the paged
@@ -48,7 +48,7 @@
 //    for all CTAs: the accumulator warps claim rows through a counter in the
 //    workspace (one atomic per claim), and a claiming warp reads the row,
 //    forms its exact sum of squares and scale (float pairs), writes the
-//    correctly rounded bf16 x^ row to the workspace and publishes it.  The
+//    bf16 x^ row (norm.cuh) to the workspace and publishes it.  The
 //    TMA producer waits until every row is published before it loads x^
 //    tiles.  It waits only after all rows have been claimed (its own CTA's
 //    warps claim until none is left) and a claimed row belongs to a running
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         named_barrier(1, kAccThreads);
         const float2 y = scale_sh[par];
 #pragma unroll 1
-        for (int v = at; v < nvec; v += kAccThreads) {  // x^, correctly rounded
+        for (int v = at; v < nvec; v += kAccThreads) {  // x^
           const uint4 xv = staged ? rowbuf[v] : (warm ? make_uint4(0, 0, 0, 0) : __ldg(xr + v));
           const uint4 gvv = staged ? gainbuf[v] : __ldg(gg + v);
           const uint4 o = normalise8(xv, gvv, y.x, y.y);

@@ -2,7 +2,7 @@
 // (sm_103a) for many token rows: the tensor-bound shapes (an inner step of a
 // large batch, every block boundary).
 //
-// Same computation as qkv_gemm.cu (x^ = RMSNorm(x) correctly rounded to bf16,
+// Same computation as qkv_gemm.cu (x^ = RMSNorm(x) rounded to bf16,
 // y = W_qkv x^ with fp32 accumulation, RoPE of the q and k parts at absolute
 // positions, one bf16 write of q, k, v to their destinations; the Flash-Cache
 // fusion of the Flash-dLLM write-up, "Flash-Cache: Fusing Projection, RoPE,

@@ -541,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, TEAM == 32 ? 3 : 4) token_scores_ker
 
 template <typename T, int TEAM, bool CLUSTER>
 cudaError_t launch_scores(const ScoreArgs& a, int cluster, cudaStream_t stream) {
+  // (64 registers, for four CTAs an SM; of a cluster's, two at most are there, which could have twice as many)
   const auto kernel = token_scores_kernel<T, TEAM, CLUSTER>;
   constexpr int kTeams = kThreads / TEAM;
   cudaLaunchConfig_t cfg = {};

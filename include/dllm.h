@@ -192,7 +192,7 @@ dllm_status dllm_qkv_weight_pack(const dllm_layer_desc* desc, const void* w_qkv,
 
 /* Block boundary (LaCache Algorithm 1 with GenStep = True; Fast-dLLM
  * compute_block_dual_cache).  For every row of every sequence:
- *   x^ = RMSNorm(x) (correctly rounded to bf16), [q k v] = x^ W_qkv^T (fp32
+ *   x^ = RMSNorm(x) (rounded to bf16), [q k v] = x^ W_qkv^T (fp32
  *   accumulation), RoPE(q, k) at position p, and k, v (and q for rows of U)
  *   written as bf16 into the pools.  Pool positions p >= N_b of each
  *   sequence's last page are set to zero.
@@ -246,7 +246,7 @@ dllm_status dllm_cache_advance(const dllm_layer_desc* desc, const dllm_batch* ba
 
 /* Inner step, part 1 (LaCache §3.3.2 Eq. (1); Flash-dLLM Flash-Cache): for
  * the B_b rows of each current block only, in one kernel: x^ = RMSNorm(x_block)
- * correctly rounded to bf16, [q k v] = x^ W_qkv^T with fp32 accumulation,
+ * rounded to bf16, [q k v] = x^ W_qkv^T with fp32 accumulation,
  * RoPE(q, k) at absolute position p = s_b + i, then one write: k, v as bf16
  * into k_pool / v_pool at (block_table[b][p/64], h, p%64) and q as bf16 into
  * q_block [M][H][d].
@@ -333,7 +333,7 @@ dllm_status dllm_step_attention(const dllm_layer_desc* desc, const dllm_batch* b
  * stage: the output is cut to the tokens of the current generation block;
  * Fast-dLLM "Block-wise Generation").  For the B_b rows of each current block
  * only (block row i of sequence b is row cu_seq[b] + s_b + i of h_full):
- *   x^ = RMSNorm(h) with gain final_gain (correctly rounded to bf16),
+ *   x^ = RMSNorm(h) with gain final_gain (rounded to bf16),
  *   logits = x^ W_lm^T (fp32 accumulation, W_lm bf16 [vocab][d_model]),
  *   and the softmax over the vocabulary, summarised per row as
  *   lse = log sum_v exp(logit_v), argmax = the lowest v with the largest
@@ -537,12 +537,15 @@ typedef struct dllm_linear_layer {
 } dllm_linear_layer;
 
 /* y = act(t) + r, or (gated) act(t_gate) * t_up + r, with t = x^ W^T + b and
- *   x^ = x, or with a gain RMSNorm(x) (correctly rounded to bf16).
+ *   x^ = x, or with a gain RMSNorm(x) (correctly rounded to bf16; a row's sum of
+ *   squares has to lie within fp32's range, else y is NaN).
  * Products are summed in fp32, by the tensor core over all of K (or over equal
  * parts of K, whose sums are added in their order) or, where rows are very few,
  * by multiply-adds in a fixed order; bias, activation, gate and residual are
  * fp32, and y is rounded to bf16 once.  The same call gives the same bits; how
- * K is cut depends on the sizes and the number of SMs alone.
+ * K is cut depends on the sizes and the number of SMs alone.  The activations are
+ * accurate relative to their value for negative t too (2^-21 (4 + z) of it, where it
+ * falls as e^-z), down to bf16's smallest.
  *   x:        device bf16 [rows][in_features], rows x_stride elements apart;
  *             16-byte aligned, the stride a multiple of 8 and >= in_features.
  *   rms_gain: device bf16 [in_features], 16-byte aligned, nullable (no norm).
@@ -589,7 +592,8 @@ typedef struct dllm_head_rows {
  *   the pair (u_a, u_b) number i of the first rotary_dim elements becomes
  *   (u_a cos - u_b sin, u_a sin + u_b cos), cos and sin those of the row's
  *   position and i in rope_table; the elements behind rotary_dim stay u.
- * All of it in fp32, rounded to bf16 once.  Row j has position row_pos[j] (as
+ * All of it in fp32 (a head's sum of squares has to lie within its range), rounded
+ * to bf16 once.  Row j has position row_pos[j] (as
  * dllm_batch_plan writes it); rows with -1 are left as they are.  A position
  * below -1 or not below rope_max_pos sets DLLM_DEVERR_BAD_SHAPE, and its row
  * is left as it is.
@@ -626,8 +630,9 @@ dllm_status dllm_head_norm_rope(const dllm_layer_desc* desc, int32_t rows, const
  *   tokens: device int32 [rows]; logp: device fp32 [rows]; both nullable together.
  *   lse, entropy: device fp32 [rows], each nullable.
  *   top_k: 0 to 32; top_ids: device int32 [rows][top_k], top_logp: device fp32
- *   [rows][top_k] (not read or written for top_k 0).  The outputs overlap
- *   neither each other nor anything that the call reads.
+ *   [rows][top_k] (not read or written for top_k 0).  The outputs and error_flag
+ *   overlap neither each other nor anything that the call reads (columns between
+ *   the rows of the logits are fine).
  * Sums and statistics are fp32, relative to the row's largest logit; the same
  * call gives the same bits. */
 dllm_status dllm_token_scores(int32_t rows, int32_t vocab, const void* logits, int32_t logits_type, int64_t row_stride,
